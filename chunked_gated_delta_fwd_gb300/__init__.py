@@ -12,7 +12,10 @@ Entry points (same names as the C calls, without the ``kda_`` prefix):
 * :func:`gate` -- ``g = g_min * Sigmoid(exp(A_h) z)`` (optionally the in-chunk
   running sum),
 * :func:`chunk_fwd` -- prefill over whole (packed, variable-length) sequences,
-* :func:`recurrent_step` -- one decode token per sequence, state in place.
+* :func:`recurrent_step` -- one decode token per sequence, state in place,
+* :func:`qk_norm_rope` -- per-head RMSNorm of q and k with the rotation by position,
+* :func:`linear_chunk_fwd`, :func:`linear_recurrent_step`,
+  :func:`linear_recurrent_multi_step` -- linear attention with a decay for each head.
 """
 
 from __future__ import annotations
@@ -29,7 +32,9 @@ __all__ = ["KdaError", "gate", "chunk_fwd", "chunk_fwd_gated", "chunk_fwd_worksp
            "library_path", "lib", "get_device_error", "profile_enable", "profile_collect", "G_MIN", "F32", "BF16", "FP32_CORES", "SEQUENTIAL",
            "segment_chunks", "recurrent_multi_step", "chunk_fwd_checkpointed",
            "chunk_fwd_fused", "gate_softplus", "UNBOUNDED_GATE",
-           "output_gate", "SCALAR_GATE", "CHECK_INPUTS", "PRECISE", "selftest_wait_timeout"]
+           "output_gate", "SCALAR_GATE", "CHECK_INPUTS", "PRECISE", "selftest_wait_timeout",
+           "qk_norm_rope", "linear_chunk_fwd", "linear_chunk_fwd_workspace_size",
+           "linear_recurrent_step", "linear_recurrent_multi_step"]
 
 G_MIN = -5.0
 F32, BF16 = 0, 1
@@ -38,6 +43,7 @@ SEQUENTIAL = 2  # flag of chunk_fwd: never split a sequence's chain into segment
 UNBOUNDED_GATE = 4  # flag of chunk_fwd: any g <= 0 (range-robust fp32-core evaluation)
 SCALAR_GATE = 8  # flag of chunk_fwd: g is [..., H], one log-decay per token and head
 CHECK_INPUTS = 16  # flag of chunk_fwd: check g and beta against their ranges on the device
+_HEAD_DECAY = 4  # flag of the linear-attention calls, set from g's shape
 PRECISE = 32  # flag of chunk_fwd (bf16 tensor cores): the state update at tf32 precision
 
 _STATUS = {
@@ -84,6 +90,16 @@ def _load() -> ctypes.CDLL:
     L.kda_recurrent_step.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp]
     L.kda_recurrent_multi_step.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32,
                                            i32, i32, vp]
+    L.kda_qk_norm_rope.argtypes = [vp, vp, i32, vp, vp, f32, vp, i32, vp, vp, i32, i32, vp, vp,
+                                   i64, i32, i32, i32, i64, i64, i64, i64, vp]
+    L.kda_linear_chunk_fwd_workspace_size.argtypes = [i64, i32, i32, i32, u32]
+    L.kda_linear_chunk_fwd_workspace_size.restype = sz
+    L.kda_linear_chunk_fwd.argtypes = [vp, vp, vp, i32, vp, f32, vp, vp, i32, i32, i64, i32, i32,
+                                       i32, i32, vp, vp, vp, sz, vp, u32]
+    L.kda_linear_recurrent_step.argtypes = [vp, vp, vp, i32, vp, f32, vp, vp, i32, i32, i32, i32,
+                                            i32, vp, u32]
+    L.kda_linear_recurrent_multi_step.argtypes = [vp, vp, vp, i32, vp, f32, vp, vp, vp, i32, i32,
+                                                  i32, i32, i32, i32, vp, u32]
     L.kda_selftest_wait_timeout.argtypes = [u32, ctypes.POINTER(i32), vp]
     L.kda_selftest_wait_timeout.restype = ctypes.c_int
     L.kda_last_error_string.restype = ctypes.c_char_p
@@ -395,6 +411,212 @@ def recurrent_multi_step(q, k, v, g, beta, S, n_advance=None, *, out=None,
         _check(lib.kda_recurrent_multi_step(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(g),
                                             _ptr(beta), _ptr(S), _ptr(o), _ptr(n_advance), N, T,
                                             H, dk, dv, _stream(dev)))
+    return o
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the tokens of a [..., H, 128] tensor whose heads are contiguous
+    and whose leading dimensions step as one (a slice of a packed projection has more
+    elements a token than its own)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be [..., H, 128]")
+    d, H = t.shape[-1], t.shape[-2]
+    step = expect = None
+    for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != expect:
+            raise ValueError(f"{name}: the tokens must be one stride apart")
+        expect = stride * size
+    if (d > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return H * d if step is None else step
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6,
+                 freq_axis=None, interleaved: bool = False, q_out=None, k_out=None):
+    """Per-head RMSNorm of q and k and the rotation by position, in one pass.
+
+    q [..., Hq, 128], k [..., Hk, 128] (bf16/fp32, the same leading dimensions); both may be
+    slices of a packed projection (heads contiguous, tokens one stride apart).  ``eps`` None
+    turns the norm off; ``q_weight``/``k_weight`` fp32 [128] or None.  ``positions`` int32
+    [...] (the leading dimensions of q), or [n_axes, ...] with ``freq_axis`` int32 [n_freq],
+    the axis of every frequency.  ``inv_freq`` fp32 [n_freq], n_freq a multiple of 8 up to 64:
+    the first 2 n_freq channels turn, as pairs (i, i + n_freq) or, ``interleaved``, (2i, 2i+1).
+    Returns ``(q_out, k_out)``; ``q_out=q, k_out=k`` works in place.
+    """
+    sq, sk = _token_stride(q, "q"), _token_stride(k, "k")
+    dev, lead = q.device, tuple(q.shape[:-2])
+    if k.device != dev or k.dtype != q.dtype:
+        raise ValueError("q and k must have one dtype and device")
+    if tuple(k.shape[:-2]) != lead or k.shape[-1] != q.shape[-1]:
+        raise ValueError(f"k must be {lead} + (Hk, {q.shape[-1]}), got {tuple(k.shape)}")
+    dt = _dtype_code(q)
+    _need(positions, "positions", torch.int32, dev)
+    _need(inv_freq, "inv_freq", torch.float32, dev)
+    n_axes = 1
+    if tuple(positions.shape) != lead:
+        if positions.dim() < 1 or tuple(positions.shape[1:]) != lead:
+            raise ValueError(f"positions must be {lead} or (n_axes,) + {lead}, got "
+                             f"{tuple(positions.shape)}")
+        n_axes = positions.shape[0]
+    if freq_axis is not None:
+        _need(freq_axis, "freq_axis", torch.int32, dev)
+        if freq_axis.numel() != inv_freq.numel():
+            raise ValueError("freq_axis must have one entry a frequency")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need(w, name, torch.float32, dev)
+            if w.numel() != q.shape[-1]:
+                raise ValueError(f"{name} must have {q.shape[-1]} entries")
+    outs = []
+    for name, x, y in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        elif y.shape != x.shape or y.dtype != x.dtype or y.device != dev:
+            raise ValueError(f"{name} must have the shape, dtype and device of its input")
+        outs.append(y)
+    so = [_token_stride(y, name) for y, name in zip(outs, ("q_out", "k_out"))]
+    H, Hk, d = q.shape[-2], k.shape[-2], q.shape[-1]
+    nt = 1
+    for x in lead:
+        nt *= x
+    with torch.cuda.device(dev):
+        _check(lib.kda_qk_norm_rope(
+            _ptr(q), _ptr(k), dt, _ptr(q_weight), _ptr(k_weight),
+            -1.0 if eps is None else float(eps), _ptr(positions), n_axes, _ptr(freq_axis),
+            _ptr(inv_freq), inv_freq.numel(), int(interleaved), _ptr(outs[0]), _ptr(outs[1]), nt,
+            H, Hk, d, sq, sk, so[0], so[1], _stream(dev)))
+    return outs[0], outs[1]
+
+
+def _linear_inputs(q, k, v, g, lead):
+    """Checks what the linear-attention calls share: q, k ``lead`` + [Hk, dk], v ``lead``
+    + [H, dv], g ``lead`` + [H] or [H].  Returns (dtype code, H, Hk, dk, dv, flag of g)."""
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(t, name, q.dtype, dev)
+    _need(g, "g", torch.float32, dev)
+    dt = _dtype_code(q)
+    Hk, dk, H, dv = q.shape[-2], q.shape[-1], v.shape[-2], v.shape[-1]
+    if k.shape != q.shape:
+        raise ValueError(f"k must have the shape of q {tuple(q.shape)}, got {tuple(k.shape)}")
+    if tuple(v.shape[:-2]) != lead:
+        raise ValueError(f"v must be {lead} + (H, dv), got {tuple(v.shape)}")
+    if tuple(g.shape) == lead + (H,):
+        return dt, H, Hk, dk, dv, 0
+    if tuple(g.shape) == (H,):
+        return dt, H, Hk, dk, dv, _HEAD_DECAY
+    raise ValueError(f"g must be {lead + (H,)} or ({H},), got {tuple(g.shape)}")
+
+
+def _like(t, name, shape, dtype, device):
+    """``t`` checked against what a result needs, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def linear_chunk_fwd_workspace_size(n_tokens: int, n_seqs: int, H: int, dtype=torch.bfloat16,
+                                    flags: int = 0) -> int:
+    code = BF16 if dtype == torch.bfloat16 else F32
+    return int(lib.kda_linear_chunk_fwd_workspace_size(int(n_tokens), int(n_seqs), int(H), code,
+                                                       int(flags)))
+
+
+def linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale: float = 1.0,
+                     output_final_state=True, workspace=None, flags: int = 0, out=None,
+                     final_state_out=None):
+    """Prompt pass of linear attention with a decay for each head,
+    ``S_t = e^{g_t} S_{t-1} + k_t v_t^T``, ``o_t = scale S_t^T q_t``.
+
+    q, k [B, T, Hk, 128] or packed [NT, Hk, 128] (with ``cu_seqlens``), v [..., H, 128], H a
+    multiple of Hk (value head h uses key head h // (H // Hk)); bf16 or fp32.  g fp32
+    log-decays <= 0, [..., H] (one a token and head) or [H].  h0, cu_seqlens, outputs and
+    ``workspace`` as :func:`chunk_fwd`; ``flags``: ``FP32_CORES``.  Returns ``(o, hT)``; hT is
+    the S of :func:`linear_recurrent_step`.
+    """
+    lead = tuple(q.shape[:-2])
+    dt, H, Hk, dk, dv, fl = _linear_inputs(q, k, v, g, lead)
+    dev = q.device
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if len(lead) not in (1, 2) or (len(lead) == 2 and lead[0] != 1):
+            raise ValueError("with cu_seqlens, q must be packed as [1, NT, Hk, D] or [NT, Hk, D]")
+        N, B, T = cu_seqlens.numel() - 1, 1, lead[-1]
+        NT = T
+    else:
+        if len(lead) != 2:
+            raise ValueError("q must be [B, T, Hk, D] without cu_seqlens")
+        B, T = lead
+        N, NT = B, B * T
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, dev)
+        if tuple(h0.shape) != (N, H, dv, dk):
+            raise ValueError(f"h0 must be [{N}, {H}, {dv}, {dk}], got {tuple(h0.shape)}")
+    o = _like(out, "out", v.shape, v.dtype, dev)
+    hT = None
+    if output_final_state:
+        hT = _like(final_state_out, "final_state_out", (N, H, dv, dk), torch.float32, dev)
+    fl |= int(flags)
+    if workspace is None:
+        need = lib.kda_linear_chunk_fwd_workspace_size(NT, N, H, dt, fl)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    with torch.cuda.device(dev):
+        _check(lib.kda_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), float(scale),
+                                        _ptr(h0), _ptr(cu_seqlens), N, B, T, H, Hk, dk, dv,
+                                        _ptr(o), _ptr(hT), _ptr(workspace), workspace.numel(),
+                                        _stream(dev), fl))
+    return o, hT
+
+
+def linear_recurrent_step(q, k, v, g, S, *, scale: float = 1.0, out=None):
+    """One token of :func:`linear_chunk_fwd`'s recurrence: q, k [N, Hk, 128], v [N, H, 128]
+    (bf16/fp32), g fp32 [N, H] or [H], S [N, H, 128, 128] fp32 updated in place.
+    Returns o [N, H, 128]."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [N, Hk, D], got {tuple(q.shape)}")
+    N, dev = q.shape[0], q.device
+    dt, H, Hk, dk, dv, fl = _linear_inputs(q, k, v, g, (N,))
+    S = _like(S, "S", (N, H, dv, dk), torch.float32, dev)
+    o = _like(out, "out", v.shape, v.dtype, dev)
+    with torch.cuda.device(dev):
+        _check(lib.kda_linear_recurrent_step(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), float(scale),
+                                             _ptr(S), _ptr(o), N, H, Hk, dk, dv, _stream(dev), fl))
+    return o
+
+
+def linear_recurrent_multi_step(q, k, v, g, S, n_advance=None, *, scale: float = 1.0, out=None,
+                                return_outputs=True):
+    """T <= 16 tokens per sequence: q, k [N, T, Hk, 128], v [N, T, H, 128] (bf16/fp32), g fp32
+    [N, T, H] or [H], S [N, H, 128, 128] fp32 advanced in place by n_advance[n] tokens
+    (int32 [N] on the device; None = all T).  Returns o [N, T, H, 128] (the outputs of all T
+    tokens), or None when return_outputs is False."""
+    if q.dim() != 4:
+        raise ValueError(f"q must be [N, T, Hk, D], got {tuple(q.shape)}")
+    N, T, dev = q.shape[0], q.shape[1], q.device
+    dt, H, Hk, dk, dv, fl = _linear_inputs(q, k, v, g, (N, T))
+    S = _like(S, "S", (N, H, dv, dk), torch.float32, dev)
+    if n_advance is not None:
+        _need(n_advance, "n_advance", torch.int32, dev)
+        if n_advance.numel() != N:
+            raise ValueError(f"n_advance must have {N} entries")
+    o = _like(out, "out", v.shape, v.dtype, dev) if return_outputs else None
+    with torch.cuda.device(dev):
+        _check(lib.kda_linear_recurrent_multi_step(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(g),
+                                                   float(scale), _ptr(S), _ptr(o),
+                                                   _ptr(n_advance), N, T, H, Hk, dk, dv,
+                                                   _stream(dev), fl))
     return o
 
 

@@ -334,6 +334,9 @@ kda_status_t kda_get_device_error(kda_stream_t stream) {
     return fail(KDA_ERR_INVALID_ARG,
                 "input check: a log-decay g outside [-5, 0] (outside (-inf, 0] with "
                 "KDA_CHUNK_UNBOUNDED_GATE) or a beta outside [0, 1], or a NaN");
+  if (host == kda::kDevErrBadAxis)
+    return fail(KDA_ERR_INVALID_ARG,
+                "kda_qk_norm_rope: an entry of freq_axis outside [0, n_axes) (axis 0 was used)");
   return fail(KDA_ERR_CUDA, "device error code %d", host);
 }
 
@@ -686,6 +689,178 @@ kda_status_t kda_recurrent_multi_step(const void* q, const void* k, const void* 
                                            N, T, H, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kda_recurrent_multi_step launch");
   return KDA_OK;
+}
+
+kda_status_t kda_qk_norm_rope(const void* q, const void* k, int dtype, const float* q_weight,
+                              const float* k_weight, float eps, const int32_t* positions,
+                              int n_axes, const int32_t* freq_axis, const float* inv_freq,
+                              int n_freq, int interleaved, void* q_out, void* k_out,
+                              int64_t n_tokens, int Hq, int Hk, int d, int64_t q_stride,
+                              int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                              kda_stream_t stream) {
+  const char* fn = "kda_qk_norm_rope";
+  if (dtype != KDA_F32 && dtype != KDA_BF16)
+    return fail(KDA_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d", fn, dtype);
+  if (d != kda::kD) return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: d=%d (need 128)", fn, d);
+  if (Hq < 1 || Hk < 1 || Hq > 65535 || Hk > 65535)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: Hq=%d Hk=%d", fn, Hq, Hk);
+  if (n_freq < 8 || n_freq > kda::kD / 2 || n_freq % 8 != 0)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: n_freq=%d (a multiple of 8 up to 64)", fn, n_freq);
+  if (n_axes < 1) return fail(KDA_ERR_INVALID_ARG, "%s: n_axes=%d", fn, n_axes);
+  if (n_axes > 1 && !freq_axis)
+    return fail(KDA_ERR_INVALID_ARG, "%s: several axes need freq_axis", fn);
+  if (n_tokens < 0 || n_tokens > INT32_MAX)
+    return fail(KDA_ERR_INVALID_ARG, "%s: n_tokens=%lld", fn, (long long)n_tokens);
+  if (!(eps < 0.f || std::isfinite(eps)))
+    return fail(KDA_ERR_INVALID_ARG, "%s: eps=%g is not finite", fn, (double)eps);
+  if (eps < 0.f && (q_weight || k_weight))
+    return fail(KDA_ERR_INVALID_ARG, "%s: a norm weight without the norm (eps < 0)", fn);
+  if (n_tokens == 0) return KDA_OK;
+  if (!q || !k || !positions || !inv_freq || !q_out || !k_out)
+    return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
+  const void* ptrs[] = {q, k, q_weight, k_weight, q_out, k_out};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p))
+      return fail(KDA_ERR_MISALIGNED, "%s: pointers must be 16-byte aligned", fn);
+  const int64_t strides[] = {q_stride, k_stride, q_out_stride, k_out_stride};
+  const int per16 = dtype == KDA_BF16 ? 8 : 4;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = (int64_t)(i & 1 ? Hk : Hq) * d;
+    if (strides[i] < row)
+      return fail(KDA_ERR_INVALID_ARG, "%s: a token stride of %lld below its %lld channels", fn,
+                  (long long)strides[i], (long long)row);
+    if (strides[i] % per16 != 0)
+      return fail(KDA_ERR_MISALIGNED, "%s: token strides must be multiples of 16 bytes", fn);
+  }
+  kda_status_t st = check_device();
+  if (st != KDA_OK) return st;
+  cudaError_t e = kda::launch_norm_rope(
+      q, k, dtype == KDA_BF16, q_weight, k_weight, eps, positions, n_axes, freq_axis, inv_freq,
+      n_freq, interleaved, q_out, k_out, n_tokens, Hq, Hk, q_stride, k_stride, q_out_stride,
+      k_out_stride, kda::device_error_flag(), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kda_qk_norm_rope launch");
+  return KDA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Head counts and sizes that the linear-attention entries share.
+kda_status_t linear_heads(const char* fn, int dtype, float scale, int H, int Hk, int dk, int dv) {
+  if (dtype != KDA_F32 && dtype != KDA_BF16)
+    return fail(KDA_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d", fn, dtype);
+  if (dk != kda::kD || dv != kda::kD)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: dk=%d dv=%d (need 128)", fn, dk, dv);
+  if (H < 1 || H > 65535 || Hk < 1 || H % Hk != 0)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: H=%d Hk=%d (H a multiple of Hk)", fn, H, Hk);
+  if (!std::isfinite(scale)) return fail(KDA_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+  return KDA_OK;
+}
+
+kda_status_t linear_step_impl(const char* fn, const void* q, const void* k, const void* v,
+                              int dtype, const float* g, float scale, float* S, void* o,
+                              const int32_t* n_advance, int N, int T, int H, int Hk, int dk,
+                              int dv, kda_stream_t stream, unsigned flags, bool multi) {
+  kda_status_t st = linear_heads(fn, dtype, scale, H, Hk, dk, dv);
+  if (st != KDA_OK) return st;
+  if (N < 0 || T < 1 || T > KDA_MULTI_STEP_MAX_T)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: N=%d T=%d", fn, N, T);
+  if ((int64_t)N * H > INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "%s: N*H too large", fn);
+  if (flags & ~(unsigned)KDA_LINEAR_HEAD_DECAY)
+    return fail(KDA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
+  if (N == 0) return KDA_OK;
+  if (!q || !k || !v || !g || !S || (!o && !multi))
+    return fail(KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+  const void* ptrs[] = {q, k, v, S, o};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p))
+      return fail(KDA_ERR_MISALIGNED, "%s: pointers must be 16-byte aligned", fn);
+  st = check_device();
+  if (st != KDA_OK) return st;
+  cudaError_t e = kda::launch_linear_step(q, k, v, dtype == KDA_BF16, g,
+                                          (flags & KDA_LINEAR_HEAD_DECAY) ? 1 : 0, scale, S, o,
+                                          n_advance, N, T, H, Hk, multi,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_linear_chunk_fwd_workspace_size(int64_t n_tokens, int n_seqs, int H, int dtype,
+                                           unsigned flags) {
+  (void)flags;
+  if (n_tokens < 0 || n_seqs < 1 || H < 1 || (dtype != KDA_F32 && dtype != KDA_BF16)) return 0;
+  return kda::plan_bytes(n_tokens, n_seqs) + kda::linear_simt_workspace_bytes(n_tokens, n_seqs, H);
+}
+
+kda_status_t kda_linear_chunk_fwd(const void* q, const void* k, const void* v, int dtype,
+                                  const float* g, float scale, const float* h0,
+                                  const int32_t* cu_seqlens, int n_seqs, int B, int64_t T, int H,
+                                  int Hk, int dk, int dv, void* o, float* hT, void* workspace,
+                                  size_t ws_bytes, kda_stream_t stream, unsigned flags) {
+  const char* fn = "kda_linear_chunk_fwd";
+  kda_status_t st = linear_heads(fn, dtype, scale, H, Hk, dk, dv);
+  if (st != KDA_OK) return st;
+  int N;
+  int64_t NT, T_per_seq = 0;
+  if (cu_seqlens) {
+    if (B != 1) return fail(KDA_ERR_INVALID_ARG, "%s: B must be 1 with cu_seqlens", fn);
+    if (n_seqs < 1) return fail(KDA_ERR_INVALID_ARG, "%s: n_seqs=%d", fn, n_seqs);
+    N = n_seqs;
+    NT = T;
+  } else {
+    if (B < 1) return fail(KDA_ERR_INVALID_ARG, "%s: B=%d", fn, B);
+    N = B;
+    NT = (int64_t)B * T;
+    T_per_seq = T;
+  }
+  if (T < 0 || NT > INT32_MAX - 2 * kda::kChunk || (int64_t)N * H > INT32_MAX)
+    return fail(KDA_ERR_INVALID_ARG, "%s: token or state count out of range", fn);
+  if (flags & ~(unsigned)(KDA_LINEAR_HEAD_DECAY | KDA_LINEAR_FP32_CORES))
+    return fail(KDA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
+  if ((NT > 0 && (!q || !k || !v || !g || !o)) || !workspace)
+    return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
+  const void* ptrs[] = {q, k, v, h0, o, hT};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p))
+      return fail(KDA_ERR_MISALIGNED, "%s: pointers must be 16-byte aligned", fn);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(KDA_ERR_MISALIGNED, "%s: workspace must be 256-byte aligned", fn);
+  const size_t need = kda_linear_chunk_fwd_workspace_size(NT, N, H, dtype, flags);
+  if (ws_bytes < need)
+    return fail(KDA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+  st = check_device();
+  if (st != KDA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* err = kda::device_error_flag();
+  const int g_head = (flags & KDA_LINEAR_HEAD_DECAY) ? 1 : 0;
+  cudaError_t e = kda::launch_plan(cu_seqlens, N, T_per_seq, NT, workspace, err, s);
+  if (e != cudaSuccess) return cuda_fail(e, "chunk plan launch");
+  e = kda::launch_linear_simt(q, k, v, dtype == KDA_BF16, g, g_head, scale, h0, o, hT, NT, N, H,
+                              Hk, workspace, s);
+  if (e != cudaSuccess) return cuda_fail(e, "linear chunk launch");
+  return KDA_OK;
+}
+
+kda_status_t kda_linear_recurrent_step(const void* q, const void* k, const void* v, int dtype,
+                                       const float* g, float scale, float* S, void* o, int N,
+                                       int H, int Hk, int dk, int dv, kda_stream_t stream,
+                                       unsigned flags) {
+  return linear_step_impl("kda_linear_recurrent_step", q, k, v, dtype, g, scale, S, o, nullptr, N,
+                          1, H, Hk, dk, dv, stream, flags, false);
+}
+
+kda_status_t kda_linear_recurrent_multi_step(const void* q, const void* k, const void* v,
+                                             int dtype, const float* g, float scale, float* S,
+                                             void* o, const int32_t* n_advance, int N, int T,
+                                             int H, int Hk, int dk, int dv, kda_stream_t stream,
+                                             unsigned flags) {
+  return linear_step_impl("kda_linear_recurrent_multi_step", q, k, v, dtype, g, scale, S, o,
+                          n_advance, N, T, H, Hk, dk, dv, stream, flags, true);
 }
 
 }  // extern "C"

@@ -20,6 +20,7 @@ constexpr int kDevErrTimeout = 7;
 constexpr int kDevErrBadSeqlens = 1;
 constexpr int kDevErrCkptCapacity = 2;
 constexpr int kDevErrPrecondition = 3;  // an input outside its stated range (checks pass)
+constexpr int kDevErrBadAxis = 4;       // a rotation axis outside the given positions
 
 // Address of this device's error flag (int on the device), or nullptr.
 int* device_error_flag();
@@ -183,5 +184,28 @@ cudaError_t launch_wait_selftest(uint64_t timeout_ns, int* err, int* warps_gave_
 // g[t][h][c] = gs[t][h] for every channel c: scalar gates spread for the fp32 path.
 cudaError_t launch_expand_scalar_gate(const float* gs, float* g, int64_t n_tokens, int H,
                                       cudaStream_t s);
+
+// Per-head RMSNorm (eps < 0: none) and rotation by position of q and k; strides in
+// elements between tokens, 16-byte multiples.  An axis outside [0, n_axes) raises
+// kDevErrBadAxis in *err.
+cudaError_t launch_norm_rope(const void* q, const void* k, int bf16, const float* wq,
+                             const float* wk, float eps, const int32_t* pos, int n_axes,
+                             const int32_t* axis, const float* freq, int F, int interleaved,
+                             void* qo, void* ko, int64_t n_tokens, int Hq, int Hk, int64_t sq,
+                             int64_t sk, int64_t sqo, int64_t sko, int* err, cudaStream_t s);
+
+// Linear attention with a decay for each head (g_head: g is [H], else [tokens][H]); q, k
+// have Hk heads, v, o and the state H (a multiple).
+// T new tokens a state, the state advanced by n_advance[n] of them (null: all).
+cudaError_t launch_linear_step(const void* q, const void* k, const void* v, int bf16,
+                               const float* g, int g_head, float scale, float* S, void* o,
+                               const int32_t* n_advance, int N, int T, int H, int Hk, bool multi,
+                               cudaStream_t s);
+// The prompt pass on fp32 CUDA cores; `ws` starts with the chunk plan.
+size_t linear_simt_workspace_bytes(int64_t n_tokens, int n_seqs, int H);
+cudaError_t launch_linear_simt(const void* q, const void* k, const void* v, int bf16,
+                               const float* g, int g_head, float scale, const float* h0, void* o,
+                               float* hT, int64_t n_tokens, int n_seqs, int H, int Hk, void* ws,
+                               cudaStream_t s);
 
 }  // namespace kda

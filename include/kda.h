@@ -393,14 +393,101 @@ kda_status_t kda_recurrent_multi_step(const void* q, const void* k, const void* 
                                       const int32_t* n_advance, int N, int T, int H, int dk,
                                       int dv, kda_stream_t stream);
 
+/*
+ * kda_qk_norm_rope -- per-head RMSNorm of q and k and the rotation by position, one
+ * pass over both.  For every row x of 128 channels (one token, one head):
+ *     y = w * x / sqrt(mean(x^2) + eps)                  (eps < 0: y = x)
+ *     phi_i = positions[axis_i][t] * inv_freq[i],  i < n_freq
+ *     (a, b) <- (a cos phi_i - b sin phi_i, a sin phi_i + b cos phi_i)
+ * on the pairs (a, b) = (y[i], y[i + n_freq]), or (y[2i], y[2i + 1]) with `interleaved`;
+ * channels from 2 n_freq on are y.  Everything is fp32 (the angle fp64, so that far
+ * positions keep their phase), rounded once at the store.
+ *   q, k      rows of Hq (Hk) x 128 channels of `dtype`, token t at t * q_stride
+ *             (k_stride) elements: slices of one packed projection need no copy.
+ *             Strides are at least Hq * 128 (Hk * 128) and multiples of 16 bytes.
+ *   q_weight, k_weight  fp32 [128] shared by the heads (NULL: ones); only with the norm.
+ *             (An L2 norm x / sqrt(sum(x^2) + e) is eps = e / 128 and weights 128^-1/2.)
+ *   eps       finite; < 0 turns the norm off.
+ *   positions int32 [n_axes][n_tokens], any sign.  One axis for text; several (time,
+ *             height, width) for images and video.
+ *   freq_axis int32 [n_freq], the axis of every frequency, 0 <= axis < n_axes (sections or
+ *             any interleaving); NULL: axis 0, allowed with n_axes = 1 only.  An entry out
+ *             of range is read as 0 and reported by kda_get_device_error.
+ *   inv_freq  fp32 [n_freq], n_freq a multiple of 8 from 8 to 64 (64: the whole head turns).
+ *   q_out, k_out  written, token strides q_out_stride, k_out_stride.  q_out may be q with
+ *             the same stride (in place), k_out may be k; any other overlap of an output
+ *             with an input or the other output is not allowed.
+ * n_tokens == 0 is a no-op.  d must be 128.
+ */
+kda_status_t kda_qk_norm_rope(const void* q, const void* k, int dtype, const float* q_weight,
+                              const float* k_weight, float eps, const int32_t* positions,
+                              int n_axes, const int32_t* freq_axis, const float* inv_freq,
+                              int n_freq, int interleaved, void* q_out, void* k_out,
+                              int64_t n_tokens, int Hq, int Hk, int d, int64_t q_stride,
+                              int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                              kda_stream_t stream);
+
+/* Flags of the linear-attention entries. */
+enum {
+  KDA_LINEAR_FP32_CORES = 1u, /* prompt pass: fp32 CUDA cores even for bf16 inputs */
+  KDA_LINEAR_HEAD_DECAY = 4u  /* g is [H]: one constant log-decay a head */
+};
+
+/*
+ * kda_linear_chunk_fwd -- prompt pass of linear attention with a decay for each head
+ * (KDA without the delta-rule erase and with a scalar decay):
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ * over whole packed sequences.  Layouts, cu_seqlens, B and T, h0, hT, workspace and
+ * errors as kda_chunk_fwd; hT continues as the S of kda_linear_recurrent_step.
+ *   q, k   [NT][Hk][128], v, o [NT][H][128] of `dtype`; H a multiple of Hk: value head
+ *          h uses query and key head h / (H / Hk).  q and k are used as given.
+ *   g      fp32 log-decays [NT][H], or [H] with KDA_LINEAR_HEAD_DECAY; any g <= 0, -inf
+ *          included (the state is dropped there).
+ *   scale  finite.
+ * KDA_F32 inputs are evaluated on fp32 CUDA cores.  A non-finite q, k or v reaches outputs
+ * of its own sequence and head only; which rows of its 128-token chunk it reaches is not
+ * specified.  cu_seqlens that does not run from 0 to NT without decreasing is reported by
+ * kda_get_device_error; the outputs are then unspecified, nothing outside o and hT is
+ * written.
+ * kda_linear_chunk_fwd_workspace_size: bytes of workspace (0 for invalid arguments).
+ */
+size_t kda_linear_chunk_fwd_workspace_size(int64_t n_tokens, int n_seqs, int H, int dtype,
+                                           unsigned flags);
+kda_status_t kda_linear_chunk_fwd(const void* q, const void* k, const void* v, int dtype,
+                                  const float* g, float scale, const float* h0,
+                                  const int32_t* cu_seqlens, int n_seqs, int B, int64_t T, int H,
+                                  int Hk, int dk, int dv, void* o, float* hT, void* workspace,
+                                  size_t ws_bytes, kda_stream_t stream, unsigned flags);
+
+/*
+ * kda_linear_recurrent_step -- one token of the recurrence above for N sequences, the
+ * states updated in place: q, k [N][Hk][128], v, o [N][H][128], g [N][H] (or [H] with
+ * KDA_LINEAR_HEAD_DECAY), S [N][H][dv][dk] fp32.  o must not overlap the inputs.
+ * N == 0 is a no-op.  Errors as kda_recurrent_step.
+ *
+ * kda_linear_recurrent_multi_step -- T (1..KDA_MULTI_STEP_MAX_T) tokens per sequence in one
+ * pass over the states: q, k [N][T][Hk][128], v, o [N][T][H][128], g [N][T][H] (or [H]);
+ * n_advance and o (may be NULL) as in kda_recurrent_multi_step.
+ */
+kda_status_t kda_linear_recurrent_step(const void* q, const void* k, const void* v, int dtype,
+                                       const float* g, float scale, float* S, void* o, int N,
+                                       int H, int Hk, int dk, int dv, kda_stream_t stream,
+                                       unsigned flags);
+kda_status_t kda_linear_recurrent_multi_step(const void* q, const void* k, const void* v,
+                                             int dtype, const float* g, float scale, float* S,
+                                             void* o, const int32_t* n_advance, int N, int T,
+                                             int H, int Hk, int dk, int dv, kda_stream_t stream,
+                                             unsigned flags);
+
 /* Message for the last non-OK status returned on this thread (never NULL). */
 const char* kda_last_error_string(void);
 
 /* Reads and clears the device error flag set by the kernels.  Synchronizes
  * `stream`.  Returns KDA_OK; KDA_ERR_DEVICE_TIMEOUT when a bounded device-side
  * wait gave up; KDA_ERR_INVALID_ARG when cu_seqlens was malformed (clamped on
- * the device), more checkpoints than slots were asked for, or the input check
- * (KDA_CHUNK_CHECK_INPUTS) found an out-of-range g or beta. */
+ * the device), more checkpoints than slots were asked for, the input check
+ * (KDA_CHUNK_CHECK_INPUTS) found an out-of-range g or beta, or a rotation axis was
+ * out of range (kda_qk_norm_rope). */
 kda_status_t kda_get_device_error(kda_stream_t stream);
 
 /*

@@ -273,3 +273,61 @@ def gate_softplus(z, A) -> np.ndarray:
     ``logaddexp(0, z)``, exact for large |z|)."""
     z, A = _f64(z), _f64(A)
     return -np.exp(A)[None, :, None] * np.logaddexp(0.0, z)
+
+
+def linear_recurrence(q, k, v, g, h0=None, cu_seqlens=None, scale: float = 1.0, n_advance=None):
+    """Linear attention with a decay for each head, token by token in fp64:
+    ``S_t = e^{g_t} S_{t-1} + k_t v_t^T``, ``o_t = scale S_t^T q_t`` (KDA without the
+    erase and with one decay a head).  q, k [NT, Hk, dk], v [NT, H, dv] (value head h uses
+    key head h // (H // Hk)), g [NT, H] or [H], h0 [N, H, dv, dk] or None.  ``n_advance``
+    [N]: the returned state is the one after that many tokens of each sequence (None: all;
+    the outputs are always of every token).  Returns ``(o, hT)``."""
+    q, k, v, g, h0 = (_f64(x) for x in (q, k, v, g, h0))
+    NT, H, dv = v.shape
+    rep = H // q.shape[1]
+    q, k = np.repeat(q, rep, axis=1), np.repeat(k, rep, axis=1)
+    g = np.broadcast_to(g, (NT, H))
+    if cu_seqlens is None:
+        cu = [0, NT]
+    else:
+        if hasattr(cu_seqlens, "detach"):
+            cu_seqlens = cu_seqlens.detach().cpu().numpy()
+        cu = [int(x) for x in cu_seqlens]
+    N, dk = len(cu) - 1, k.shape[2]
+    o, hT = np.zeros((NT, H, dv)), np.zeros((N, H, dv, dk))
+    for n in range(N):
+        S = np.zeros((H, dv, dk)) if h0 is None else h0[n].copy()
+        last = cu[n + 1] - cu[n] if n_advance is None else int(n_advance[n])
+        if last == 0:
+            hT[n] = S
+        for i, t in enumerate(range(cu[n], cu[n + 1])):
+            S = np.exp(g[t])[:, None, None] * S + v[t][:, :, None] * k[t][:, None, :]
+            o[t] = scale * np.einsum("hvk,hk->hv", S, q[t])
+            if i + 1 == last:
+                hT[n] = S
+    return o, hT
+
+
+def norm_rope(x, positions, inv_freq, weight=None, eps=1e-6, freq_axis=None, interleaved=False):
+    """``x / rms(x) * weight`` over the channels of each head (eps None: x as it is), then
+    the rotation of the pairs (i, i + F), or (2i, 2i + 1), by ``positions[axis_i] *
+    inv_freq[i]``, as a complex product, fp64.  x [NT, H, D], positions [NT] or
+    [n_axes, NT]; channels from 2F on are not rotated."""
+    x, inv_freq = _f64(x), _f64(inv_freq)
+    pos = _f64(positions)
+    F = len(inv_freq)
+    axis = np.zeros(F, dtype=int) if freq_axis is None else np.asarray(
+        freq_axis.cpu() if hasattr(freq_axis, "cpu") else freq_axis, dtype=int)
+    pos = pos.reshape(-1, x.shape[0])
+    y = x
+    if eps is not None:
+        y = y / np.sqrt(np.mean(y * y, axis=-1, keepdims=True) + eps)
+        if weight is not None:
+            y = y * _f64(weight)
+    turn = np.exp(1j * pos[axis].T * inv_freq)[:, None, :]
+    out = y.copy()
+    lo, hi = (slice(0, 2 * F, 2), slice(1, 2 * F, 2)) if interleaved else (slice(0, F),
+                                                                          slice(F, 2 * F))
+    z = (y[..., lo] + 1j * y[..., hi]) * turn
+    out[..., lo], out[..., hi] = z.real, z.imag
+    return out
