@@ -542,7 +542,8 @@ def linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale: float = 1.0
     q, k [B, T, Hk, 128] or packed [NT, Hk, 128] (with ``cu_seqlens``), v [..., H, 128], H a
     multiple of Hk (value head h uses key head h // (H // Hk)); bf16 or fp32.  g fp32
     log-decays <= 0, [..., H] (one a token and head) or [H].  h0, cu_seqlens, outputs and
-    ``workspace`` as :func:`chunk_fwd`; ``flags``: ``FP32_CORES``.  Returns ``(o, hT)``; hT is
+    ``workspace`` as :func:`chunk_fwd`; ``flags``: ``FP32_CORES``, ``SEQUENTIAL`` and
+    ``segment_chunks(n)`` (segments of n 128-token chunks).  Returns ``(o, hT)``; hT is
     the S of :func:`linear_recurrent_step`.
     """
     lead = tuple(q.shape[:-2])
@@ -568,11 +569,11 @@ def linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale: float = 1.0
     if output_final_state:
         hT = _like(final_state_out, "final_state_out", (N, H, dv, dk), torch.float32, dev)
     fl |= int(flags)
-    if workspace is None:
-        need = lib.kda_linear_chunk_fwd_workspace_size(NT, N, H, dt, fl)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, dev)
     with torch.cuda.device(dev):
+        if workspace is None:
+            need = lib.kda_linear_chunk_fwd_workspace_size(NT, N, H, dt, fl)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _need(workspace, "workspace", torch.uint8, dev)
         _check(lib.kda_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), float(scale),
                                         _ptr(h0), _ptr(cu_seqlens), N, B, T, H, Hk, dk, dv,
                                         _ptr(o), _ptr(hT), _ptr(workspace), workspace.numel(),

@@ -758,6 +758,11 @@ kda_status_t linear_heads(const char* fn, int dtype, float scale, int H, int Hk,
   return KDA_OK;
 }
 
+int linear_segments(int64_t n_tokens, int n_seqs, int H, unsigned flags) {
+  return kda::linear_segment_chunks(n_tokens, n_seqs, H, (int)(flags >> 16),
+                                    (flags & KDA_LINEAR_SEQUENTIAL) != 0);
+}
+
 kda_status_t linear_step_impl(const char* fn, const void* q, const void* k, const void* v,
                               int dtype, const float* g, float scale, float* S, void* o,
                               const int32_t* n_advance, int N, int T, int H, int Hk, int dk,
@@ -792,8 +797,10 @@ extern "C" {
 
 size_t kda_linear_chunk_fwd_workspace_size(int64_t n_tokens, int n_seqs, int H, int dtype,
                                            unsigned flags) {
-  (void)flags;
   if (n_tokens < 0 || n_seqs < 1 || H < 1 || (dtype != KDA_F32 && dtype != KDA_BF16)) return 0;
+  if (dtype == KDA_BF16 && !(flags & KDA_LINEAR_FP32_CORES))
+    return kda::linear_tc_workspace_bytes(n_tokens, n_seqs, H,
+                                          linear_segments(n_tokens, n_seqs, H, flags));
   return kda::plan_bytes(n_tokens, n_seqs) + kda::linear_simt_workspace_bytes(n_tokens, n_seqs, H);
 }
 
@@ -820,7 +827,8 @@ kda_status_t kda_linear_chunk_fwd(const void* q, const void* k, const void* v, i
   }
   if (T < 0 || NT > INT32_MAX - 2 * kda::kChunk || (int64_t)N * H > INT32_MAX)
     return fail(KDA_ERR_INVALID_ARG, "%s: token or state count out of range", fn);
-  if (flags & ~(unsigned)(KDA_LINEAR_HEAD_DECAY | KDA_LINEAR_FP32_CORES))
+  if (flags & ~(unsigned)(KDA_LINEAR_HEAD_DECAY | KDA_LINEAR_FP32_CORES | KDA_LINEAR_SEQUENTIAL |
+                          0xffff0000u))
     return fail(KDA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
   if ((NT > 0 && (!q || !k || !v || !g || !o)) || !workspace)
     return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
@@ -838,7 +846,14 @@ kda_status_t kda_linear_chunk_fwd(const void* q, const void* k, const void* v, i
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int* err = kda::device_error_flag();
   const int g_head = (flags & KDA_LINEAR_HEAD_DECAY) ? 1 : 0;
-  cudaError_t e = kda::launch_plan(cu_seqlens, N, T_per_seq, NT, workspace, err, s);
+  cudaError_t e;
+  if (dtype == KDA_BF16 && !(flags & KDA_LINEAR_FP32_CORES)) {
+    e = kda::launch_linear_tc(q, k, v, g, g_head, scale, h0, cu_seqlens, T_per_seq, o, hT, NT, N, H,
+                              Hk, linear_segments(NT, N, H, flags), workspace, err, s);
+    if (e != cudaSuccess) return cuda_fail(e, "linear chunk launch");
+    return KDA_OK;
+  }
+  e = kda::launch_plan(cu_seqlens, N, T_per_seq, NT, workspace, err, s);
   if (e != cudaSuccess) return cuda_fail(e, "chunk plan launch");
   e = kda::launch_linear_simt(q, k, v, dtype == KDA_BF16, g, g_head, scale, h0, o, hT, NT, N, H,
                               Hk, workspace, s);

@@ -207,5 +207,13 @@ cudaError_t launch_linear_simt(const void* q, const void* k, const void* v, int 
                                const float* g, int g_head, float scale, const float* h0, void* o,
                                float* hT, int64_t n_tokens, int n_seqs, int H, int Hk, void* ws,
                                cudaStream_t s);
+// The prompt pass on the tensor cores (bf16), cu_seqlens or T_per_seq tokens a sequence,
+// in 128-token chunks; seg_chunks > 0: sequences are cut into segments of so many.
+int linear_segment_chunks(int64_t n_tokens, int n_seqs, int H, int forced, bool sequential);
+size_t linear_tc_workspace_bytes(int64_t n_tokens, int n_seqs, int H, int seg_chunks);
+cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const float* g,
+                             int g_head, float scale, const float* h0, const int32_t* cu,
+                             int64_t T_per_seq, void* o, float* hT, int64_t n_tokens, int n_seqs,
+                             int H, int Hk, int seg_chunks, void* ws, int* err, cudaStream_t s);
 
 }  // namespace kda

@@ -430,6 +430,7 @@ kda_status_t kda_qk_norm_rope(const void* q, const void* k, int dtype, const flo
 /* Flags of the linear-attention entries. */
 enum {
   KDA_LINEAR_FP32_CORES = 1u, /* prompt pass: fp32 CUDA cores even for bf16 inputs */
+  KDA_LINEAR_SEQUENTIAL = 2u, /* prompt pass: never cut a sequence into segments */
   KDA_LINEAR_HEAD_DECAY = 4u  /* g is [H]: one constant log-decay a head */
 };
 
@@ -444,7 +445,12 @@ enum {
  *   g      fp32 log-decays [NT][H], or [H] with KDA_LINEAR_HEAD_DECAY; any g <= 0, -inf
  *          included (the state is dropped there).
  *   scale  finite.
- * KDA_F32 inputs are evaluated on fp32 CUDA cores.  A non-finite q, k or v reaches outputs
+ * KDA_BF16 inputs run on the tensor cores in 128-token chunks (fp32 accumulation and state;
+ * o within about one more bf16 rounding of the fp32 result, hT to fp32 accuracy), KDA_F32
+ * inputs on fp32 CUDA cores.  When few (sequence, head) pairs would leave SMs idle, long
+ * bf16 sequences are cut into segments that run at once (the result equals the
+ * uncut one up to rounding); KDA_CHUNK_SEGMENT_CHUNKS(n) forces segments of n 128-token
+ * chunks, KDA_LINEAR_SEQUENTIAL turns them off.  A non-finite q, k or v reaches outputs
  * of its own sequence and head only; which rows of its 128-token chunk it reaches is not
  * specified.  cu_seqlens that does not run from 0 to NT without decreasing is reported by
  * kda_get_device_error; the outputs are then unspecified, nothing outside o and hT is

@@ -395,3 +395,49 @@ def test_layer_prompt_then_tokens(kda, dtype):
     assert errors(S, rh)[0] <= F32_REL_L2
     qr = oracle.norm_rope(q_in, pos, f, wq)
     assert errors(qn, qr)[0] <= (2.0 ** -8 if dtype == torch.bfloat16 else 1e-6)
+
+
+# -------------------------------------------------------------------------- segments
+@pytest.mark.parametrize("decay", ["token", "head"])
+@pytest.mark.parametrize("n", [1, 2, 5])
+def test_segments_match_the_oracle(kda, n, decay):
+    """Sequences cut into segments of n chunks: empty, one-token, exact and ragged lengths."""
+    d = make([700, 0, 1, 128 * n, 128 * n + 1, 127], 3, 3, torch.bfloat16, seed=90 + n, decay=decay)
+    check(*chunk(kda, d, flags=kda.segment_chunks(n), scale=0.5), d, 0.5)
+    kda.get_device_error()
+
+
+def test_segments_with_the_state_in_place_and_dropped(kda):
+    d = make([1500], 2, 1, torch.bfloat16, seed=95)
+    d["g"][600:603] = -float("inf")
+    S = d["h0"].cuda()
+    c = cuda(d)
+    o, hT = kda.linear_chunk_fwd(c["q"], c["k"], c["v"], c["g"], S, c["cu"], final_state_out=S,
+                                 flags=kda.segment_chunks(3))
+    assert hT is S
+    check(o, S, d)
+
+
+def test_segments_chosen_for_a_long_sequence(kda):
+    """One long sequence with few heads is cut by default (the kernels that ran say so) and
+    agrees with the uncut run and, on its first head, with the oracle."""
+    d = make([8192 + 77], 2, 2, torch.bfloat16, seed=97, decay="head")
+    kda.profile_enable(True)
+    o, hT = chunk(kda, d)
+    ran = kda.profile_collect()
+    kda.profile_enable(False)
+    assert ran["kda_linear_tc"][0] == 1 and "kda_linear_tc_state" in ran
+    o1, h1 = chunk(kda, d, flags=kda.SEQUENTIAL)
+    assert errors(o, to64(o1))[0] <= 2.0 ** -8 and errors(hT, to64(h1))[0] <= F32_REL_L2
+    one = dict(d, q=d["q"][:, :1], k=d["k"][:, :1], v=d["v"][:, :1], g=d["g"][:1], h0=d["h0"][:, :1])
+    check(o[:, :1], hT[:, :1], one)
+
+
+def test_segments_with_malformed_cu_seqlens(kda):
+    d = make([400, 300], 2, 2, torch.bfloat16, seed=99)
+    kda.get_device_error()
+    for cu in ([0, 700, 500], [300, 700, 700], [0, -3, 900]):
+        d["cu"] = torch.tensor(cu, dtype=torch.int32)
+        chunk(kda, d, flags=kda.segment_chunks(1))
+        with pytest.raises(kda.KdaError, match="cu_seqlens"):
+            kda.get_device_error()
