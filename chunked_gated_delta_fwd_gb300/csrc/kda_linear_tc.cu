@@ -11,20 +11,30 @@
 // memory as S^T (lanes = value rows, fp32) for a whole chain.  Four MMA groups a chunk
 // (M = N = K = 128 each):
 //     QK   scores = Q K^T                      (lanes = tokens)
-//     QS   Q S, from a bf16 copy of S^T        (lanes = tokens)
-//     KV   S^T += V^T Kw, Kw_j = e^{G_C - G_j} k_j, after S^T *= e^{G_C}
-//     PV   P V with P = scale * decay * scores, bf16, from tensor memory
-// QS and PV have an accumulator each: e^{G_i} is applied to Q S in fp32 where o is written.
+//     QS   O = Q S, from a bf16 copy of S^T    (lanes = tokens); then O_i *= scale e^{G_i}
+//     KV   S^T += Vw^T K, Vw_j = e^{G_C - G_j} v_j, after S^T *= e^{G_C}
+//     PV   O += P V with P = scale * decay * scores, bf16
 // Rounding: P and the copy of S to bf16 (o is bf16 as well, each adds an error of the size
-// of o's own rounding).  The final state is fp32, so Kw is kept as two bf16 parts, hi + lo
-// (16 bits of each weighted key), and KV is issued for both.
+// of o's own rounding).  The final state is fp32, so Vw is kept as two bf16 parts, hi + lo
+// (17 bits of each weighted value), and KV is issued for both.
 //
-// Tiles of q, k and v arrive by tensor copies, 128-byte swizzled; the same bytes serve as a
-// K-major operand (channels contracted) and as an MN-major one (tokens contracted), so
-// nothing is transposed.  Kw overwrites the k tile in place (hi) and one more tile (lo).
+// What bounds a chunk is shared-memory bandwidth (128 bytes a clock): an M = N = 128 MMA
+// reads 128 bytes of operands a clock when both come from shared memory.  So P and both
+// parts of Vw are A operands in tensor memory, k and v tiles are used as the tensor copies
+// left them (128-byte swizzled: the same bytes are a K-major operand where channels are
+// contracted and an MN-major one where tokens are), v reaches the lanes of its channels by
+// transposing matrix loads, and o leaves by a tensor copy from a staged tile instead of
+// 16-byte row pieces.
 //
-// Warps: copy, MMA issue, decay vectors; then four groups of four, one warp of each on
-// every SM sub-partition: weighted keys, scores -> P, outputs, state.
+// o leaves from the tile that held q (its last reader, QS, is done by then), so the ring
+// holds two whole chunks of q, k and v.
+//
+// Warps: a front warp (jobs, decay vectors, tensor copies in), MMA issue, copies out; then
+// four groups of four, one warp of each on every SM sub-partition: weighted values, scores
+// -> P, outputs, state.  The front warp decodes the work and hands every chunk to the others
+// as one record in shared memory, and loops stay rolled: five roles run at once, and with
+// 94 KB of code (jobs decoded by every role, unrolled loops) instruction fetch bounded
+// the kernel, at 8500 clocks a chunk.
 //
 // Decays.  With L_i the sum of g inside a 32-token block up to i, U_j the sum behind j in
 // its block and T_b the block totals, every exponent but those inside a diagonal block is
@@ -49,45 +59,72 @@ constexpr int D = kD;   // 128
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinG = -100.f;
 
-constexpr int kSlots = 5;                  // ring of q / k / v tiles
 constexpr uint32_t kTileBytes = C * D * 2;  // 32 KB: two 64-channel blocks of 128 rows
 constexpr uint32_t kHalfTile = kTileBytes / 2;
-constexpr uint32_t kLoOff = kSlots * kTileBytes;
-constexpr uint32_t kSbOff = kLoOff + kTileBytes;   // bf16 copy of S^T, K-major
-constexpr uint32_t kVecOff = kSbOff + kTileBytes;  // two decay vectors
-struct Vec {
-  float L[C];   // sum of g (log2 units) inside the token's 32-token block, inclusive
-  float cf[C];  // 2^(sum of g behind the token inside its block)
-  float T[4];   // block totals
-  float pad[4];
+enum { tK = 0, tQ = 1, tV = 2 };            // tile t of chunk `it` sits in slot 3 (it & 1) + t
+constexpr uint32_t kSbOff = 6 * kTileBytes;  // bf16 copy of S^T, K-major
+constexpr uint32_t kVecOff = kSbOff + kTileBytes;
+
+// A chunk as the front warp hands it out: what it is, and its decays (log2 units).
+struct __align__(16) Rec {
+  float L[C];    // sum of g inside the token's 32-token block, inclusive
+  float cf[C];   // 2^(sum of g behind the token inside its block)
+  float T[4];    // block totals
+  float aft[4];  // 2^(totals of the blocks behind)
+  const float* init;  // first chunk of a job: state to start from (null: zero)
+  float* fin;         // last chunk of a job: where the state goes (null: nowhere)
+  float* decay;       // last chunk: where the job's whole decay goes (null: nowhere)
+  int tok, len, h, flags;
+  float total;   // of the chunk
+  float sofar;   // of the job, with this chunk
 };
-constexpr uint32_t kBarOff = kVecOff + 2 * sizeof(Vec);
-constexpr uint32_t kSmemUsed = kBarOff + 24 * 8 + 16;
+enum { kFirst = 1, kLast = 2, kStop = 4 };
+constexpr uint32_t kBarOff = kVecOff + 2 * sizeof(Rec);
+constexpr uint32_t kBarBytes = 32 * 8;
+constexpr uint32_t kSmemUsed = kBarOff + kBarBytes + 16;
 constexpr uint32_t kSmemBytes = 232448;  // all an SM has: one CTA each
 static_assert(kSmemUsed <= kSmemBytes, "shared memory");
 
 // barriers
 enum {
-  bFull = 0,              // [5] tile landed
-  bEmpty = bFull + kSlots,  // [5] tile read by its last MMA
-  bVFull = bEmpty + kSlots,  // [2] decay vector written
-  bVEmpty = bVFull + 2,      // [2] decay vector read
-  bQK = bVEmpty + 2,         // scores complete
-  bKt = bQK + 1,             // [2] weighted keys of tokens 0-63, 64-127 written
-  bP = bKt + 2,              // P written
-  bS = bP + 1,               // state scaled and copied
-  bKV = bS + 1,              // state updated
-  bPV = bKV + 1,             // outputs complete
-  bO = bPV + 1,              // accumulators read out
-  bDrain = bO + 1,
+  bFull = 0,           // [6] tile landed
+  bEmpty = bFull + 6,  // [6] tile free again
+  bRFull = bEmpty + 6,  // [2] record written
+  bREmpty = bRFull + 2,  // [2] record read
+  bQK = bREmpty + 2,   // scores complete
+  bVw = bQK + 1,       // [2] weighted values of tokens 0-63, 64-127 written
+  bP = bVw + 2,        // P written
+  bS = bP + 1,         // state scaled and copied
+  bKV = bS + 1,        // state updated
+  bQS = bKV + 1,       // Q S complete
+  bOs = bQS + 1,       // O scaled
+  bPV = bOs + 1,       // outputs complete
+  bO = bPV + 1,        // outputs read out
+  bOut = bO + 1,       // outputs staged
+  bDrain = bOut + 1,
   kBars = bDrain + 1
 };
-static_assert(kBars <= 24, "barriers");
+static_assert(kBars * 8 <= kBarBytes, "barriers");
 
-constexpr uint32_t kT_S = 0, kT_P = 128, kT_QS = 256, kT_PV = 384;  // TMEM columns
+// TMEM columns: state, scores (P over their left half), O, weighted values hi and lo
+constexpr uint32_t kT_S = 0, kT_P = 128, kT_O = 256, kT_Vhi = 384, kT_Vlo = 448;
 
 constexpr int kGroup = 128;
 constexpr int kThreads = 128 + 4 * kGroup;
+// A wait gives up after this many polls (each suspends for up to about a microsecond).
+constexpr uint32_t kPolls = 1u << 24;
+
+__device__ __forceinline__ bool wait_poll(uint32_t bar, uint32_t parity, int* err,
+                                          volatile int* abort_flag) {
+#pragma unroll 1
+  for (uint32_t n = 0; n < kPolls; ++n) {
+    if (mbar_try_wait(bar, parity & 1u)) return true;
+    if (*abort_flag) return false;
+  }
+  atomicExch(err, kDevErrTimeout);
+  *abort_flag = 1;
+  return false;
+}
 
 struct LinArgs {
   const float* g;
@@ -129,7 +166,7 @@ __device__ __forceinline__ void seq_range(const LinArgs& a, int n, int64_t& t0, 
   bool bad = x0 != t0 || x1 != t1 || t1 < t0 || (n == 0 && x0 != 0) ||
              (n == a.n_seqs - 1 && x1 != a.n_tokens);
   if (t1 < t0) t1 = t0;
-  if (bad && a.err) atomicExch(a.err, kDevErrBadSeqlens);
+  if (bad) atomicExch(a.err, kDevErrBadSeqlens);
 }
 
 template <bool kOut>
@@ -171,44 +208,63 @@ __device__ __forceinline__ Job get_job(const LinArgs& a, int item) {
   return j;
 }
 
+// Four transposed 8 x 8 bf16 matrices; lane l gives the address of row l % 8 of matrix l / 8
+// and gets, of each, column l / 4 of rows 2 (l % 4) and + 1 as one pair.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 lanes x 8 columns: of each four columns, registers 2i and 2i + 1 of lane l go to TMEM
+// lanes l / 4 and l / 4 + 8, column 4 i + l % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// 32 lanes x 8 columns store.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// 3-D tiled tensor copy shared -> global in the calling thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::
+                   "l"(reinterpret_cast<uint64_t>(tmap)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // kOut: outputs and final states.  Otherwise the state alone (the first pass over segments).
 template <bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     lin_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, const LinArgs a) {
-  constexpr int kTiles = kOut ? 3 : 2;  // tiles a chunk, in the order k, (q,) v
+                  const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_o, const LinArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   if (pad + kSmemUsed > kSmemBytes) {  // (uniform; dynamic shared memory starts aligned)
-    if (threadIdx.x == 0 && a.err) atomicExch(a.err, kDevErrTimeout);
+    if (threadIdx.x == 0) atomicExch(a.err, kDevErrTimeout);
     return;
   }
   uint8_t* sm = smem_raw + pad;
   const uint32_t base = smem_addr(sm);
   const uint32_t bars = base + kBarOff;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBarOff + 24 * 8);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBarOff + 24 * 8 + 8);
-  Vec* vecs = reinterpret_cast<Vec*>(sm + kVecOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBarOff + kBarBytes);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBarOff + kBarBytes + 8);
+  Rec* recs = reinterpret_cast<Rec*>(sm + kVecOff);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
   if (t == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(bar(bFull + i), 1);
-      mbar_init(bar(bEmpty + i), 1);
+    // arrivals a phase: copies, commits and single threads 1, groups one a warp
+    for (int i = 0; i < kBars; ++i) {
+      const bool group = (i >= bVw && i <= bS) || i == bOs || i == bO || i == bOut;
+      const bool rec = i == bREmpty || i == bREmpty + 1;  // every warp that reads records
+      mbar_init(bar(i), rec ? (kOut ? 18 : 9) : (group ? 4 : 1));
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(bVFull + i), 1);
-      mbar_init(bar(bVEmpty + i), kOut ? 16 : 8);  // warps that read the vector
-      mbar_init(bar(bKt + i), 4);
-    }
-    mbar_init(bar(bQK), 1);
-    mbar_init(bar(bP), 4);
-    mbar_init(bar(bS), 4);
-    mbar_init(bar(bKV), 1);
-    mbar_init(bar(bPV), 1);
-    mbar_init(bar(bO), 4);
-    mbar_init(bar(bDrain), 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -218,155 +274,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int items = job_count<kOut>(a);
-  auto wait = [&](int b, uint32_t parity) {
-    return wait_or_abort(bar(b), parity & 1u, a.err, abort_flag);
-  };
+  auto wait = [&](int b, uint32_t parity) { return wait_poll(bar(b), parity, a.err, abort_flag); };
   // the same for a whole warp: one outcome, so that warp-wide instructions stay together
   auto wait_warp = [&](int b, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(b, parity)) != 0;
   };
-  // ring position of tile i of chunk `it` (0: k, then q with outputs, last: v)
-  auto slot_of = [&](int it, int i) { return (kTiles * it + i) % kSlots; };
-  auto phase_of = [&](int it, int i) { return (uint32_t)((kTiles * it + i) / kSlots) & 1u; };
+  auto arrive = [&](int b) {  // once a warp, after all of its lanes
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
+  auto full = [](int tile, int it) { return bFull + 3 * (it & 1) + tile; };
+  auto empty = [](int tile, int it) { return bEmpty + 3 * (it & 1) + tile; };
+  auto slot = [](int tile, int it) { return (uint32_t)(3 * (it & 1) + tile) * kTileBytes; };
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ copies
-    if (lane == 0) {
-      int m = 0;  // tiles issued
-      bool ok = true;
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const Job j = get_job<kOut>(a, item);
-        for (int c = 0; c < j.chunks && ok; ++c) {
-          const int tok = (int)(j.t0 + (int64_t)c * C);
-          for (int i = 0; i < kTiles; ++i, ++m) {
-            const int s = m % kSlots;
-            if (m >= kSlots && !wait(bEmpty + s, (uint32_t)(m / kSlots - 1))) {
-              ok = false;
-              break;
-            }
-            const bool is_v = i == kTiles - 1;
-            const void* tm = is_v ? &tm_v : (i == 0 ? &tm_k : &tm_q);
-            const int head = is_v ? j.h : j.h / a.rep;
-            const uint32_t dst = base + s * kTileBytes;
-            mbar_arrive_expect_tx(bar(bFull + s), kTileBytes);
-            tma_load_3d(dst, tm, 0, head, tok, bar(bFull + s));
-            tma_load_3d(dst + kHalfTile, tm, 64, head, tok, bar(bFull + s));
-          }
-        }
-      }
-      if (*abort_flag)  // copies in flight must land before the CTA exits
-        for (int x = max(0, m - kSlots); x < m; ++x)
-          mbar_wait(bar(bFull + x % kSlots), (uint32_t)(x / kSlots) & 1u, a.err);
-    }
-  } else if (warp == 1) {
-    // -------------------------------------------------------------------- MMAs
-    // Order a chunk: QS, KV, PV, then QK of the next chunk.  KV goes as early as its
-    // operands allow: the state group works on its result while PV and QK run.
-    if (lane == 0) {
-      int total = 0;
-      for (int item = blockIdx.x; item < items; item += gridDim.x)
-        total += get_job<kOut>(a, item).chunks;
-      const uint32_t id_kk = idesc_bf16_mn(C, C, 0, 0);  // both operands K-major
-      const uint32_t id_kn = idesc_bf16_mn(C, D, 0, 1);  // B MN-major
-      const uint32_t id_nn = idesc_bf16_mn(D, D, 1, 1);  // both MN-major
-      bool any = false;
-      auto tile = [&](int it, int i) { return base + (uint32_t)slot_of(it, i) * kTileBytes; };
-      // K step s of a K-major tile / of an MN-major one (descriptors of step 0, advanced)
-      auto kstep = [](int s) { return (uint32_t)(s >> 2) * kHalfTile + (uint32_t)(s & 3) * 32u; };
-      auto qk = [&](int it) {
-        if (!wait(bFull + slot_of(it, 0), phase_of(it, 0)) ||
-            !wait(bFull + slot_of(it, 1), phase_of(it, 1)))
-          return false;
-        tc_fence_after();
-        const uint64_t dq = kmajor_desc(tile(it, 1), C, 0), dk = kmajor_desc(tile(it, 0), C, 0);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-          mma_bf16(tmem + kT_P, desc_advance(dq, kstep(s)), desc_advance(dk, kstep(s)), id_kk, s > 0);
-        mma_commit(bar(bQK));
-        any = true;
-        return true;
-      };
-      bool ok = total == 0 || !kOut || qk(0);
-      for (int it = 0; it < total && ok; ++it) {
-        const uint32_t par = (uint32_t)it;
-        ok = wait(bS, par);
-        if (!ok) break;
-        if (kOut) {
-          if (it > 0 && !wait(bO, par - 1)) break;
-          tc_fence_after();
-          const uint64_t dq = kmajor_desc(tile(it, 1), C, 0),
-                         ds = kmajor_desc(base + kSbOff, D, 0);
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_bf16(tmem + kT_QS, desc_advance(dq, kstep(s)), desc_advance(ds, kstep(s)), id_kk,
-                     s > 0);
-          mma_commit(bar(bEmpty + slot_of(it, 1)));
-          any = true;
-        }
-        ok = wait(bFull + slot_of(it, kTiles - 1), phase_of(it, kTiles - 1));
-        const uint64_t dv = mnmajor_desc_lbo(tile(it, kTiles - 1), kHalfTile, 1024, 0);
-        const uint64_t dhi = mnmajor_desc_lbo(tile(it, 0), kHalfTile, 1024, 0);
-        const uint64_t dlo = mnmajor_desc_lbo(base + kLoOff, kHalfTile, 1024, 0);
-        for (int hf = 0; hf < 2 && ok; ++hf) {  // tokens 0-63, 64-127
-          ok = wait(bKt + hf, par);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < C / 32; ++s) {
-            const uint32_t off = (uint32_t)(4 * hf + s) * 2048u;
-            mma_bf16(tmem + kT_S, desc_advance(dv, off), desc_advance(dlo, off), id_nn, 1u);
-            mma_bf16(tmem + kT_S, desc_advance(dv, off), desc_advance(dhi, off), id_nn, 1u);
-          }
-          any = true;
-        }
-        if (!ok) break;
-        mma_commit(bar(bKV));
-        mma_commit(bar(bEmpty + slot_of(it, 0)));
-        if (kOut) {
-          ok = wait(bP, par);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < C / 16; ++s)
-            mma_bf16_ta(tmem + kT_PV, tmem + kT_P + 8 * s, desc_advance(dv, (uint32_t)s * 2048u),
-                        id_kn, s > 0);
-          mma_commit(bar(bPV));
-        }
-        mma_commit(bar(bEmpty + slot_of(it, kTiles - 1)));
-        if (kOut && it + 1 < total) ok = qk(it + 1);
-      }
-      if (*abort_flag && any) {  // drain MMAs in flight
-        mma_commit(bar(bDrain));
-        mbar_wait(bar(bDrain), 0, a.err);
-      }
-    }
-  } else if (warp == 2) {
-    // ----------------------------------------------------------- decay vectors
-    int it = 0;
+    // ------------------------------------------------- jobs, decay vectors, copies in
+    const int items = job_count<kOut>(a);
+    constexpr int kTiles = kOut ? 3 : 2;
+    int it = 0, d = 0, m = 0;  // chunks, records, tiles copied
     bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const Job j = get_job<kOut>(a, item);
-      for (int c = 0; c < j.chunks; ++c, ++it) {
+    for (int item = blockIdx.x; ok; item += gridDim.x) {
+      const bool stop = item >= items;
+      Job j{};
+      if (!stop) j = get_job<kOut>(a, item);
+      float sofar = 0.f;
+      const int kv_head = j.h / a.rep;
+#pragma unroll 1
+      for (int c = 0; c < max(j.chunks, 1); ++c, ++d) {  // a job without tokens is one record
         const int len = min(C, j.tokens - c * C);
-        const int64_t tok = j.t0 + (int64_t)c * C;
+        const int tok = (int)(j.t0 + (int64_t)c * C);
         float g[4], u[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const int r = 32 * b + lane;
           g[b] = 0.f;
-          if (r < len) g[b] = __ldg(a.g + (a.g_head ? (int64_t)j.h : (tok + r) * a.H + j.h));
+          if (r < len)
+            g[b] = __ldg(a.g + (a.g_head ? (int64_t)j.h : (int64_t)(tok + r) * a.H + j.h));
         }
-        ok = it < 2 || wait_warp(bVEmpty + (it & 1), (uint32_t)(it >> 1) - 1);
+        ok = d < 2 || wait_warp(bREmpty + (d & 1), (uint32_t)(d >> 1) - 1);
         if (!ok) break;
-        Vec& v = vecs[it & 1];
+        Rec& v = recs[d & 1];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           g[b] = (g[b] < kMinG ? kMinG : g[b]) * kLog2e;  // NaN stays NaN
           u[b] = __shfl_down_sync(0xffffffffu, g[b], 1);
           if (lane == 31) u[b] = 0.f;
         }
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
@@ -375,270 +329,508 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane >= o) g[b] += x;
             if (lane + o < 32) u[b] += y;
           }
+        float after = 0.f;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 3; b >= 0; --b) {
           v.L[32 * b + lane] = g[b];
           v.cf[32 * b + lane] = exp2_approx(u[b]);
-          if (lane == 31) v.T[b] = g[b];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bVFull + (it & 1)));
-      }
-    }
-  } else if (warp >= 4 && warp < 8) {
-    // ------------------------------------------------------------ weighted keys
-    // Two threads a row, 64 rows at a time: hi part in place, lo part into its own tile.
-    // Rows past the sequence's end hold other tokens: their weighted keys and their
-    // values become zeros, so that nothing of them (a NaN) meets this sequence.
-    const int gt = t - 128, blk = gt & 1;
-    int it = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const Job j = get_job<kOut>(a, item);
-      for (int c = 0; c < j.chunks; ++c, ++it) {
-        const int len = min(C, j.tokens - c * C);
-        ok = wait_warp(bFull + slot_of(it, 0), phase_of(it, 0)) &&
-             wait_warp(bVFull + (it & 1), (uint32_t)(it >> 1)) &&
-             (!kOut || wait_warp(bQK, (uint32_t)it)) &&       // the raw keys are read
-             (it == 0 || wait_warp(bKV, (uint32_t)it - 1)) &&  // the lo tile is read
-             (len == C || wait_warp(bFull + slot_of(it, kTiles - 1), phase_of(it, kTiles - 1)));
-        if (!ok) break;
-        const Vec& v = vecs[it & 1];
-        uint8_t* kt = sm + slot_of(it, 0) * kTileBytes + blk * kHalfTile;
-        uint8_t* lo = sm + kLoOff + blk * kHalfTile;
-        uint8_t* vt = sm + slot_of(it, kTiles - 1) * kTileBytes + blk * kHalfTile;
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          const int r = 64 * hf + (gt >> 1), b = r >> 5;
-          float after = 0.f;
-#pragma unroll
-          for (int x = 1; x < 4; ++x) after += x > b ? v.T[x] : 0.f;
-          const float w = v.cf[r] * exp2_approx(after);
-          const bool in = r < len;
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            const uint32_t off = (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4));
-            const uint4 x = *reinterpret_cast<const uint4*>(kt + off);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-            uint32_t hw[4], lw[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float p = bf16_lo(xw[e]) * w, q = bf16_hi(xw[e]) * w;
-              hw[e] = pack_bf16(p, q);
-              lw[e] = pack_bf16(p - bf16_lo(hw[e]), q - bf16_hi(hw[e]));
-              if (!in) hw[e] = lw[e] = 0u;
-            }
-            *reinterpret_cast<uint4*>(kt + off) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-            *reinterpret_cast<uint4*>(lo + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-            if (!in) *reinterpret_cast<uint4*>(vt + off) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+          const float T = __shfl_sync(0xffffffffu, g[b], 31);
           if (lane == 0) {
-            mbar_arrive(bar(bKt + hf));
-            if (hf == 1) mbar_arrive(bar(bVEmpty + (it & 1)));
+            v.T[b] = T;
+            v.aft[b] = exp2_approx(after);
           }
+          after += T;
+        }
+        sofar += after;
+        if (lane == 0) {
+          v.init = j.init;
+          v.fin = j.fin;
+          v.decay = j.decay;
+          v.tok = tok;
+          v.len = len;
+          v.h = j.h;
+          v.flags = stop ? kStop : ((c == 0 ? kFirst : 0) | (c + 1 >= j.chunks ? kLast : 0));
+          v.total = after;
+          v.sofar = sofar;
+        }
+        arrive(bRFull + (d & 1));
+        if (len > 0) {
+          if (lane == 0) {
+#pragma unroll 1
+            for (int i = 0; i < 3; i += kOut ? 1 : 2) {
+              if (it >= 2 && !wait(empty(i, it), (uint32_t)(it >> 1) - 1)) {
+                ok = false;
+                break;
+              }
+              const void* tm = i == tK ? &tm_k : (i == tQ ? &tm_q : &tm_v);
+              const int head = i == tV ? j.h : kv_head;
+              const uint32_t dst = base + slot(i, it);
+              mbar_arrive_expect_tx(bar(full(i, it)), kTileBytes);
+              tma_load_3d(dst, tm, 0, head, tok, bar(full(i, it)));
+              tma_load_3d(dst + kHalfTile, tm, 64, head, tok, bar(full(i, it)));
+              ++m;
+            }
+          }
+          ++it;
+          ok = __all_sync(0xffffffffu, ok) != 0;
+          if (!ok) break;
         }
       }
+      if (stop) break;
     }
-  } else if (warp >= 8 && warp < 12) {
-    // -------------------------------------------------------------- scores -> P
-    // Thread = token row.  P (packed pairs) overwrites the scores' columns from the left,
-    // behind the block of scores being read.
-    if (kOut) {
-      const int w = warp & 3;
-      const uint32_t row = tmem + ((uint32_t)(32 * w) << 16) + kT_P;
-      int it = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const Job j = get_job<kOut>(a, item);
-        for (int c = 0; c < j.chunks; ++c, ++it) {
-          ok = wait_warp(bVFull + (it & 1), (uint32_t)(it >> 1)) && wait_warp(bQK, (uint32_t)it);
+    if (lane == 0 && *abort_flag) {  // copies in flight must land before the CTA exits
+#pragma unroll 1
+      for (int x = max(0, m - 2 * kTiles); x < m; ++x)
+        mbar_wait(bar(full(kOut ? x % 3 : 2 * (x % 2), x / kTiles)),
+                  (uint32_t)(x / kTiles >> 1) & 1u, a.err);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------------- MMAs
+    // Order a chunk: QS, KV, PV, then QK of the next chunk.  KV goes as early as its
+    // operands allow: the state group works on its result while PV and QK run.
+    if (lane == 0) {
+      const uint32_t id_kk = idesc_bf16_mn(C, C, 0, 0);  // both operands K-major
+      const uint32_t id_kn = idesc_bf16_mn(C, D, 0, 1);  // B MN-major
+      bool ok = true, any = false;
+      int d = 0;
+      // D = A B^T over 128 channels, both tiles K-major
+      auto mma_kk = [&](uint32_t dst, uint32_t at, uint32_t bt) {
+        uint64_t da = kmajor_desc(at, C, 0), db = kmajor_desc(bt, C, 0);
+#pragma unroll 1
+        for (int s = 0; s < 8; s += 2) {
+          mma_bf16(dst, da, db, id_kk, s > 0);
+          mma_bf16(dst, desc_advance(da, 32), desc_advance(db, 32), id_kk, 1u);
+          const uint32_t step = s == 2 ? kHalfTile - 64u : 64u;  // on to the next channel block
+          da = desc_advance(da, step);
+          db = desc_advance(db, step);
+        }
+      };
+#pragma unroll 1
+      for (int it = -1; ok; ++it) {
+        const uint32_t par = (uint32_t)it;
+        if (it >= 0) {
+          ok = wait(bS, par) && (!kOut || it == 0 || wait(bO, par - 1));
           if (!ok) break;
           tc_fence_after();
-          const Vec& v = vecs[it & 1];
-          const float Li = v.L[32 * w + lane];
+          if (kOut) {
+            mma_kk(tmem + kT_O, base + slot(tQ, it), base + kSbOff);
+            mma_commit(bar(bQS));
+          } else {
+            ok = wait(full(tK, it), par >> 1);
+            if (!ok) break;
+          }
+          any = true;
+          uint64_t dk = mnmajor_desc_lbo(base + slot(tK, it), kHalfTile, 1024, 0);
+          uint32_t va = tmem + kT_Vhi;
 #pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
-            uint32_t pk[16];
-            if (b > w) {  // keys behind every token of this warp
+          for (int s = 0; s < 8; ++s) {  // tokens 0-63, 64-127
+            if ((s & 3) == 0) {
+              ok = wait(bVw + (s >> 2), par);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            mma_bf16_ta(tmem + kT_S, va + (kT_Vlo - kT_Vhi), dk, id_kn, 1u);
+            mma_bf16_ta(tmem + kT_S, va, dk, id_kn, 1u);
+            dk = desc_advance(dk, 2048);
+            va += 8;
+          }
+          if (!ok) break;
+          mma_commit(bar(bKV));
+          mma_commit(bar(empty(tK, it)));
+          if (kOut) {
+            ok = wait(bP, par) && wait(bOs, par);
+            if (!ok) break;
+            tc_fence_after();
+            uint64_t dv = mnmajor_desc_lbo(base + slot(tV, it), kHalfTile, 1024, 0);
+#pragma unroll 1
+            for (int s = 0; s < 8; s += 2) {
+              mma_bf16_ta(tmem + kT_O, tmem + kT_P + 8 * s, dv, id_kn, 1u);
+              mma_bf16_ta(tmem + kT_O, tmem + kT_P + 8 * s + 8, desc_advance(dv, 2048), id_kn, 1u);
+              dv = desc_advance(dv, 4096);
+            }
+            mma_commit(bar(bPV));
+          }
+          mma_commit(bar(empty(tV, it)));
+        }
+        int len = 0;  // the next record that is a chunk
+        while (len <= 0) {
+          ok = wait(bRFull + (d & 1), (uint32_t)(d >> 1));
+          if (!ok) break;
+          len = recs[d & 1].len;
+          const int flags = recs[d & 1].flags;
+          mbar_arrive(bar(bREmpty + (d & 1)));
+          ++d;
+          if (flags & kStop) ok = false;
+          if (!ok) break;
+        }
+        if (!ok) break;
+        if (kOut) {
+          const uint32_t ph = (uint32_t)((it + 1) >> 1);
+          ok = wait(full(tK, it + 1), ph) && wait(full(tQ, it + 1), ph);
+          if (!ok) break;
+          tc_fence_after();
+          mma_kk(tmem + kT_P, base + slot(tQ, it + 1), base + slot(tK, it + 1));
+          mma_commit(bar(bQK));
+          any = true;
+        }
+      }
+      if (*abort_flag && any) {  // drain MMAs in flight
+        mma_commit(bar(bDrain));
+        mbar_wait(bar(bDrain), 0, a.err);
+      }
+    }
+  } else if (warp == 3) {
+    // ----------------------------------------------------------------- copies out
+    if (kOut && lane == 0) {
+      int it = 0;
+#pragma unroll 1
+      for (int d = 0;; ++d) {
+        if (!wait(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
+        const Rec& v = recs[d & 1];
+        const int len = v.len, flags = v.flags, h = v.h, tok = v.tok;
+        mbar_arrive(bar(bREmpty + (d & 1)));
+        if (flags & kStop) break;
+        if (len <= 0) continue;
+        if (!wait(bOut, (uint32_t)it)) break;
+        if (len == C) {  // a partial chunk was written by the output group
+          const uint32_t src = base + slot(tQ, it);
+          tma_store_3d(&tm_o, src, 0, h, tok);
+          tma_store_3d(&tm_o, src + kHalfTile, 64, h, tok);
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+        mbar_arrive(bar(empty(tQ, it)));
+        ++it;
+      }
+      bulk_wait_all();
+    }
+  } else if (warp >= 4) {
+    // The four groups: records in order, each with its own work on a chunk.
+    const int group = (warp >> 2) - 1, w = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
+    const int row = 32 * w + lane;
+    if (!kOut && (group == 1 || group == 2)) {
+      // no scores and no outputs
+    } else if (group == 0) {
+      // -------------------------------------------------------- weighted values
+      // Warp w takes value rows 32 w .. + 31: a transposing load brings 16 rows x 16
+      // tokens, a lane holding token pairs of one row, as the 16-lane stores to tensor
+      // memory want them.  Rows of k and v past the sequence's end hold other tokens: they
+      // become zeros (and so do their weighted values), so that nothing of them (a NaN)
+      // meets this sequence.
+      // matrix m of a load: value rows 8 (m & 1), tokens 8 (m >> 1); this lane's row of it
+      const int mrow = (lane & 7) + 8 * (lane >> 4), mdv = (lane >> 3) & 1;
+      int it = 0;
+#pragma unroll 1
+      for (int d = 0;; ++d) {
+        if (!wait_warp(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
+        const Rec& v = recs[d & 1];
+        const int len = v.len, flags = v.flags;
+        if (flags & kStop) break;
+        if (len > 0) {
+          const uint32_t ph = (uint32_t)(it >> 1);
+          bool ok = wait_warp(full(tV, it), ph) &&
+                    (it == 0 || wait_warp(bKV, (uint32_t)it - 1));  // the last chunk's are read
+          if (len < C) {
+            ok = ok && wait_warp(full(tK, it), ph) && (!kOut || wait_warp(bQK, (uint32_t)it));
+            // one outcome for the group, which meets at a barrier again below
+            ok = named_sync_and(2, kGroup, ok);
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t vt = base + slot(tV, it) + (uint32_t)(w >> 1) * kHalfTile;
+#pragma unroll 1
+          for (int x = 0; x < 16; ++x) {  // 16 tokens x 16 value rows: tokens outer
+            const int tok0 = 16 * (x >> 1), dh = x & 1;
+            const int tok = tok0 + mrow, ch = 4 * (w & 1) + 2 * dh + mdv;
+            uint32_t y[4], hi[4], lo[4];
+            ldmatrix4_trans(vt + (uint32_t)(tok * 128 + ((ch ^ (tok & 7)) << 4)), y);
+            const int pt = tok0 + 2 * (lane & 3);
+            const float f = v.aft[tok0 >> 5];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) pk[i] = 0u;
-            } else {
-              float s[32];
-              tmem_ld32(row + 32 * b, s);
-              tmem_wait_ld();
-              if (b < w) {
-                float between = 0.f;
+            for (int m = 0; m < 2; ++m) {  // eight tokens each
+              float2 ww = *reinterpret_cast<const float2*>(&v.cf[pt + 8 * m]);
+              ww = __fmul2_rn(ww, make_float2(f, f));
 #pragma unroll
-                for (int x = 1; x < 3; ++x) between += (x > b && x < w) ? v.T[x] : 0.f;
-                const float rf = a.scale * exp2_approx(Li + between);
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 f = *reinterpret_cast<const float4*>(&v.cf[32 * b + i]);
-                  pk[i / 2] = pack_bf16(s[i] * (f.x * rf), s[i + 1] * (f.y * rf));
-                  pk[i / 2 + 1] = pack_bf16(s[i + 2] * (f.z * rf), s[i + 3] * (f.w * rf));
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 L = *reinterpret_cast<const float4*>(&v.L[32 * b + i]);
-                  const float Lj[4] = {L.x, L.y, L.z, L.w};
-                  float p[4];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    p[e] = i + e <= lane ? s[i + e] * (a.scale * exp2_approx(Li - Lj[e])) : 0.f;
-                  pk[i / 2] = pack_bf16(p[0], p[1]);
-                  pk[i / 2 + 1] = pack_bf16(p[2], p[3]);
-                }
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t z = y[2 * m + e];
+                const float2 p = __fmul2_rn(make_float2(bf16_lo(z), bf16_hi(z)), ww);
+                const uint32_t h = pack_bf16(p.x, p.y);
+                hi[2 * m + e] = h;
+                lo[2 * m + e] = pack_bf16(p.x - bf16_lo(h), p.y - bf16_hi(h));
               }
             }
-            tmem_st16(row + 16 * b, pk);
+            if (tok0 + 16 > len) {
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const int q = pt + 8 * (m >> 1);
+                const uint32_t keep = (q < len ? 0xffffu : 0u) | (q + 1 < len ? 0xffff0000u : 0u);
+                hi[m] &= keep;
+                lo[m] &= keep;
+              }
+            }
+            const uint32_t dst = lanes + ((uint32_t)(16 * dh) << 16) + (uint32_t)(tok0 >> 1);
+            tmem_st_16x128b_x2(dst + kT_Vhi, hi);
+            tmem_st_16x128b_x2(dst + kT_Vlo, lo);
+            if ((x & 7) == 7 && len == C) {  // a half is done
+              tmem_wait_st();
+              tc_fence_before();
+              arrive(bVw + (x >> 3));
+            }
+          }
+          if (len < C) {
+            tmem_wait_st();
+            tc_fence_before();
+            named_sync(2, kGroup);  // the group has read the v tile
+#pragma unroll 1
+            for (int e = row; e < (C - len) * 16; e += kGroup) {
+              const uint32_t off = (uint32_t)((e >> 3) & 1) * kHalfTile +
+                                   (uint32_t)((len + (e >> 4)) * 128 + (e & 7) * 16);
+              *reinterpret_cast<uint4*>(sm + slot(tV, it) + off) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(sm + slot(tK, it) + off) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            arrive(bVw);
+            arrive(bVw + 1);
+          }
+          ++it;
+        }
+        arrive(bREmpty + (d & 1));
+      }
+    } else if (group == 1) {
+      // ------------------------------------------------------------ scores -> P
+      // Thread = token row, 16 keys at a time.  P (packed pairs) overwrites the scores'
+      // columns from the left, behind the scores being read.
+      const uint32_t col = lanes + kT_P;
+      int it = 0;
+#pragma unroll 1
+      for (int d = 0;; ++d) {
+        if (!wait_warp(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
+        const Rec& v = recs[d & 1];
+        const int len = v.len, flags = v.flags;
+        if (flags & kStop) break;
+        if (len > 0) {
+          if (!wait_warp(bQK, (uint32_t)it)) break;
+          tc_fence_after();
+          const float Li = v.L[row];
+          float upto = Li;  // decay exponent from the end of key block b to this token
+          float rf[3];
+#pragma unroll
+          for (int b = 2; b >= 0; --b) {
+            if (b < w) {
+              rf[b] = a.scale * exp2_approx(upto);
+              upto += v.T[b];
+            } else {
+              rf[b] = 0.f;
+            }
+          }
+#pragma unroll 1
+          for (int x = 0; x < 2 * w; ++x) {  // blocks left of the diagonal one
+            float s[16];
+            uint32_t pk[8];
+            tmem_ld16(col + 16 * x, s);
+            const float r = x < 2 ? rf[0] : (x < 4 ? rf[1] : rf[2]);
+            const float2 r2 = make_float2(r, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&v.cf[16 * x + i]);
+              const float2 p = __fmul2_rn(__fmul2_rn(make_float2(f.x, f.y), r2),
+                                          make_float2(s[i], s[i + 1]));
+              const float2 q = __fmul2_rn(__fmul2_rn(make_float2(f.z, f.w), r2),
+                                          make_float2(s[i + 2], s[i + 3]));
+              pk[i / 2] = pack_bf16(p.x, p.y);
+              pk[i / 2 + 1] = pack_bf16(q.x, q.y);
+            }
+            tmem_st8(col + 8 * x, pk);
+          }
+#pragma unroll 1
+          for (int x = 2 * w; x < 2 * w + 2; ++x) {  // the diagonal block
+            float s[16];
+            uint32_t pk[8];
+            tmem_ld16(col + 16 * x, s);
+            tmem_wait_ld();
+            const int j0 = 16 * x;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 L = *reinterpret_cast<const float4*>(&v.L[j0 + i]);
+              const float Lj[4] = {L.x, L.y, L.z, L.w};
+              float p[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                p[e] = j0 + i + e <= row ? s[i + e] * (a.scale * exp2_approx(Li - Lj[e])) : 0.f;
+              pk[i / 2] = pack_bf16(p[0], p[1]);
+              pk[i / 2 + 1] = pack_bf16(p[2], p[3]);
+            }
+            tmem_st8(col + 8 * x, pk);
+          }
+#pragma unroll 1
+          for (int x = 2 * w + 2; x < 8; ++x) {  // keys behind every token of this warp
+            const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            tmem_st8(col + 8 * x, z);
           }
           tmem_wait_st();
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(bP));
-            mbar_arrive(bar(bVEmpty + (it & 1)));
-          }
+          arrive(bP);
+          ++it;
         }
+        arrive(bREmpty + (d & 1));
       }
-    }
-  } else if (warp >= 12 && warp < 16) {
-    // ----------------------------------------------------------------- outputs
-    if (kOut) {
-      const int w = warp & 3, i0 = 32 * w + lane;
-      const uint32_t row = tmem + ((uint32_t)(32 * w) << 16);
+    } else if (group == 2) {
+      // --------------------------------------------------------------- outputs
+      // Thread = token row: O *= scale e^{G_i} between QS and PV; then the chunk goes to
+      // the q tile's slot for the copy out, a partial one (its rows end inside the tile)
+      // straight to memory.
+      const uint32_t col = lanes + kT_O;
       int it = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-        const Job j = get_job<kOut>(a, item);
-        for (int c = 0; c < j.chunks; ++c, ++it) {
-          const int len = min(C, j.tokens - c * C);
-          ok = wait_warp(bVFull + (it & 1), (uint32_t)(it >> 1));
-          if (!ok) break;
-          const Vec& v = vecs[it & 1];
-          float x = v.L[i0];
+#pragma unroll 1
+      for (int d = 0;; ++d) {
+        if (!wait_warp(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
+        const Rec& v = recs[d & 1];
+        const int len = v.len, flags = v.flags, h = v.h, tok = v.tok;
+        float e0 = v.L[row];
 #pragma unroll
-          for (int b = 0; b < 3; ++b) x += b < w ? v.T[b] : 0.f;
-          const float E = a.scale * exp2_approx(x);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(bVEmpty + (it & 1)));
-          ok = wait_warp(bPV, (uint32_t)it);
-          if (!ok) break;
-          tc_fence_after();
-          __nv_bfloat16* orow = a.o + ((j.t0 + (int64_t)c * C + i0) * a.H + j.h) * D;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            float qs[32], pv[32];
-            tmem_ld32(row + kT_QS + 32 * p, qs);
-            tmem_ld32(row + kT_PV + 32 * p, pv);
-            tmem_wait_ld();
-            if (p == 3) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(bO));
-            }
-            if (i0 < len) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t y[4];
-#pragma unroll
-                for (int f = 0; f < 4; ++f)
-                  y[f] = pack_bf16(fmaf(E, qs[e + 2 * f], pv[e + 2 * f]),
-                                   fmaf(E, qs[e + 2 * f + 1], pv[e + 2 * f + 1]));
-                *reinterpret_cast<uint4*>(orow + 32 * p + e) = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-            }
-          }
-        }
-      }
-    }
-  } else if (warp >= 16) {
-    // ------------------------------------------------------------------- state
-    // Thread = value row.  Before chunk c: the row to bf16 for QS (and times e^{G_C} back
-    // into tensor memory for KV); the first chunk takes the initial state instead.
-    const int dv = t - (128 + 3 * kGroup);
-    const uint32_t row = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kT_S;
-    uint8_t* sb = sm + kSbOff;
-    int it = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const Job j = get_job<kOut>(a, item);
-      float decay = 0.f;
-      const float* init = j.init ? j.init + dv * D : nullptr;
-      for (int c = 0; c < j.chunks; ++c, ++it) {
-        ok = wait_warp(bVFull + (it & 1), (uint32_t)(it >> 1)) &&
-             (c == 0 || wait_warp(bKV, (uint32_t)it - 1));
-        if (!ok) break;
+        for (int b = 0; b < 3; ++b) e0 += b < w ? v.T[b] : 0.f;
+        arrive(bREmpty + (d & 1));
+        if (flags & kStop) break;
+        if (len <= 0) continue;
+        const float e1 = a.scale * exp2_approx(e0);
+        const float2 e2 = make_float2(e1, e1);
+        if (!wait_warp(bQS, (uint32_t)it)) break;
         tc_fence_after();
-        const Vec& v = vecs[it & 1];
-        const float tot = (v.T[0] + v.T[1]) + (v.T[2] + v.T[3]);
-        decay += tot;
-        const float gam = exp2_approx(tot);
-#pragma unroll
+#pragma unroll 1
         for (int p = 0; p < 4; ++p) {
-          float s[32];
-          if (c > 0) {
-            tmem_ld32(row + 32 * p, s);
-            tmem_wait_ld();
-          } else {
+          float y[32];
+          tmem_ld32(col + 32 * p, y);
+          tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 x = init ? *reinterpret_cast<const float4*>(init + 32 * p + i)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-              s[i] = x.x; s[i + 1] = x.y; s[i + 2] = x.z; s[i + 3] = x.w;
-            }
+          for (int i = 0; i < 32; i += 2) {
+            const float2 z = __fmul2_rn(make_float2(y[i], y[i + 1]), e2);
+            y[i] = z.x;
+            y[i + 1] = z.y;
           }
-          if (kOut) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 y = make_uint4(pack_bf16(s[8 * e], s[8 * e + 1]),
-                                         pack_bf16(s[8 * e + 2], s[8 * e + 3]),
-                                         pack_bf16(s[8 * e + 4], s[8 * e + 5]),
-                                         pack_bf16(s[8 * e + 6], s[8 * e + 7]));
-              *reinterpret_cast<uint4*>(sb + sw128_chunk(D, dv, 4 * p + e)) = y;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] *= gam;
-          tmem_st32(row + 32 * p, s);
+          tmem_st32(col + 32 * p, y);
         }
         tmem_wait_st();
         tc_fence_before();
-        if (kOut) fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(bS));
-          mbar_arrive(bar(bVEmpty + (it & 1)));
-        }
-      }
-      if (!ok) break;
-      if (j.chunks > 0) {
-        ok = wait_warp(bKV, (uint32_t)it - 1);
-        if (!ok) break;
+        arrive(bOs);
+        if (!wait_warp(bPV, (uint32_t)it)) break;
         tc_fence_after();
-      }
-      if (j.fin) {
+        uint8_t* stage = sm + slot(tQ, it) + row * 128;
+        __nv_bfloat16* orow = a.o + ((int64_t)(tok + row) * a.H + h) * D;
 #pragma unroll 1
         for (int p = 0; p < 4; ++p) {
-          float s[32];
-          if (j.chunks > 0) {
-            tmem_ld32(row + 32 * p, s);
-            tmem_wait_ld();
-          }
+          float y[32];
+          tmem_ld32(col + 32 * p, y);
+          tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float4 y = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-            if (j.chunks == 0)
-              y = init ? *reinterpret_cast<const float4*>(init + 32 * p + i)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-            *reinterpret_cast<float4*>(j.fin + dv * D + 32 * p + i) = y;
+          for (int e = 0; e < 4; ++e) {
+            const uint4 z = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]),
+                                       pack_bf16(y[8 * e + 2], y[8 * e + 3]),
+                                       pack_bf16(y[8 * e + 4], y[8 * e + 5]),
+                                       pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+            if (len == C)
+              *reinterpret_cast<uint4*>(stage + (p >> 1) * kHalfTile +
+                                        (((4 * (p & 1) + e) ^ (row & 7)) << 4)) = z;
+            else if (row < len)
+              *reinterpret_cast<uint4*>(orow + 32 * p + 8 * e) = z;
           }
         }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        arrive(bO);
+        arrive(bOut);
+        ++it;
       }
-      if (j.decay && dv == 0) *j.decay = exp2_approx(decay);
+    } else {
+      // ----------------------------------------------------------------- state
+      // Thread = value row.  Before a chunk: the row to bf16 for QS, and times e^{G_C} back
+      // into tensor memory for KV; a job's first chunk takes its initial state instead.
+      const uint32_t col = lanes + kT_S;
+      uint8_t* sb = sm + kSbOff + row * 128;
+      int it = 0;
+#pragma unroll 1
+      for (int d = 0;; ++d) {
+        if (!wait_warp(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
+        const Rec& v = recs[d & 1];
+        const int len = v.len, flags = v.flags;
+        const float* init = v.init;
+        float* fin = (flags & kLast) ? v.fin : nullptr;
+        float* decay = (flags & kLast) ? v.decay : nullptr;
+        const float sofar = v.sofar, gam = exp2_approx(v.total);
+        arrive(bREmpty + (d & 1));
+        if (flags & kStop) break;
+        const bool first = (flags & kFirst) != 0;
+        if (decay && row == 0) *decay = exp2_approx(sofar);
+        if (init) init += row * D;
+        if (fin) fin += row * D;
+        if (len > 0) {
+          // (a job's end waits for the state, so its KV is done where the next one begins)
+          if (!first && !wait_warp(bKV, (uint32_t)it - 1)) break;
+          tc_fence_after();
+        }
+        // pass 0: before the chunk; pass 1: the final state, after its KV
+#pragma unroll 1
+        for (int pass = len > 0 ? 0 : 1; pass < 2; ++pass) {
+          if (pass == 1) {
+            if (!(flags & kLast)) break;
+            if (len > 0) {
+              if (!wait_warp(bKV, (uint32_t)it)) break;
+              tc_fence_after();
+            }
+            if (!fin) break;
+          }
+          const bool from_init = pass == 0 ? first : len <= 0;
+#pragma unroll 1
+          for (int p = 0; p < 4; ++p) {
+            float s[32];
+            if (from_init) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 x = init ? *reinterpret_cast<const float4*>(init + 32 * p + i)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                s[i] = x.x; s[i + 1] = x.y; s[i + 2] = x.z; s[i + 3] = x.w;
+              }
+            } else {
+              tmem_ld32(col + 32 * p, s);
+              tmem_wait_ld();
+            }
+            if (pass == 1) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(fin + 32 * p + i) =
+                    make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+            } else {
+              if (kOut) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint4 y = make_uint4(pack_bf16(s[8 * e], s[8 * e + 1]),
+                                             pack_bf16(s[8 * e + 2], s[8 * e + 3]),
+                                             pack_bf16(s[8 * e + 4], s[8 * e + 5]),
+                                             pack_bf16(s[8 * e + 6], s[8 * e + 7]));
+                  *reinterpret_cast<uint4*>(sb + (p >> 1) * kHalfTile +
+                                            (((4 * (p & 1) + e) ^ (row & 7)) << 4)) = y;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 z = __fmul2_rn(make_float2(s[i], s[i + 1]), make_float2(gam, gam));
+                s[i] = z.x;
+                s[i + 1] = z.y;
+              }
+              tmem_st32(col + 32 * p, s);
+            }
+          }
+          if (pass == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            if (kOut) fence_proxy_async_smem();
+            arrive(bS);
+          }
+        }
+        if (*abort_flag) break;
+        if (len > 0) ++it;
+      }
     }
   }
   tc_fence_before();
@@ -809,7 +1001,7 @@ cudaError_t run(const CUtensorMap* tm, const LinArgs& a, int64_t items, const ch
   const int sms = sm_count();
   ProfScope prof_scope(name, s);
   lin_tc_kernel<kOut><<<(unsigned)(items < sms ? items : sms), kThreads, kSmemBytes, s>>>(
-      tm[0], tm[1], tm[2], a);
+      tm[0], tm[1], tm[2], tm[3], a);
   return cudaGetLastError();
 }
 
@@ -835,6 +1027,7 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
                              int g_head, float scale, const float* h0, const int32_t* cu,
                              int64_t T_per_seq, void* o, float* hT, int64_t n_tokens, int n_seqs,
                              int H, int Hk, int seg_chunks, void* ws, int* err, cudaStream_t s) {
+  if (!err) return cudaErrorInvalidSymbol;  // the kernels report through it
   LinArgs a{};
   a.g = g;
   a.g_head = g_head;
@@ -849,13 +1042,14 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
   a.o = static_cast<__nv_bfloat16*>(o);
   a.hT = hT;
   a.err = err;
-  CUtensorMap tm[3];
+  CUtensorMap tm[4];
   memset(tm, 0, sizeof(tm));
   cudaError_t e = cudaSuccess;
   if (n_tokens > 0) {  // with no tokens there are no chunks to copy
     e = encode_tiles(&tm[0], q, Hk, n_tokens);
     if (e == cudaSuccess) e = encode_tiles(&tm[1], k, Hk, n_tokens);
     if (e == cudaSuccess) e = encode_tiles(&tm[2], v, H, n_tokens);
+    if (e == cudaSuccess) e = encode_tiles(&tm[3], o, H, n_tokens);
     if (e != cudaSuccess) return e;
   }
   if (seg_chunks <= 0) return run<true>(tm, a, (int64_t)n_seqs * H, "kda_linear_tc", s);
