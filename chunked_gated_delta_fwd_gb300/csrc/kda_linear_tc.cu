@@ -208,6 +208,64 @@ __device__ __forceinline__ Job get_job(const LinArgs& a, int item) {
   return j;
 }
 
+// The issuing warps run their control flow with all lanes, so that descriptors, addresses
+// and loop counters stay in the warp's uniform registers, where these instructions take
+// them from; `lead` (1 on one lane) predicates the instruction alone.  (Issued from inside
+// a one-lane branch every operand was moved over first: 110 to 250 clocks an MMA that the
+// tensor pipe finishes in 64.)
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t ad, uint64_t bd,
+                                       uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t at, uint64_t bd,
+                                       uint32_t idesc) {  // accumulates
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(at), "l"(bd), "r"(idesc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+// Both 64-channel boxes of a tile, completing on `bar`.
+__device__ __forceinline__ void load_tile(uint32_t lead, uint32_t dst, const void* tmap, int head,
+                                          int tok, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b64 st;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 st, [%5], %7;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%2, {0, %3, %4}], [%5];\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%1], [%2, {64, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "r"(dst + kHalfTile), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(head), "r"(tok), "r"(bar),
+      "r"(lead), "r"(kTileBytes)
+      : "memory");
+}
+
 // Four transposed 8 x 8 bf16 matrices; lane l gives the address of row l % 8 of matrix l / 8
 // and gets, of each, column l / 4 of rows 2 (l % 4) and + 1 as one pair.
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -291,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- jobs, decay vectors, copies in
     const int items = job_count<kOut>(a);
     constexpr int kTiles = kOut ? 3 : 2;
+    const uint32_t lead = elect_lane();
     int it = 0, d = 0, m = 0;  // chunks, records, tiles copied
     bool ok = true;
     for (int item = blockIdx.x; ok; item += gridDim.x) {
@@ -355,30 +414,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         arrive(bRFull + (d & 1));
         if (len > 0) {
-          if (lane == 0) {
 #pragma unroll 1
-            for (int i = 0; i < 3; i += kOut ? 1 : 2) {
-              if (it >= 2 && !wait(empty(i, it), (uint32_t)(it >> 1) - 1)) {
-                ok = false;
-                break;
-              }
-              const void* tm = i == tK ? &tm_k : (i == tQ ? &tm_q : &tm_v);
-              const int head = i == tV ? j.h : kv_head;
-              const uint32_t dst = base + slot(i, it);
-              mbar_arrive_expect_tx(bar(full(i, it)), kTileBytes);
-              tma_load_3d(dst, tm, 0, head, tok, bar(full(i, it)));
-              tma_load_3d(dst + kHalfTile, tm, 64, head, tok, bar(full(i, it)));
-              ++m;
-            }
+          for (int i = 0; i < 3; i += kOut ? 1 : 2) {
+            ok = it < 2 || wait_warp(empty(i, it), (uint32_t)(it >> 1) - 1);
+            if (!ok) break;
+            const void* tm = i == tK ? &tm_k : (i == tQ ? &tm_q : &tm_v);
+            load_tile(lead, base + slot(i, it), tm, i == tV ? j.h : kv_head, tok, bar(full(i, it)));
+            ++m;
           }
-          ++it;
-          ok = __all_sync(0xffffffffu, ok) != 0;
           if (!ok) break;
+          ++it;
         }
       }
       if (stop) break;
     }
-    if (lane == 0 && *abort_flag) {  // copies in flight must land before the CTA exits
+    if (*abort_flag) {  // copies in flight must land before the CTA exits
 #pragma unroll 1
       for (int x = max(0, m - 2 * kTiles); x < m; ++x)
         mbar_wait(bar(full(kOut ? x % 3 : 2 * (x % 2), x / kTiles)),
@@ -388,96 +438,94 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------------- MMAs
     // Order a chunk: QS, KV, PV, then QK of the next chunk.  KV goes as early as its
     // operands allow: the state group works on its result while PV and QK run.
-    if (lane == 0) {
-      const uint32_t id_kk = idesc_bf16_mn(C, C, 0, 0);  // both operands K-major
-      const uint32_t id_kn = idesc_bf16_mn(C, D, 0, 1);  // B MN-major
-      bool ok = true, any = false;
-      int d = 0;
-      // D = A B^T over 128 channels, both tiles K-major
-      auto mma_kk = [&](uint32_t dst, uint32_t at, uint32_t bt) {
-        uint64_t da = kmajor_desc(at, C, 0), db = kmajor_desc(bt, C, 0);
+    const uint32_t lead = elect_lane();
+    const uint32_t id_kk = idesc_bf16_mn(C, C, 0, 0);  // both operands K-major
+    const uint32_t id_kn = idesc_bf16_mn(C, D, 0, 1);  // B MN-major
+    bool ok = true, any = false;
+    int d = 0;
+    // D = A B^T over 128 channels, both tiles K-major
+    auto mma_kk = [&](uint32_t dst, uint32_t at, uint32_t bt) {
+      const uint64_t da = kmajor_desc(at, C, 0), db = kmajor_desc(bt, C, 0);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const uint32_t off = (uint32_t)(s >> 2) * kHalfTile + (uint32_t)(s & 3) * 32u;
+        mma_ss(lead, dst, desc_advance(da, off), desc_advance(db, off), id_kk, s > 0);
+      }
+    };
 #pragma unroll 1
-        for (int s = 0; s < 8; s += 2) {
-          mma_bf16(dst, da, db, id_kk, s > 0);
-          mma_bf16(dst, desc_advance(da, 32), desc_advance(db, 32), id_kk, 1u);
-          const uint32_t step = s == 2 ? kHalfTile - 64u : 64u;  // on to the next channel block
-          da = desc_advance(da, step);
-          db = desc_advance(db, step);
+    for (int it = -1; ok; ++it) {
+      const uint32_t par = (uint32_t)it;
+      if (it >= 0) {
+        ok = wait_warp(bS, par) && (!kOut || it == 0 || wait_warp(bO, par - 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (kOut) {
+          mma_kk(tmem + kT_O, base + slot(tQ, it), base + kSbOff);
+          commit_to(lead, bar(bQS));
+        } else {
+          ok = wait_warp(full(tK, it), par >> 1);
+          if (!ok) break;
         }
-      };
+        any = true;
+        uint64_t dk = mnmajor_desc_lbo(base + slot(tK, it), kHalfTile, 1024, 0);
+        uint32_t va = tmem + kT_Vhi;
 #pragma unroll 1
-      for (int it = -1; ok; ++it) {
-        const uint32_t par = (uint32_t)it;
-        if (it >= 0) {
-          ok = wait(bS, par) && (!kOut || it == 0 || wait(bO, par - 1));
+        for (int hf = 0; hf < 2; ++hf) {  // tokens 0-63, 64-127
+          ok = wait_warp(bVw + hf, par);
           if (!ok) break;
           tc_fence_after();
-          if (kOut) {
-            mma_kk(tmem + kT_O, base + slot(tQ, it), base + kSbOff);
-            mma_commit(bar(bQS));
-          } else {
-            ok = wait(full(tK, it), par >> 1);
-            if (!ok) break;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint64_t b = desc_advance(dk, (uint32_t)s * 2048u);
+            mma_ts(lead, tmem + kT_S, va + (kT_Vlo - kT_Vhi) + 8 * s, b, id_kn);
+            mma_ts(lead, tmem + kT_S, va + 8 * s, b, id_kn);
           }
-          any = true;
-          uint64_t dk = mnmajor_desc_lbo(base + slot(tK, it), kHalfTile, 1024, 0);
-          uint32_t va = tmem + kT_Vhi;
-#pragma unroll 1
-          for (int s = 0; s < 8; ++s) {  // tokens 0-63, 64-127
-            if ((s & 3) == 0) {
-              ok = wait(bVw + (s >> 2), par);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            mma_bf16_ta(tmem + kT_S, va + (kT_Vlo - kT_Vhi), dk, id_kn, 1u);
-            mma_bf16_ta(tmem + kT_S, va, dk, id_kn, 1u);
-            dk = desc_advance(dk, 2048);
-            va += 8;
-          }
-          if (!ok) break;
-          mma_commit(bar(bKV));
-          mma_commit(bar(empty(tK, it)));
-          if (kOut) {
-            ok = wait(bP, par) && wait(bOs, par);
-            if (!ok) break;
-            tc_fence_after();
-            uint64_t dv = mnmajor_desc_lbo(base + slot(tV, it), kHalfTile, 1024, 0);
-#pragma unroll 1
-            for (int s = 0; s < 8; s += 2) {
-              mma_bf16_ta(tmem + kT_O, tmem + kT_P + 8 * s, dv, id_kn, 1u);
-              mma_bf16_ta(tmem + kT_O, tmem + kT_P + 8 * s + 8, desc_advance(dv, 2048), id_kn, 1u);
-              dv = desc_advance(dv, 4096);
-            }
-            mma_commit(bar(bPV));
-          }
-          mma_commit(bar(empty(tV, it)));
-        }
-        int len = 0;  // the next record that is a chunk
-        while (len <= 0) {
-          ok = wait(bRFull + (d & 1), (uint32_t)(d >> 1));
-          if (!ok) break;
-          len = recs[d & 1].len;
-          const int flags = recs[d & 1].flags;
-          mbar_arrive(bar(bREmpty + (d & 1)));
-          ++d;
-          if (flags & kStop) ok = false;
-          if (!ok) break;
+          dk = desc_advance(dk, 4 * 2048);
+          va += 32;
         }
         if (!ok) break;
+        commit_to(lead, bar(bKV));
+        commit_to(lead, bar(empty(tK, it)));
         if (kOut) {
-          const uint32_t ph = (uint32_t)((it + 1) >> 1);
-          ok = wait(full(tK, it + 1), ph) && wait(full(tQ, it + 1), ph);
+          ok = wait_warp(bP, par) && wait_warp(bOs, par);
           if (!ok) break;
           tc_fence_after();
-          mma_kk(tmem + kT_P, base + slot(tQ, it + 1), base + slot(tK, it + 1));
-          mma_commit(bar(bQK));
-          any = true;
+          const uint64_t dv = mnmajor_desc_lbo(base + slot(tV, it), kHalfTile, 1024, 0);
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_ts(lead, tmem + kT_O, tmem + kT_P + 8 * s, desc_advance(dv, (uint32_t)s * 2048u),
+                   id_kn);
+          commit_to(lead, bar(bPV));
         }
+        commit_to(lead, bar(empty(tV, it)));
       }
-      if (*abort_flag && any) {  // drain MMAs in flight
-        mma_commit(bar(bDrain));
-        mbar_wait(bar(bDrain), 0, a.err);
+      int len = 0;  // the next record that is a chunk
+#pragma unroll 1
+      while (len <= 0) {
+        ok = wait_warp(bRFull + (d & 1), (uint32_t)(d >> 1));
+        if (!ok) break;
+        len = recs[d & 1].len;
+        const int flags = recs[d & 1].flags;
+        arrive(bREmpty + (d & 1));
+        ++d;
+        ok = __all_sync(0xffffffffu, (flags & kStop) == 0) != 0;
+        if (!ok) break;
+        len = __shfl_sync(0xffffffffu, len, 0);
       }
+      if (!ok) break;
+      if (kOut) {
+        const uint32_t ph = (uint32_t)((it + 1) >> 1);
+        ok = wait_warp(full(tK, it + 1), ph) && wait_warp(full(tQ, it + 1), ph);
+        if (!ok) break;
+        tc_fence_after();
+        mma_kk(tmem + kT_P, base + slot(tQ, it + 1), base + slot(tK, it + 1));
+        commit_to(lead, bar(bQK));
+        any = true;
+      }
+    }
+    if (*abort_flag && any) {  // drain MMAs in flight
+      commit_to(lead, bar(bDrain));
+      mbar_wait(bar(bDrain), 0, a.err);
     }
   } else if (warp == 3) {
     // ----------------------------------------------------------------- copies out
@@ -540,42 +588,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t vt = base + slot(tV, it) + (uint32_t)(w >> 1) * kHalfTile;
 #pragma unroll 1
-          for (int x = 0; x < 16; ++x) {  // 16 tokens x 16 value rows: tokens outer
-            const int tok0 = 16 * (x >> 1), dh = x & 1;
-            const int tok = tok0 + mrow, ch = 4 * (w & 1) + 2 * dh + mdv;
-            uint32_t y[4], hi[4], lo[4];
-            ldmatrix4_trans(vt + (uint32_t)(tok * 128 + ((ch ^ (tok & 7)) << 4)), y);
+          for (int x = 0; x < 8; ++x) {  // 16 tokens x 32 value rows
+            const int tok0 = 16 * x, tok = tok0 + mrow;
+            uint32_t y[2][4];
+#pragma unroll
+            for (int dh = 0; dh < 2; ++dh)
+              ldmatrix4_trans(vt + (uint32_t)(tok * 128 +
+                                              (((4 * (w & 1) + 2 * dh + mdv) ^ (tok & 7)) << 4)),
+                              y[dh]);
             const int pt = tok0 + 2 * (lane & 3);
             const float f = v.aft[tok0 >> 5];
+            float2 ww[2];  // weights of this lane's token pairs, eight tokens apart
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {  // eight tokens each
-              float2 ww = *reinterpret_cast<const float2*>(&v.cf[pt + 8 * m]);
-              ww = __fmul2_rn(ww, make_float2(f, f));
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t z = y[2 * m + e];
-                const float2 p = __fmul2_rn(make_float2(bf16_lo(z), bf16_hi(z)), ww);
-                const uint32_t h = pack_bf16(p.x, p.y);
-                hi[2 * m + e] = h;
-                lo[2 * m + e] = pack_bf16(p.x - bf16_lo(h), p.y - bf16_hi(h));
-              }
-            }
+            for (int m = 0; m < 2; ++m)
+              ww[m] = __fmul2_rn(*reinterpret_cast<const float2*>(&v.cf[pt + 8 * m]),
+                                 make_float2(f, f));
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
             if (tok0 + 16 > len) {
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const int q = pt + 8 * (m >> 1);
-                const uint32_t keep = (q < len ? 0xffffu : 0u) | (q + 1 < len ? 0xffff0000u : 0u);
-                hi[m] &= keep;
-                lo[m] &= keep;
-              }
+              for (int m = 0; m < 2; ++m)
+                keep[m] = (pt + 8 * m < len ? 0xffffu : 0u) | (pt + 8 * m + 1 < len ? 0xffff0000u : 0u);
             }
-            const uint32_t dst = lanes + ((uint32_t)(16 * dh) << 16) + (uint32_t)(tok0 >> 1);
-            tmem_st_16x128b_x2(dst + kT_Vhi, hi);
-            tmem_st_16x128b_x2(dst + kT_Vlo, lo);
-            if ((x & 7) == 7 && len == C) {  // a half is done
+#pragma unroll
+            for (int dh = 0; dh < 2; ++dh) {
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const uint32_t z = y[dh][m];
+                const float2 p = __fmul2_rn(make_float2(bf16_lo(z), bf16_hi(z)), ww[m >> 1]);
+                const uint32_t h = pack_bf16(p.x, p.y);
+                hi[m] = h & keep[m >> 1];
+                lo[m] = pack_bf16(p.x - bf16_lo(h), p.y - bf16_hi(h)) & keep[m >> 1];
+              }
+              const uint32_t dst = lanes + ((uint32_t)(16 * dh) << 16) + (uint32_t)(tok0 >> 1);
+              tmem_st_16x128b_x2(dst + kT_Vhi, hi);
+              tmem_st_16x128b_x2(dst + kT_Vlo, lo);
+            }
+            if ((x & 3) == 3 && len == C) {  // a half is done
               tmem_wait_st();
               tc_fence_before();
-              arrive(bVw + (x >> 3));
+              arrive(bVw + (x >> 2));
             }
           }
           if (len < C) {
