@@ -111,19 +111,28 @@ constexpr uint32_t kT_S = 0, kT_P = 128, kT_O = 256, kT_Vhi = 384, kT_Vlo = 448;
 
 constexpr int kGroup = 128;
 constexpr int kThreads = 128 + 4 * kGroup;
-// A wait gives up after this many polls (each suspends for up to about a microsecond).
-constexpr uint32_t kPolls = 1u << 24;
+// A wait gives up after this many polls, each of which suspends for up to a microsecond.
+constexpr uint32_t kPolls = 1u << 22, kPollNs = 1000;
 
-__device__ __forceinline__ bool wait_poll(uint32_t bar, uint32_t parity, int* err,
-                                          volatile int* abort_flag) {
-#pragma unroll 1
-  for (uint32_t n = 0; n < kPolls; ++n) {
-    if (mbar_try_wait(bar, parity & 1u)) return true;
-    if (*abort_flag) return false;
-  }
-  atomicExch(err, kDevErrTimeout);
-  *abort_flag = 1;
-  return false;
+// Waits for the phase of `parity` to complete; 0 if it has not after kPolls polls.  (The loop
+// is all there is to a wait site: a role whose wait fails reports that where it ends.)
+__device__ __forceinline__ uint32_t wait_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n\t"
+      "POLL:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra POLL;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity & 1u), "n"(kPolls), "n"(kPollNs)
+      : "memory");
+  return ok;
 }
 
 struct LinArgs {
@@ -274,12 +283,15 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                : "r"(addr)
                : "memory");
 }
-// 16 lanes x 8 columns: of each four columns, registers 2i and 2i + 1 of lane l go to TMEM
+// 16 lanes x 32 columns: of each four columns, registers 2i and 2i + 1 of lane l go to TMEM
 // lanes l / 4 and l / 4 + 8, column 4 i + l % 4.
-__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&v)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3])
-               : "memory");
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 // 32 lanes x 8 columns store.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
@@ -312,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars = base + kBarOff;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBarOff + kBarBytes);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kBarOff + kBarBytes + 8);
   Rec* recs = reinterpret_cast<Rec*>(sm + kVecOff);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  bool done = false;  // this role has come to the end of the work
 
   if (t == 0) {
     // arrivals a phase: copies, commits and single threads 1, groups one a warp
@@ -323,7 +335,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool rec = i == bREmpty || i == bREmpty + 1;  // every warp that reads records
       mbar_init(bar(i), rec ? (kOut ? 18 : 9) : (group ? 4 : 1));
     }
-    *abort_flag = 0;
     mbar_fence_init();
   }
   if (warp == 3) tmem_alloc(smem_addr(tmem_slot), 512);
@@ -332,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  auto wait = [&](int b, uint32_t parity) { return wait_poll(bar(b), parity, a.err, abort_flag); };
+  auto wait = [&](int b, uint32_t parity) { return wait_poll(bar(b), parity) != 0; };
   // the same for a whole warp: one outcome, so that warp-wide instructions stay together
   auto wait_warp = [&](int b, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(b, parity)) != 0;
@@ -346,94 +357,126 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto slot = [](int tile, int it) { return (uint32_t)(3 * (it & 1) + tile) * kTileBytes; };
 
   if (warp == 0) {
-    // ------------------------------------------------- jobs, decay vectors, copies in
-    const int items = job_count<kOut>(a);
+    // ------------------------------------------------------------------ copies in
     constexpr int kTiles = kOut ? 3 : 2;
+    const int items = job_count<kOut>(a);
     const uint32_t lead = elect_lane();
-    int it = 0, d = 0, m = 0;  // chunks, records, tiles copied
+    int it = 0, m = 0;  // chunks, tiles copied
     bool ok = true;
-    for (int item = blockIdx.x; ok; item += gridDim.x) {
-      const bool stop = item >= items;
-      Job j{};
-      if (!stop) j = get_job<kOut>(a, item);
-      float sofar = 0.f;
+#pragma unroll 1
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const Job j = get_job<kOut>(a, item);
       const int kv_head = j.h / a.rep;
 #pragma unroll 1
-      for (int c = 0; c < max(j.chunks, 1); ++c, ++d) {  // a job without tokens is one record
-        const int len = min(C, j.tokens - c * C);
+      for (int c = 0; c < j.chunks && ok; ++c, ++it) {
         const int tok = (int)(j.t0 + (int64_t)c * C);
-        float g[4], u[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int r = 32 * b + lane;
-          g[b] = 0.f;
-          if (r < len)
-            g[b] = __ldg(a.g + (a.g_head ? (int64_t)j.h : (int64_t)(tok + r) * a.H + j.h));
-        }
-        ok = d < 2 || wait_warp(bREmpty + (d & 1), (uint32_t)(d >> 1) - 1);
-        if (!ok) break;
-        Rec& v = recs[d & 1];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          g[b] = (g[b] < kMinG ? kMinG : g[b]) * kLog2e;  // NaN stays NaN
-          u[b] = __shfl_down_sync(0xffffffffu, g[b], 1);
-          if (lane == 31) u[b] = 0.f;
-        }
 #pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float x = __shfl_up_sync(0xffffffffu, g[b], o);
-            const float y = __shfl_down_sync(0xffffffffu, u[b], o);
-            if (lane >= o) g[b] += x;
-            if (lane + o < 32) u[b] += y;
-          }
-        float after = 0.f;
-#pragma unroll
-        for (int b = 3; b >= 0; --b) {
-          v.L[32 * b + lane] = g[b];
-          v.cf[32 * b + lane] = exp2_approx(u[b]);
-          const float T = __shfl_sync(0xffffffffu, g[b], 31);
-          if (lane == 0) {
-            v.T[b] = T;
-            v.aft[b] = exp2_approx(after);
-          }
-          after += T;
-        }
-        sofar += after;
-        if (lane == 0) {
-          v.init = j.init;
-          v.fin = j.fin;
-          v.decay = j.decay;
-          v.tok = tok;
-          v.len = len;
-          v.h = j.h;
-          v.flags = stop ? kStop : ((c == 0 ? kFirst : 0) | (c + 1 >= j.chunks ? kLast : 0));
-          v.total = after;
-          v.sofar = sofar;
-        }
-        arrive(bRFull + (d & 1));
-        if (len > 0) {
-#pragma unroll 1
-          for (int i = 0; i < 3; i += kOut ? 1 : 2) {
-            ok = it < 2 || wait_warp(empty(i, it), (uint32_t)(it >> 1) - 1);
-            if (!ok) break;
-            const void* tm = i == tK ? &tm_k : (i == tQ ? &tm_q : &tm_v);
-            load_tile(lead, base + slot(i, it), tm, i == tV ? j.h : kv_head, tok, bar(full(i, it)));
-            ++m;
-          }
+        for (int i = 0; i < 3; i += kOut ? 1 : 2) {
+          ok = it < 2 || wait_warp(empty(i, it), (uint32_t)(it >> 1) - 1);
           if (!ok) break;
-          ++it;
+          const void* tm = i == tK ? &tm_k : (i == tQ ? &tm_q : &tm_v);
+          load_tile(lead, base + slot(i, it), tm, i == tV ? j.h : kv_head, tok, bar(full(i, it)));
+          ++m;
         }
       }
-      if (stop) break;
     }
-    if (*abort_flag) {  // copies in flight must land before the CTA exits
+    done = ok;
+    if (!ok) {  // copies in flight must land before the CTA exits
 #pragma unroll 1
       for (int x = max(0, m - 2 * kTiles); x < m; ++x)
-        mbar_wait(bar(full(kOut ? x % 3 : 2 * (x % 2), x / kTiles)),
-                  (uint32_t)(x / kTiles >> 1) & 1u, a.err);
+        wait(full(kOut ? x % 3 : 2 * (x % 2), x / kTiles), (uint32_t)(x / kTiles >> 1));
     }
+  } else if (warp == 2) {
+    // --------------------------------------------------------------------- records
+    // One a chunk (a job without tokens is one record, the end of the work another); the
+    // next chunk's g is on its way while this one's sums are formed.
+    const int items = job_count<kOut>(a);
+    int d = 0;
+    bool ok = true;
+    float gn[4];
+    auto fetch = [&](const Job& j, int c) {
+      const int len = j.tokens - c * C;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int r = 32 * b + lane;
+        gn[b] = 0.f;
+        if (r < len)
+          gn[b] = __ldg(a.g + (a.g_head ? (int64_t)j.h : (j.t0 + (int64_t)(c * C + r)) * a.H + j.h));
+      }
+    };
+    int item = blockIdx.x, c = 0;
+    float sofar = 0.f;
+    Job j{};
+    bool stop = item >= items;
+    if (!stop) j = get_job<kOut>(a, item);
+    fetch(j, 0);
+#pragma unroll 1
+    for (;; ++d) {
+      // this record's job and g; then on to the next chunk or job, whose g is fetched here
+      const Job jc = j;
+      const int cc = c;
+      const bool last = cc + 1 >= jc.chunks, end = stop;
+      float g[4], u[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) g[b] = gn[b];
+      if (!end) {
+        if (last) {
+          item += gridDim.x;
+          c = 0;
+          stop = item >= items;
+          j = Job{};
+          if (!stop) j = get_job<kOut>(a, item);
+        } else {
+          ++c;
+        }
+        fetch(j, c);
+      }
+      ok = d < 2 || wait_warp(bREmpty + (d & 1), (uint32_t)(d >> 1) - 1);
+      if (!ok) break;
+      Rec& v = recs[d & 1];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        g[b] = (g[b] < kMinG ? kMinG : g[b]) * kLog2e;  // NaN stays NaN
+        u[b] = __shfl_down_sync(0xffffffffu, g[b], 1);
+        if (lane == 31) u[b] = 0.f;
+      }
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float x = __shfl_up_sync(0xffffffffu, g[b], o);
+          const float y = __shfl_down_sync(0xffffffffu, u[b], o);
+          if (lane >= o) g[b] += x;
+          if (lane + o < 32) u[b] += y;
+        }
+      float after = 0.f;
+#pragma unroll
+      for (int b = 3; b >= 0; --b) {
+        v.L[32 * b + lane] = g[b];
+        v.cf[32 * b + lane] = exp2_approx(u[b]);
+        const float T = __shfl_sync(0xffffffffu, g[b], 31);
+        if (lane == 0) {
+          v.T[b] = T;
+          v.aft[b] = exp2_approx(after);
+        }
+        after += T;
+      }
+      sofar = cc == 0 ? after : sofar + after;
+      if (lane == 0) {
+        v.init = jc.init;
+        v.fin = jc.fin;
+        v.decay = jc.decay;
+        v.tok = (int)(jc.t0 + (int64_t)cc * C);
+        v.len = min(C, jc.tokens - cc * C);
+        v.h = jc.h;
+        v.flags = end ? kStop : ((cc == 0 ? kFirst : 0) | (last ? kLast : 0));
+        v.total = after;
+        v.sofar = sofar;
+      }
+      arrive(bRFull + (d & 1));
+      if (end) break;
+    }
+    done = ok;
   } else if (warp == 1) {
     // -------------------------------------------------------------------- MMAs
     // Order a chunk: QS, KV, PV, then QK of the next chunk.  KV goes as early as its
@@ -508,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int flags = recs[d & 1].flags;
         arrive(bREmpty + (d & 1));
         ++d;
-        ok = __all_sync(0xffffffffu, (flags & kStop) == 0) != 0;
+        done = __any_sync(0xffffffffu, (flags & kStop) != 0) != 0;
+        ok = !done;
         if (!ok) break;
         len = __shfl_sync(0xffffffffu, len, 0);
       }
@@ -523,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         any = true;
       }
     }
-    if (*abort_flag && any) {  // drain MMAs in flight
+    if (!done && any) {  // drain MMAs in flight
       commit_to(lead, bar(bDrain));
-      mbar_wait(bar(bDrain), 0, a.err);
+      wait(bDrain, 0);
     }
   } else if (warp == 3) {
     // ----------------------------------------------------------------- copies out
@@ -537,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Rec& v = recs[d & 1];
         const int len = v.len, flags = v.flags, h = v.h, tok = v.tok;
         mbar_arrive(bar(bREmpty + (d & 1)));
-        if (flags & kStop) break;
+        done = (flags & kStop) != 0;
+        if (done) break;
         if (len <= 0) continue;
         if (!wait(bOut, (uint32_t)it)) break;
         if (len == C) {  // a partial chunk was written by the output group
@@ -551,6 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++it;
       }
       bulk_wait_all();
+    } else {
+      done = true;
     }
   } else if (warp >= 4) {
     // The four groups: records in order, each with its own work on a chunk.
@@ -558,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
     const int row = 32 * w + lane;
     if (!kOut && (group == 1 || group == 2)) {
-      // no scores and no outputs
+      done = true;  // no scores and no outputs
     } else if (group == 0) {
       // -------------------------------------------------------- weighted values
       // Warp w takes value rows 32 w .. + 31: a transposing load brings 16 rows x 16
@@ -574,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
         const Rec& v = recs[d & 1];
         const int len = v.len, flags = v.flags;
-        if (flags & kStop) break;
+        done = (flags & kStop) != 0;
+        if (done) break;
         if (len > 0) {
           const uint32_t ph = (uint32_t)(it >> 1);
           bool ok = wait_warp(full(tV, it), ph) &&
@@ -588,46 +636,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t vt = base + slot(tV, it) + (uint32_t)(w >> 1) * kHalfTile;
 #pragma unroll 1
-          for (int x = 0; x < 8; ++x) {  // 16 tokens x 32 value rows
-            const int tok0 = 16 * x, tok = tok0 + mrow;
-            uint32_t y[2][4];
+          for (int hf = 0; hf < 2; ++hf) {  // tokens 64 hf .. + 63
+            float2 ww[8];  // weights of this lane's token pairs, eight tokens apart
+            const int pt = 64 * hf + 2 * (lane & 3);
 #pragma unroll
-            for (int dh = 0; dh < 2; ++dh)
-              ldmatrix4_trans(vt + (uint32_t)(tok * 128 +
-                                              (((4 * (w & 1) + 2 * dh + mdv) ^ (tok & 7)) << 4)),
-                              y[dh]);
-            const int pt = tok0 + 2 * (lane & 3);
-            const float f = v.aft[tok0 >> 5];
-            float2 ww[2];  // weights of this lane's token pairs, eight tokens apart
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-              ww[m] = __fmul2_rn(*reinterpret_cast<const float2*>(&v.cf[pt + 8 * m]),
+            for (int i = 0; i < 8; ++i) {
+              const float f = v.aft[2 * hf + (i >> 2)];
+              ww[i] = __fmul2_rn(*reinterpret_cast<const float2*>(&v.cf[pt + 8 * i]),
                                  make_float2(f, f));
-            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-            if (tok0 + 16 > len) {
-#pragma unroll
-              for (int m = 0; m < 2; ++m)
-                keep[m] = (pt + 8 * m < len ? 0xffffu : 0u) | (pt + 8 * m + 1 < len ? 0xffff0000u : 0u);
             }
+#pragma unroll 1
+            for (int dh = 0; dh < 2; ++dh) {  // 16 value rows
+              uint32_t hi[16], lo[16];
+              const uint32_t src = vt + (uint32_t)((64 * hf + mrow) * 128 +
+                                                   (((4 * (w & 1) + 2 * dh + mdv) ^ (lane & 7)) << 4));
 #pragma unroll
-            for (int dh = 0; dh < 2; ++dh) {
-              uint32_t hi[4], lo[4];
+              for (int i = 0; i < 4; ++i) {  // 16 tokens
+                uint32_t y[4];
+                ldmatrix4_trans(src + 2048u * i, y);
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const uint32_t z = y[dh][m];
-                const float2 p = __fmul2_rn(make_float2(bf16_lo(z), bf16_hi(z)), ww[m >> 1]);
-                const uint32_t h = pack_bf16(p.x, p.y);
-                hi[m] = h & keep[m >> 1];
-                lo[m] = pack_bf16(p.x - bf16_lo(h), p.y - bf16_hi(h)) & keep[m >> 1];
+                for (int m = 0; m < 4; ++m) {
+                  const float2 p = __fmul2_rn(make_float2(bf16_lo(y[m]), bf16_hi(y[m])),
+                                              ww[2 * i + (m >> 1)]);
+                  const uint32_t h = pack_bf16(p.x, p.y);
+                  hi[4 * i + m] = h;
+                  lo[4 * i + m] = pack_bf16(p.x - bf16_lo(h), p.y - bf16_hi(h));
+                }
               }
-              const uint32_t dst = lanes + ((uint32_t)(16 * dh) << 16) + (uint32_t)(tok0 >> 1);
-              tmem_st_16x128b_x2(dst + kT_Vhi, hi);
-              tmem_st_16x128b_x2(dst + kT_Vlo, lo);
+              if (64 * hf + 64 > len) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const int q = pt + 8 * (i >> 1);
+                  const uint32_t keep = (q < len ? 0xffffu : 0u) | (q + 1 < len ? 0xffff0000u : 0u);
+                  hi[i] &= keep;
+                  lo[i] &= keep;
+                }
+              }
+              const uint32_t dst = lanes + ((uint32_t)(16 * dh) << 16) + 32u * hf;
+              tmem_st_16x128b_x8(dst + kT_Vhi, hi);
+              tmem_st_16x128b_x8(dst + kT_Vlo, lo);
             }
-            if ((x & 3) == 3 && len == C) {  // a half is done
+            if (len == C) {
               tmem_wait_st();
               tc_fence_before();
-              arrive(bVw + (x >> 2));
+              arrive(bVw + hf);
             }
           }
           if (len < C) {
@@ -660,7 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
         const Rec& v = recs[d & 1];
         const int len = v.len, flags = v.flags;
-        if (flags & kStop) break;
+        done = (flags & kStop) != 0;
+        if (done) break;
         if (len > 0) {
           if (!wait_warp(bQK, (uint32_t)it)) break;
           tc_fence_after();
@@ -744,7 +797,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < 3; ++b) e0 += b < w ? v.T[b] : 0.f;
         arrive(bREmpty + (d & 1));
-        if (flags & kStop) break;
+        done = (flags & kStop) != 0;
+        if (done) break;
         if (len <= 0) continue;
         const float e1 = a.scale * exp2_approx(e0);
         const float2 e2 = make_float2(e1, e1);
@@ -811,7 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* decay = (flags & kLast) ? v.decay : nullptr;
         const float sofar = v.sofar, gam = exp2_approx(v.total);
         arrive(bREmpty + (d & 1));
-        if (flags & kStop) break;
+        done = (flags & kStop) != 0;
+        if (done) break;
         const bool first = (flags & kFirst) != 0;
         if (decay && row == 0) *decay = exp2_approx(sofar);
         if (init) init += row * D;
@@ -821,13 +876,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!first && !wait_warp(bKV, (uint32_t)it - 1)) break;
           tc_fence_after();
         }
+        bool ok = true;
         // pass 0: before the chunk; pass 1: the final state, after its KV
 #pragma unroll 1
         for (int pass = len > 0 ? 0 : 1; pass < 2; ++pass) {
           if (pass == 1) {
             if (!(flags & kLast)) break;
             if (len > 0) {
-              if (!wait_warp(bKV, (uint32_t)it)) break;
+              ok = wait_warp(bKV, (uint32_t)it);
+              if (!ok) break;
               tc_fence_after();
             }
             if (!fin) break;
@@ -880,11 +937,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive(bS);
           }
         }
-        if (*abort_flag) break;
+        if (!ok) break;
         if (len > 0) ++it;
       }
     }
   }
+  if (!done && lane == 0) atomicExch(a.err, kDevErrTimeout);  // a wait gave up
   tc_fence_before();
   __syncthreads();
   if (warp == 3) {
