@@ -29,9 +29,8 @@
 // o leaves from the tile that held q (its last reader, QS, is done by then), so the ring
 // holds two whole chunks of q, k and v.
 //
-// Warps: a front warp (jobs, decay vectors, tensor copies in), MMA issue, copies out; then
-// four groups of four, one warp of each on every SM sub-partition: weighted values, scores
-// -> P, outputs, state.  The front warp decodes the work and hands every chunk to the others
+// Warps: copies in, MMA issue, decay records, copies out; then four groups of four, one warp of each on every SM sub-partition: weighted values, scores
+// -> P, outputs, state.  The record warp decodes the work and hands every chunk to the others
 // as one record in shared memory, and loops stay rolled: five roles run at once, and with
 // 94 KB of code (jobs decoded by every role, unrolled loops) instruction fetch bounded
 // the kernel, at 8500 clocks a chunk.
@@ -61,11 +60,11 @@ constexpr float kMinG = -100.f;
 
 constexpr uint32_t kTileBytes = C * D * 2;  // 32 KB: two 64-channel blocks of 128 rows
 constexpr uint32_t kHalfTile = kTileBytes / 2;
-enum { tK = 0, tQ = 1, tV = 2 };            // tile t of chunk `it` sits in slot 3 (it & 1) + t
+enum { tK = 0, tV = 1, tQ = 2 };            // tile t of chunk `it` sits in slot 3 (it & 1) + t
 constexpr uint32_t kSbOff = 6 * kTileBytes;  // bf16 copy of S^T, K-major
 constexpr uint32_t kVecOff = kSbOff + kTileBytes;
 
-// A chunk as the front warp hands it out: what it is, and its decays (log2 units).
+// A chunk as the record warp hands it out: what it is, and its decays (log2 units).
 struct __align__(16) Rec {
   float L[C];    // sum of g inside the token's 32-token block, inclusive
   float cf[C];   // 2^(sum of g behind the token inside its block)
@@ -110,7 +109,7 @@ static_assert(kBars * 8 <= kBarBytes, "barriers");
 constexpr uint32_t kT_S = 0, kT_P = 128, kT_O = 256, kT_Vhi = 384, kT_Vlo = 448;
 
 constexpr int kGroup = 128;
-constexpr int kThreads = 128 + 4 * kGroup;
+constexpr int kThreads = 128 + 5 * kGroup;  // the state takes two groups
 // A wait gives up after this many polls, each of which suspends for up to a microsecond.
 constexpr uint32_t kPolls = 1u << 22, kPollNs = 1000;
 
@@ -293,6 +292,19 @@ __device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// v (wh + wl) of a bf16 pair in two bf16 parts: hi = v wh rounded; v wh - hi has at most
+// eight significant bits and is exact; v wl joins it with the second rounding.
+__device__ __forceinline__ void weigh(uint32_t v, uint32_t wh, uint32_t wl, uint32_t& hi,
+                                      uint32_t& lo) {
+  asm("{\n\t.reg .b32 n, r, z;\n\t"
+      "mov.b32 z, 0x80008000;\n\t"  // -0: the product alone, its sign kept
+      "fma.rn.bf16x2 %0, %2, %3, z;\n\t"
+      "neg.bf16x2 n, %0;\n\t"
+      "fma.rn.bf16x2 r, %2, %3, n;\n\t"
+      "fma.rn.bf16x2 %1, %2, %4, r;\n\t}"
+      : "=&r"(hi), "=&r"(lo)
+      : "r"(v), "r"(wh), "r"(wl));
+}
 // 32 lanes x 8 columns store.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
@@ -333,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kBars; ++i) {
       const bool group = (i >= bVw && i <= bS) || i == bOs || i == bO || i == bOut;
       const bool rec = i == bREmpty || i == bREmpty + 1;  // every warp that reads records
-      mbar_init(bar(i), rec ? (kOut ? 18 : 9) : (group ? 4 : 1));
+      mbar_init(bar(i), rec ? (kOut ? 22 : 13) : (i == bS ? 8 : (group ? 4 : 1)));
     }
     mbar_fence_init();
   }
@@ -371,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < j.chunks && ok; ++c, ++it) {
         const int tok = (int)(j.t0 + (int64_t)c * C);
 #pragma unroll 1
-        for (int i = 0; i < 3; i += kOut ? 1 : 2) {
+        for (int i = 0; i < kTiles; ++i) {  // in the order their slots fall free
           ok = it < 2 || wait_warp(empty(i, it), (uint32_t)(it >> 1) - 1);
           if (!ok) break;
           const void* tm = i == tK ? &tm_k : (i == tQ ? &tm_q : &tm_v);
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {  // copies in flight must land before the CTA exits
 #pragma unroll 1
       for (int x = max(0, m - 2 * kTiles); x < m; ++x)
-        wait(full(kOut ? x % 3 : 2 * (x % 2), x / kTiles), (uint32_t)(x / kTiles >> 1));
+        wait(full(x % kTiles, x / kTiles), (uint32_t)(x / kTiles >> 1));
     }
   } else if (warp == 2) {
     // --------------------------------------------------------------------- records
@@ -637,13 +649,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vt = base + slot(tV, it) + (uint32_t)(w >> 1) * kHalfTile;
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {  // tokens 64 hf .. + 63
-            float2 ww[8];  // weights of this lane's token pairs, eight tokens apart
+            // weights of this lane's token pairs, eight tokens apart, in two bf16 parts
+            uint32_t wh[8], wl[8];
             const int pt = 64 * hf + 2 * (lane & 3);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float f = v.aft[2 * hf + (i >> 2)];
-              ww[i] = __fmul2_rn(*reinterpret_cast<const float2*>(&v.cf[pt + 8 * i]),
-                                 make_float2(f, f));
+              const float2 c = __fmul2_rn(*reinterpret_cast<const float2*>(&v.cf[pt + 8 * i]),
+                                          make_float2(f, f));
+              wh[i] = pack_bf16(c.x, c.y);
+              wl[i] = pack_bf16(c.x - bf16_lo(wh[i]), c.y - bf16_hi(wh[i]));
             }
 #pragma unroll 1
             for (int dh = 0; dh < 2; ++dh) {  // 16 value rows
@@ -655,13 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t y[4];
                 ldmatrix4_trans(src + 2048u * i, y);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                  const float2 p = __fmul2_rn(make_float2(bf16_lo(y[m]), bf16_hi(y[m])),
-                                              ww[2 * i + (m >> 1)]);
-                  const uint32_t h = pack_bf16(p.x, p.y);
-                  hi[4 * i + m] = h;
-                  lo[4 * i + m] = pack_bf16(p.x - bf16_lo(h), p.y - bf16_hi(h));
-                }
+                for (int m = 0; m < 4; ++m)
+                  weigh(y[m], wh[2 * i + (m >> 1)], wl[2 * i + (m >> 1)], hi[4 * i + m], lo[4 * i + m]);
               }
               if (64 * hf + 64 > len) {
 #pragma unroll
@@ -850,10 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ----------------------------------------------------------------- state
-      // Thread = value row.  Before a chunk: the row to bf16 for QS, and times e^{G_C} back
+      // Two groups: thread = value row and 64 of its columns.  Before a chunk: the row to bf16 for QS, and times e^{G_C} back
       // into tensor memory for KV; a job's first chunk takes its initial state instead.
-      const uint32_t col = lanes + kT_S;
-      uint8_t* sb = sm + kSbOff + row * 128;
+      const int half = group - 3;
+      const uint32_t col = lanes + kT_S + 64 * half;
+      uint8_t* sb = sm + kSbOff + half * kHalfTile + row * 128;
       int it = 0;
 #pragma unroll 1
       for (int d = 0;; ++d) {
@@ -868,9 +879,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         done = (flags & kStop) != 0;
         if (done) break;
         const bool first = (flags & kFirst) != 0;
-        if (decay && row == 0) *decay = exp2_approx(sofar);
-        if (init) init += row * D;
-        if (fin) fin += row * D;
+        if (decay && row == 0 && half == 0) *decay = exp2_approx(sofar);
+        if (init) init += row * D + 64 * half;
+        if (fin) fin += row * D + 64 * half;
         if (len > 0) {
           // (a job's end waits for the state, so its KV is done where the next one begins)
           if (!first && !wait_warp(bKV, (uint32_t)it - 1)) break;
@@ -891,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const bool from_init = pass == 0 ? first : len <= 0;
 #pragma unroll 1
-          for (int p = 0; p < 4; ++p) {
+          for (int p = 0; p < 2; ++p) {
             float s[32];
             if (from_init) {
 #pragma unroll
@@ -917,8 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              pack_bf16(s[8 * e + 2], s[8 * e + 3]),
                                              pack_bf16(s[8 * e + 4], s[8 * e + 5]),
                                              pack_bf16(s[8 * e + 6], s[8 * e + 7]));
-                  *reinterpret_cast<uint4*>(sb + (p >> 1) * kHalfTile +
-                                            (((4 * (p & 1) + e) ^ (row & 7)) << 4)) = y;
+                  *reinterpret_cast<uint4*>(sb + (((4 * p + e) ^ (row & 7)) << 4)) = y;
                 }
               }
 #pragma unroll
