@@ -99,8 +99,8 @@ enum {
   bOs = bQS + 1,       // O scaled
   bPV = bOs + 1,       // outputs complete
   bO = bPV + 1,        // outputs read out
-  bOut = bO + 1,       // outputs staged
-  bDrain = bOut + 1,
+  bOut = bO + 1,       // [2] channels 0-63, 64-127 of the outputs staged
+  bDrain = bOut + 2,
   kBars = bDrain + 1
 };
 static_assert(kBars * 8 <= kBarBytes, "barriers");
@@ -109,7 +109,7 @@ static_assert(kBars * 8 <= kBarBytes, "barriers");
 constexpr uint32_t kT_S = 0, kT_P = 128, kT_O = 256, kT_Vhi = 384, kT_Vlo = 448;
 
 constexpr int kGroup = 128;
-constexpr int kThreads = 128 + 5 * kGroup;  // the state takes two groups
+constexpr int kThreads = 128 + 5 * kGroup;  // the outputs take two groups
 // A wait gives up after this many polls, each of which suspends for up to a microsecond.
 constexpr uint32_t kPolls = 1u << 22, kPollNs = 1000;
 
@@ -305,12 +305,6 @@ __device__ __forceinline__ void weigh(uint32_t v, uint32_t wh, uint32_t wl, uint
       : "=&r"(hi), "=&r"(lo)
       : "r"(v), "r"(wh), "r"(wl));
 }
-// 32 lanes x 8 columns store.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
 // 3-D tiled tensor copy shared -> global in the calling thread's bulk group.
 __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::
@@ -343,9 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (t == 0) {
     // arrivals a phase: copies, commits and single threads 1, groups one a warp
     for (int i = 0; i < kBars; ++i) {
-      const bool group = (i >= bVw && i <= bS) || i == bOs || i == bO || i == bOut;
+      const bool group = (i >= bVw && i <= bS) || (i >= bOut && i < bOut + 2);
+      const bool outs = i == bOs || i == bO;  // both output groups
       const bool rec = i == bREmpty || i == bREmpty + 1;  // every warp that reads records
-      mbar_init(bar(i), rec ? (kOut ? 22 : 13) : (i == bS ? 8 : (group ? 4 : 1)));
+      mbar_init(bar(i), rec ? (kOut ? 22 : 9) : (outs ? 8 : (group ? 4 : 1)));
     }
     mbar_fence_init();
   }
@@ -596,14 +591,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         done = (flags & kStop) != 0;
         if (done) break;
         if (len <= 0) continue;
-        if (!wait(bOut, (uint32_t)it)) break;
-        if (len == C) {  // a partial chunk was written by the output group
-          const uint32_t src = base + slot(tQ, it);
-          tma_store_3d(&tm_o, src, 0, h, tok);
-          tma_store_3d(&tm_o, src + kHalfTile, 64, h, tok);
-          bulk_commit();
-          bulk_wait_read_all();
+        bool ok = true;
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          ok = ok && wait(bOut + hf, (uint32_t)it);
+          if (ok && len == C) {  // a partial chunk was written by the output groups
+            tma_store_3d(&tm_o, base + slot(tQ, it) + hf * kHalfTile, 64 * hf, h, tok);
+            bulk_commit();
+          }
         }
+        bulk_wait_read_all();
+        if (!ok) break;
         mbar_arrive(bar(empty(tQ, it)));
         ++it;
       }
@@ -616,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = (warp >> 2) - 1, w = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
     const int row = 32 * w + lane;
-    if (!kOut && (group == 1 || group == 2)) {
+    if (!kOut && group >= 1 && group <= 3) {
       done = true;  // no scores and no outputs
     } else if (group == 0) {
       // -------------------------------------------------------- weighted values
@@ -713,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (group == 1) {
       // ------------------------------------------------------------ scores -> P
-      // Thread = token row, 16 keys at a time.  P (packed pairs) overwrites the scores'
+      // Thread = token row, 32 keys at a time.  P (packed pairs) overwrites the scores'
       // columns from the left, behind the scores being read.
       const uint32_t col = lanes + kT_P;
       int it = 0;
@@ -740,16 +738,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
 #pragma unroll 1
-          for (int x = 0; x < 2 * w; ++x) {  // blocks left of the diagonal one
-            float s[16];
-            uint32_t pk[8];
-            tmem_ld16(col + 16 * x, s);
-            const float r = x < 2 ? rf[0] : (x < 4 ? rf[1] : rf[2]);
+          for (int b = 0; b < w; ++b) {  // blocks left of the diagonal one
+            float s[32];
+            uint32_t pk[16];
+            tmem_ld32(col + 32 * b, s);
+            const float r = b == 0 ? rf[0] : (b == 1 ? rf[1] : rf[2]);
             const float2 r2 = make_float2(r, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&v.cf[16 * x + i]);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&v.cf[32 * b + i]);
               const float2 p = __fmul2_rn(__fmul2_rn(make_float2(f.x, f.y), r2),
                                           make_float2(s[i], s[i + 1]));
               const float2 q = __fmul2_rn(__fmul2_rn(make_float2(f.z, f.w), r2),
@@ -757,32 +755,30 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[i / 2] = pack_bf16(p.x, p.y);
               pk[i / 2 + 1] = pack_bf16(q.x, q.y);
             }
-            tmem_st8(col + 8 * x, pk);
+            tmem_st16(col + 16 * b, pk);
           }
-#pragma unroll 1
-          for (int x = 2 * w; x < 2 * w + 2; ++x) {  // the diagonal block
-            float s[16];
-            uint32_t pk[8];
-            tmem_ld16(col + 16 * x, s);
+          {  // the diagonal block
+            float s[32];
+            uint32_t pk[16];
+            tmem_ld32(col + 32 * w, s);
             tmem_wait_ld();
-            const int j0 = 16 * x;
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float4 L = *reinterpret_cast<const float4*>(&v.L[j0 + i]);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 L = *reinterpret_cast<const float4*>(&v.L[32 * w + i]);
               const float Lj[4] = {L.x, L.y, L.z, L.w};
               float p[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                p[e] = j0 + i + e <= row ? s[i + e] * (a.scale * exp2_approx(Li - Lj[e])) : 0.f;
+                p[e] = i + e <= lane ? s[i + e] * (a.scale * exp2_approx(Li - Lj[e])) : 0.f;
               pk[i / 2] = pack_bf16(p[0], p[1]);
               pk[i / 2 + 1] = pack_bf16(p[2], p[3]);
             }
-            tmem_st8(col + 8 * x, pk);
+            tmem_st16(col + 16 * w, pk);
           }
 #pragma unroll 1
-          for (int x = 2 * w + 2; x < 8; ++x) {  // keys behind every token of this warp
-            const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            tmem_st8(col + 8 * x, z);
+          for (int b = w + 1; b < 4; ++b) {  // keys behind every token of this warp
+            const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            tmem_st16(col + 16 * b, z);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -791,12 +787,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         arrive(bREmpty + (d & 1));
       }
-    } else if (group == 2) {
+    } else if (group <= 3) {
       // --------------------------------------------------------------- outputs
-      // Thread = token row: O *= scale e^{G_i} between QS and PV; then the chunk goes to
+      // Two groups, thread = token row and 64 of its channels: O *= scale e^{G_i} between QS and PV; then the chunk goes to
       // the q tile's slot for the copy out, a partial one (its rows end inside the tile)
       // straight to memory.
-      const uint32_t col = lanes + kT_O;
+      const int half = group - 2;
+      const uint32_t col = lanes + kT_O + 64 * half;
       int it = 0;
 #pragma unroll 1
       for (int d = 0;; ++d) {
@@ -815,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(bQS, (uint32_t)it)) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < 2; ++p) {
           float y[32];
           tmem_ld32(col + 32 * p, y);
           tmem_wait_ld();
@@ -832,39 +829,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(bOs);
         if (!wait_warp(bPV, (uint32_t)it)) break;
         tc_fence_after();
-        uint8_t* stage = sm + slot(tQ, it) + row * 128;
-        __nv_bfloat16* orow = a.o + ((int64_t)(tok + row) * a.H + h) * D;
+        uint8_t* stage = sm + slot(tQ, it) + half * kHalfTile + row * 128;
+        __nv_bfloat16* orow = a.o + ((int64_t)(tok + row) * a.H + h) * D + 64 * half;
 #pragma unroll 1
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < 2; ++p) {
           float y[32];
           tmem_ld32(col + 32 * p, y);
           tmem_wait_ld();
+          if (p == 1) {
+            tc_fence_before();
+            arrive(bO);
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint4 z = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]),
-                                       pack_bf16(y[8 * e + 2], y[8 * e + 3]),
-                                       pack_bf16(y[8 * e + 4], y[8 * e + 5]),
-                                       pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+            const float* x = &y[8 * e];
+            const uint4 z = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                       pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
             if (len == C)
-              *reinterpret_cast<uint4*>(stage + (p >> 1) * kHalfTile +
-                                        (((4 * (p & 1) + e) ^ (row & 7)) << 4)) = z;
+              *reinterpret_cast<uint4*>(stage + (((4 * p + e) ^ (row & 7)) << 4)) = z;
             else if (row < len)
               *reinterpret_cast<uint4*>(orow + 32 * p + 8 * e) = z;
           }
         }
-        tc_fence_before();
         fence_proxy_async_smem();
-        arrive(bO);
-        arrive(bOut);
+        arrive(bOut + half);
         ++it;
       }
     } else {
       // ----------------------------------------------------------------- state
-      // Two groups: thread = value row and 64 of its columns.  Before a chunk: the row to bf16 for QS, and times e^{G_C} back
+      // Thread = value row.  Before a chunk: the row to bf16 for QS, and times e^{G_C} back
       // into tensor memory for KV; a job's first chunk takes its initial state instead.
-      const int half = group - 3;
-      const uint32_t col = lanes + kT_S + 64 * half;
-      uint8_t* sb = sm + kSbOff + half * kHalfTile + row * 128;
+      const uint32_t col = lanes + kT_S;
+      uint8_t* sb = sm + kSbOff + row * 128;
       int it = 0;
 #pragma unroll 1
       for (int d = 0;; ++d) {
@@ -879,9 +875,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         done = (flags & kStop) != 0;
         if (done) break;
         const bool first = (flags & kFirst) != 0;
-        if (decay && row == 0 && half == 0) *decay = exp2_approx(sofar);
-        if (init) init += row * D + 64 * half;
-        if (fin) fin += row * D + 64 * half;
+        if (decay && row == 0) *decay = exp2_approx(sofar);
+        if (init) init += row * D;
+        if (fin) fin += row * D;
         if (len > 0) {
           // (a job's end waits for the state, so its KV is done where the next one begins)
           if (!first && !wait_warp(bKV, (uint32_t)it - 1)) break;
@@ -902,42 +898,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const bool from_init = pass == 0 ? first : len <= 0;
 #pragma unroll 1
-          for (int p = 0; p < 2; ++p) {
-            float s[32];
+          for (int p = 0; p < 4; ++p) {
+            float x[32];
             if (from_init) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
-                const float4 x = init ? *reinterpret_cast<const float4*>(init + 32 * p + i)
+                const float4 y = init ? *reinterpret_cast<const float4*>(init + 32 * p + i)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-                s[i] = x.x; s[i + 1] = x.y; s[i + 2] = x.z; s[i + 3] = x.w;
+                x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
               }
             } else {
-              tmem_ld32(col + 32 * p, s);
+              tmem_ld32(col + 32 * p, x);
               tmem_wait_ld();
             }
             if (pass == 1) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 *reinterpret_cast<float4*>(fin + 32 * p + i) =
-                    make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+                    make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
             } else {
               if (kOut) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const uint4 y = make_uint4(pack_bf16(s[8 * e], s[8 * e + 1]),
-                                             pack_bf16(s[8 * e + 2], s[8 * e + 3]),
-                                             pack_bf16(s[8 * e + 4], s[8 * e + 5]),
-                                             pack_bf16(s[8 * e + 6], s[8 * e + 7]));
-                  *reinterpret_cast<uint4*>(sb + (((4 * p + e) ^ (row & 7)) << 4)) = y;
+                  const uint4 y = make_uint4(pack_bf16(x[8 * e], x[8 * e + 1]),
+                                             pack_bf16(x[8 * e + 2], x[8 * e + 3]),
+                                             pack_bf16(x[8 * e + 4], x[8 * e + 5]),
+                                             pack_bf16(x[8 * e + 6], x[8 * e + 7]));
+                  *reinterpret_cast<uint4*>(sb + (p >> 1) * kHalfTile +
+                                            (((4 * (p & 1) + e) ^ (row & 7)) << 4)) = y;
                 }
               }
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
-                const float2 z = __fmul2_rn(make_float2(s[i], s[i + 1]), make_float2(gam, gam));
-                s[i] = z.x;
-                s[i + 1] = z.y;
+                const float2 z = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(gam, gam));
+                x[i] = z.x;
+                x[i + 1] = z.y;
               }
-              tmem_st32(col + 32 * p, s);
+              tmem_st32(col + 32 * p, x);
             }
           }
           if (pass == 0) {
