@@ -105,11 +105,11 @@ enum {
 };
 static_assert(kBars * 8 <= kBarBytes, "barriers");
 
-// TMEM columns: state, scores (P over their left half), O, weighted values hi and lo
+// TMEM columns: state, scores (P over the left half of each half of them), O, weighted values hi and lo
 constexpr uint32_t kT_S = 0, kT_P = 128, kT_O = 256, kT_Vhi = 384, kT_Vlo = 448;
 
 constexpr int kGroup = 128;
-constexpr int kThreads = 128 + 5 * kGroup;  // the outputs take two groups
+constexpr int kThreads = 128 + 6 * kGroup;  // scores and outputs take two groups each
 // A wait gives up after this many polls, each of which suspends for up to a microsecond.
 constexpr uint32_t kPolls = 1u << 22, kPollNs = 1000;
 
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool group = (i >= bVw && i <= bS) || (i >= bOut && i < bOut + 2);
       const bool outs = i == bOs || i == bO;  // both output groups
       const bool rec = i == bREmpty || i == bREmpty + 1;  // every warp that reads records
-      mbar_init(bar(i), rec ? (kOut ? 22 : 9) : (outs ? 8 : (group ? 4 : 1)));
+      mbar_init(bar(i), rec ? (kOut ? 26 : 9) : (outs || i == bP ? 8 : (group ? 4 : 1)));
     }
     mbar_fence_init();
   }
@@ -486,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     done = ok;
   } else if (warp == 1) {
     // -------------------------------------------------------------------- MMAs
-    // Order a chunk: QS, KV, PV, then QK of the next chunk.  KV goes as early as its
-    // operands allow: the state group works on its result while PV and QK run.
+    // Order a chunk: KV, QS, PV, then QK of the next chunk.  KV comes first: the state group
+    // works on its result, the next chunk's first operand, while the others run.
     const uint32_t lead = elect_lane();
     const uint32_t id_kk = idesc_bf16_mn(C, C, 0, 0);  // both operands K-major
     const uint32_t id_kn = idesc_bf16_mn(C, D, 0, 1);  // B MN-major
@@ -506,16 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = -1; ok; ++it) {
       const uint32_t par = (uint32_t)it;
       if (it >= 0) {
-        ok = wait_warp(bS, par) && (!kOut || it == 0 || wait_warp(bO, par - 1));
+        ok = wait_warp(bS, par);
         if (!ok) break;
         tc_fence_after();
-        if (kOut) {
-          mma_kk(tmem + kT_O, base + slot(tQ, it), base + kSbOff);
-          commit_to(lead, bar(bQS));
-        } else {
-          ok = wait_warp(full(tK, it), par >> 1);
-          if (!ok) break;
-        }
+        ok = kOut || wait_warp(full(tK, it), par >> 1);  // (with outputs QK has waited for k)
+        if (!ok) break;
         any = true;
         uint64_t dk = mnmajor_desc_lbo(base + slot(tK, it), kHalfTile, 1024, 0);
         uint32_t va = tmem + kT_Vhi;
@@ -537,13 +532,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit_to(lead, bar(bKV));
         commit_to(lead, bar(empty(tK, it)));
         if (kOut) {
+          ok = it == 0 || wait_warp(bO, par - 1);
+          if (!ok) break;
+          tc_fence_after();
+          mma_kk(tmem + kT_O, base + slot(tQ, it), base + kSbOff);
+          commit_to(lead, bar(bQS));
           ok = wait_warp(bP, par) && wait_warp(bOs, par);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dv = mnmajor_desc_lbo(base + slot(tV, it), kHalfTile, 1024, 0);
 #pragma unroll
           for (int s = 0; s < 8; ++s)
-            mma_ts(lead, tmem + kT_O, tmem + kT_P + 8 * s, desc_advance(dv, (uint32_t)s * 2048u),
+            mma_ts(lead, tmem + kT_O, tmem + kT_P + (uint32_t)(8 * s + (s & 4) * 8), desc_advance(dv, (uint32_t)s * 2048u),
                    id_kn);
           commit_to(lead, bar(bPV));
         }
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = (warp >> 2) - 1, w = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
     const int row = 32 * w + lane;
-    if (!kOut && group >= 1 && group <= 3) {
+    if (!kOut && group >= 1 && group <= 4) {
       done = true;  // no scores and no outputs
     } else if (group == 0) {
       // -------------------------------------------------------- weighted values
@@ -709,10 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         arrive(bREmpty + (d & 1));
       }
-    } else if (group == 1) {
+    } else if (group <= 2) {
       // ------------------------------------------------------------ scores -> P
-      // Thread = token row, 32 keys at a time.  P (packed pairs) overwrites the scores'
-      // columns from the left, behind the scores being read.
+      // Two groups, thread = token row and 64 of its keys, 32 at a time.  P (packed pairs)
+      // overwrites the left half of the group's own scores, behind the scores being read.
+      const int b0 = 2 * (group - 1);  // first of the group's two key blocks
       const uint32_t col = lanes + kT_P;
       int it = 0;
 #pragma unroll 1
@@ -726,59 +727,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait_warp(bQK, (uint32_t)it)) break;
           tc_fence_after();
           const float Li = v.L[row];
-          float upto = Li;  // decay exponent from the end of key block b to this token
-          float rf[3];
+#pragma unroll 1
+          for (int b = b0; b < b0 + 2; ++b) {
+            float s[32];
+            uint32_t pk[16];
+            if (b > w) {  // keys behind every token of this warp
 #pragma unroll
-          for (int b = 2; b >= 0; --b) {
-            if (b < w) {
-              rf[b] = a.scale * exp2_approx(upto);
-              upto += v.T[b];
+              for (int i = 0; i < 16; ++i) pk[i] = 0u;
             } else {
-              rf[b] = 0.f;
-            }
-          }
-#pragma unroll 1
-          for (int b = 0; b < w; ++b) {  // blocks left of the diagonal one
-            float s[32];
-            uint32_t pk[16];
-            tmem_ld32(col + 32 * b, s);
-            const float r = b == 0 ? rf[0] : (b == 1 ? rf[1] : rf[2]);
-            const float2 r2 = make_float2(r, r);
-            tmem_wait_ld();
+              tmem_ld32(col + 32 * b, s);
+              float upto = Li;  // decay exponent from the end of the key block to this token
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&v.cf[32 * b + i]);
-              const float2 p = __fmul2_rn(__fmul2_rn(make_float2(f.x, f.y), r2),
-                                          make_float2(s[i], s[i + 1]));
-              const float2 q = __fmul2_rn(__fmul2_rn(make_float2(f.z, f.w), r2),
-                                          make_float2(s[i + 2], s[i + 3]));
-              pk[i / 2] = pack_bf16(p.x, p.y);
-              pk[i / 2 + 1] = pack_bf16(q.x, q.y);
-            }
-            tmem_st16(col + 16 * b, pk);
-          }
-          {  // the diagonal block
-            float s[32];
-            uint32_t pk[16];
-            tmem_ld32(col + 32 * w, s);
-            tmem_wait_ld();
+              for (int x = 1; x < 3; ++x) upto += (x > b && x < w) ? v.T[x] : 0.f;
+              const float r = a.scale * exp2_approx(upto);
+              const float2 r2 = make_float2(r, r);
+              tmem_wait_ld();
+              if (b < w) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 L = *reinterpret_cast<const float4*>(&v.L[32 * w + i]);
-              const float Lj[4] = {L.x, L.y, L.z, L.w};
-              float p[4];
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 f = *reinterpret_cast<const float4*>(&v.cf[32 * b + i]);
+                  const float2 p = __fmul2_rn(__fmul2_rn(make_float2(f.x, f.y), r2),
+                                              make_float2(s[i], s[i + 1]));
+                  const float2 q = __fmul2_rn(__fmul2_rn(make_float2(f.z, f.w), r2),
+                                              make_float2(s[i + 2], s[i + 3]));
+                  pk[i / 2] = pack_bf16(p.x, p.y);
+                  pk[i / 2 + 1] = pack_bf16(q.x, q.y);
+                }
+              } else {  // the diagonal block
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                p[e] = i + e <= lane ? s[i + e] * (a.scale * exp2_approx(Li - Lj[e])) : 0.f;
-              pk[i / 2] = pack_bf16(p[0], p[1]);
-              pk[i / 2 + 1] = pack_bf16(p[2], p[3]);
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 L = *reinterpret_cast<const float4*>(&v.L[32 * b + i]);
+                  const float Lj[4] = {L.x, L.y, L.z, L.w};
+                  float p[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    p[e] = i + e <= lane ? s[i + e] * (a.scale * exp2_approx(Li - Lj[e])) : 0.f;
+                  pk[i / 2] = pack_bf16(p[0], p[1]);
+                  pk[i / 2 + 1] = pack_bf16(p[2], p[3]);
+                }
+              }
             }
-            tmem_st16(col + 16 * w, pk);
-          }
-#pragma unroll 1
-          for (int b = w + 1; b < 4; ++b) {  // keys behind every token of this warp
-            const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            tmem_st16(col + 16 * b, z);
+            tmem_st16(col + 32 * b0 + 16 * (b - b0), pk);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -787,12 +776,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         arrive(bREmpty + (d & 1));
       }
-    } else if (group <= 3) {
+    } else if (group <= 4) {
       // --------------------------------------------------------------- outputs
       // Two groups, thread = token row and 64 of its channels: O *= scale e^{G_i} between QS and PV; then the chunk goes to
       // the q tile's slot for the copy out, a partial one (its rows end inside the tile)
       // straight to memory.
-      const int half = group - 2;
+      const int half = group - 3;
       const uint32_t col = lanes + kT_O + 64 * half;
       int it = 0;
 #pragma unroll 1
@@ -918,6 +907,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
             } else {
               if (kOut) {
+                if (p == 0 && it > 0) {  // QS has read the copy of the chunk before
+                  ok = wait_warp(bQS, (uint32_t)it - 1);
+                  if (!ok) break;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const uint4 y = make_uint4(pack_bf16(x[8 * e], x[8 * e + 1]),
@@ -937,6 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(col + 32 * p, x);
             }
           }
+          if (!ok) break;
           if (pass == 0) {
             tmem_wait_st();
             tc_fence_before();
