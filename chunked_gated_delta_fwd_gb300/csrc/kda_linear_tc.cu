@@ -29,7 +29,7 @@
 // o leaves from the tile that held q (its last reader, QS, is done by then), so the ring
 // holds two whole chunks of q, k and v.
 //
-// Warps: copies in, MMA issue, decay records, copies out; then four groups of four, one warp of each on every SM sub-partition: weighted values, scores
+// Warps: copies, MMA issue, decay records, jobs; then groups of four, one warp of each on every SM sub-partition: weighted values, scores
 // -> P, outputs, state.  The record warp decodes the work and hands every chunk to the others
 // as one record in shared memory, and loops stay rolled: five roles run at once, and with
 // 94 KB of code (jobs decoded by every role, unrolled loops) instruction fetch bounded
@@ -78,7 +78,15 @@ struct __align__(16) Rec {
   float sofar;   // of the job, with this chunk
 };
 enum { kFirst = 1, kLast = 2, kStop = 4 };
-constexpr uint32_t kBarOff = kVecOff + 2 * sizeof(Rec);
+// A chain (or a segment of one), as the scheduling warp hands it out.
+struct Job {
+  const float* init;
+  float* fin;
+  float* decay;
+  int tok, tokens, h, stop;
+};
+constexpr uint32_t kJobOff = kVecOff + 2 * sizeof(Rec);
+constexpr uint32_t kBarOff = kJobOff + 2 * sizeof(Job);
 constexpr uint32_t kBarBytes = 32 * 8;
 constexpr uint32_t kSmemUsed = kBarOff + kBarBytes + 16;
 constexpr uint32_t kSmemBytes = 232448;  // all an SM has: one CTA each
@@ -90,7 +98,9 @@ enum {
   bEmpty = bFull + 6,  // [6] tile free again
   bRFull = bEmpty + 6,  // [2] record written
   bREmpty = bRFull + 2,  // [2] record read
-  bQK = bREmpty + 2,   // scores complete
+  bJFull = bREmpty + 2,  // [2] job written
+  bJNext = bJFull + 2,   // the next job is wanted and has room
+  bQK = bJNext + 1,    // scores complete
   bVw = bQK + 1,       // [2] weighted values of tokens 0-63, 64-127 written
   bP = bVw + 2,        // P written
   bS = bP + 1,         // state scaled and copied
@@ -99,8 +109,7 @@ enum {
   bOs = bQS + 1,       // O scaled
   bPV = bOs + 1,       // outputs complete
   bO = bPV + 1,        // outputs read out
-  bOut = bO + 1,       // [2] channels 0-63, 64-127 of the outputs staged
-  bDrain = bOut + 2,
+  bDrain = bO + 1,
   kBars = bDrain + 1
 };
 static_assert(kBars * 8 <= kBarBytes, "barriers");
@@ -150,15 +159,8 @@ struct LinArgs {
   const float* s_in;    // states entering segments [segment][H][dv][dk]
   float* s_end;         // local end states
   float* seg_decay;     // [segment][H]
+  int* ticket;          // next job (null: every gridDim.x-th, from blockIdx.x)
   int* err;
-};
-
-struct Job {
-  int h, tokens, chunks;
-  int64_t t0;
-  const float* init;
-  float* fin;
-  float* decay;
 };
 
 // Tokens of sequence n, clamped to the inputs; a malformed cu_seqlens is reported.
@@ -184,20 +186,20 @@ __device__ __forceinline__ int job_count(const LinArgs& a) {
 
 template <bool kOut>
 __device__ __forceinline__ Job get_job(const LinArgs& a, int item) {
-  Job j;
+  Job j{};
   const int u = item / a.H;
   j.h = item - u * a.H;
-  j.decay = nullptr;
   if (!a.tab) {
-    int64_t t1;
-    seq_range(a, u, j.t0, t1);
-    j.tokens = (int)(t1 - j.t0);
+    int64_t t0, t1;
+    seq_range(a, u, t0, t1);
+    j.tok = (int)t0;
+    j.tokens = (int)(t1 - t0);
     const int64_t s = (int64_t)item * D * D;
     j.init = a.h0 ? a.h0 + s : nullptr;
     j.fin = a.hT ? a.hT + s : nullptr;
   } else {
     const int4 e = a.tab[u];
-    j.t0 = e.y;
+    j.tok = e.y;
     j.tokens = e.z;
     const int k = e.w & 0x7fffffff;
     const bool last = e.w < 0;
@@ -212,7 +214,6 @@ __device__ __forceinline__ Job get_job(const LinArgs& a, int item) {
       j.decay = a.seg_decay + item;
     }
   }
-  j.chunks = (j.tokens + C - 1) / C;
   return j;
 }
 
@@ -305,20 +306,40 @@ __device__ __forceinline__ void weigh(uint32_t v, uint32_t wh, uint32_t wl, uint
       : "=&r"(hi), "=&r"(lo)
       : "r"(v), "r"(wh), "r"(wl));
 }
-// 3-D tiled tensor copy shared -> global in the calling thread's bulk group.
-__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::
-                   "l"(reinterpret_cast<uint64_t>(tmap)),
-               "r"(src), "r"(x), "r"(y), "r"(z)
-               : "memory");
+// 16 lanes x 64 columns: registers 4 i + 2 r + e of lane l hold TMEM lane l / 4 + 8 r, column
+// 8 i + 2 (l % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Within each four lanes: word j of lane q becomes word q of lane j.
+__device__ __forceinline__ void transpose4(uint32_t (&z)[4], int lane) {
+#pragma unroll
+  for (int m = 2; m >= 1; m >>= 1) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & m) continue;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? z[k] : z[k + m], m);
+      if (up) z[k] = got;
+      else z[k + m] = got;
+    }
+  }
 }
 
 // kOut: outputs and final states.  Otherwise the state alone (the first pass over segments).
 template <bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     lin_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_o, const LinArgs a) {
+                  const __grid_constant__ CUtensorMap tm_v, const LinArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   if (pad + kSmemUsed > kSmemBytes) {  // (uniform; dynamic shared memory starts aligned)
@@ -331,16 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kBarOff + kBarBytes);
   Rec* recs = reinterpret_cast<Rec*>(sm + kVecOff);
+  Job* jobs = reinterpret_cast<Job*>(sm + kJobOff);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   bool done = false;  // this role has come to the end of the work
 
   if (t == 0) {
     // arrivals a phase: copies, commits and single threads 1, groups one a warp
     for (int i = 0; i < kBars; ++i) {
-      const bool group = (i >= bVw && i <= bS) || (i >= bOut && i < bOut + 2);
+      const bool group = i >= bVw && i <= bS;
       const bool outs = i == bOs || i == bO;  // both output groups
       const bool rec = i == bREmpty || i == bREmpty + 1;  // every warp that reads records
-      mbar_init(bar(i), rec ? (kOut ? 26 : 9) : (outs || i == bP ? 8 : (group ? 4 : 1)));
+      mbar_init(bar(i), rec ? (kOut ? 25 : 9) : (outs || i == bP ? 8 : (group ? 4 : (i == bJNext ? 2 : 1))));
     }
     mbar_fence_init();
   }
@@ -366,26 +388,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------------ copies in
     constexpr int kTiles = kOut ? 3 : 2;
-    const int items = job_count<kOut>(a);
     const uint32_t lead = elect_lane();
     int it = 0, m = 0;  // chunks, tiles copied
     bool ok = true;
 #pragma unroll 1
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const Job j = get_job<kOut>(a, item);
+    for (int n = 0;; ++n) {
+      ok = wait_warp(bJFull + (n & 1), (uint32_t)(n >> 1));
+      if (!ok) break;
+      const Job j = jobs[n & 1];
+      if (j.stop) break;
       const int kv_head = j.h / a.rep;
+      // the next job is asked for two chunks before this one's end: late, so that CTAs that
+      // draw jobs by ticket end together, and early enough for its decoding
+      const int ask = j.tokens - 2 * C;
+      if (ask <= 0) arrive(bJNext);
 #pragma unroll 1
-      for (int c = 0; c < j.chunks && ok; ++c, ++it) {
-        const int tok = (int)(j.t0 + (int64_t)c * C);
+      for (int c = 0; c < j.tokens && ok; c += C, ++it) {
+        if (c < ask && c + C >= ask) arrive(bJNext);
 #pragma unroll 1
         for (int i = 0; i < kTiles; ++i) {  // in the order their slots fall free
           ok = it < 2 || wait_warp(empty(i, it), (uint32_t)(it >> 1) - 1);
           if (!ok) break;
           const void* tm = i == tK ? &tm_k : (i == tQ ? &tm_q : &tm_v);
-          load_tile(lead, base + slot(i, it), tm, i == tV ? j.h : kv_head, tok, bar(full(i, it)));
+          load_tile(lead, base + slot(i, it), tm, i == tV ? j.h : kv_head, j.tok + c,
+                    bar(full(i, it)));
           ++m;
         }
       }
+      if (!ok) break;
     }
     done = ok;
     if (!ok) {  // copies in flight must land before the CTA exits
@@ -397,46 +427,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------------------- records
     // One a chunk (a job without tokens is one record, the end of the work another); the
     // next chunk's g is on its way while this one's sums are formed.
-    const int items = job_count<kOut>(a);
-    int d = 0;
-    bool ok = true;
+    int d = 0, n = 0, c = 0;
     float gn[4];
-    auto fetch = [&](const Job& j, int c) {
-      const int len = j.tokens - c * C;
+    float sofar = 0.f;
+    Job j;
+    bool ok = true;
+    auto next_job = [&]() {
+      ok = wait_warp(bJFull + (n & 1), (uint32_t)(n >> 1));
+      j = jobs[n & 1];
+      arrive(bJNext);  // (the job before this one needs its place no more)
+      ++n;
+    };
+    auto fetch = [&]() {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int r = 32 * b + lane;
+        const int r = c + 32 * b + lane;
         gn[b] = 0.f;
-        if (r < len)
-          gn[b] = __ldg(a.g + (a.g_head ? (int64_t)j.h : (j.t0 + (int64_t)(c * C + r)) * a.H + j.h));
+        if (ok && r < j.tokens)
+          gn[b] = __ldg(a.g + (a.g_head ? (int64_t)j.h : (int64_t)(j.tok + r) * a.H + j.h));
       }
     };
-    int item = blockIdx.x, c = 0;
-    float sofar = 0.f;
-    Job j{};
-    bool stop = item >= items;
-    if (!stop) j = get_job<kOut>(a, item);
-    fetch(j, 0);
+    next_job();
+    fetch();
 #pragma unroll 1
-    for (;; ++d) {
+    for (; ok; ++d) {
       // this record's job and g; then on to the next chunk or job, whose g is fetched here
       const Job jc = j;
       const int cc = c;
-      const bool last = cc + 1 >= jc.chunks, end = stop;
+      const bool last = cc + C >= jc.tokens, end = jc.stop != 0;
       float g[4], u[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) g[b] = gn[b];
       if (!end) {
+        c += C;
         if (last) {
-          item += gridDim.x;
           c = 0;
-          stop = item >= items;
-          j = Job{};
-          if (!stop) j = get_job<kOut>(a, item);
-        } else {
-          ++c;
+          next_job();
+          if (!ok) break;
         }
-        fetch(j, c);
+        fetch();
       }
       ok = d < 2 || wait_warp(bREmpty + (d & 1), (uint32_t)(d >> 1) - 1);
       if (!ok) break;
@@ -473,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         v.init = jc.init;
         v.fin = jc.fin;
         v.decay = jc.decay;
-        v.tok = (int)(jc.t0 + (int64_t)cc * C);
-        v.len = min(C, jc.tokens - cc * C);
+        v.tok = jc.tok + cc;
+        v.len = min(C, jc.tokens - cc);
         v.h = jc.h;
         v.flags = end ? kStop : ((cc == 0 ? kFirst : 0) | (last ? kLast : 0));
         v.total = after;
@@ -537,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           mma_kk(tmem + kT_O, base + slot(tQ, it), base + kSbOff);
           commit_to(lead, bar(bQS));
+          commit_to(lead, bar(empty(tQ, it)));
           ok = wait_warp(bP, par) && wait_warp(bOs, par);
           if (!ok) break;
           tc_fence_after();
@@ -579,35 +609,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(bDrain, 0);
     }
   } else if (warp == 3) {
-    // ----------------------------------------------------------------- copies out
-    if (kOut && lane == 0) {
-      int it = 0;
+    // ------------------------------------------------------------------------ jobs
+    const int items = job_count<kOut>(a);
+    int item = blockIdx.x;
 #pragma unroll 1
-      for (int d = 0;; ++d) {
-        if (!wait(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
-        const Rec& v = recs[d & 1];
-        const int len = v.len, flags = v.flags, h = v.h, tok = v.tok;
-        mbar_arrive(bar(bREmpty + (d & 1)));
-        done = (flags & kStop) != 0;
-        if (done) break;
-        if (len <= 0) continue;
-        bool ok = true;
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          ok = ok && wait(bOut + hf, (uint32_t)it);
-          if (ok && len == C) {  // a partial chunk was written by the output groups
-            tma_store_3d(&tm_o, base + slot(tQ, it) + hf * kHalfTile, 64 * hf, h, tok);
-            bulk_commit();
-          }
-        }
-        bulk_wait_read_all();
-        if (!ok) break;
-        mbar_arrive(bar(empty(tQ, it)));
-        ++it;
+    for (int n = 0;; ++n) {
+      Job j{};
+      j.stop = item >= items;
+      if (!j.stop) j = get_job<kOut>(a, item);
+      if (lane == 0) jobs[n & 1] = j;
+      arrive(bJFull + (n & 1));
+      done = j.stop != 0;
+      if (done || !wait_warp(bJNext, (uint32_t)n)) break;
+      if (a.ticket) {
+        if (lane == 0) item = (int)gridDim.x + atomicAdd(a.ticket, 1);
+        item = __shfl_sync(0xffffffffu, item, 0);
+      } else {
+        item += (int)gridDim.x;
       }
-      bulk_wait_all();
-    } else {
-      done = true;
     }
   } else if (warp >= 4) {
     // The four groups: records in order, each with its own work on a chunk.
@@ -818,30 +837,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(bOs);
         if (!wait_warp(bPV, (uint32_t)it)) break;
         tc_fence_after();
-        uint8_t* stage = sm + slot(tQ, it) + half * kHalfTile + row * 128;
-        __nv_bfloat16* orow = a.o + ((int64_t)(tok + row) * a.H + h) * D + 64 * half;
+        // 16 rows x 64 channels at a time, four lanes a row; lane q of them holds pairs
+        // 8 i + 2 q, and a 4 x 4 exchange of pairs leaves it channels 8 q .. 8 q + 7
+        __nv_bfloat16* orow = a.o + ((int64_t)(tok + 32 * w + (lane >> 2)) * a.H + h) * D + 64 * half +
+                              8 * (lane & 3);
 #pragma unroll 1
-        for (int p = 0; p < 2; ++p) {
-          float y[32];
-          tmem_ld32(col + 32 * p, y);
+        for (int sl = 0; sl < 2; ++sl) {
+          uint32_t y[32];
+          tmem_ld_16x256b_x8(col + ((uint32_t)(16 * sl) << 16), y);
           tmem_wait_ld();
-          if (p == 1) {
+          if (sl == 1) {
             tc_fence_before();
             arrive(bO);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float* x = &y[8 * e];
-            const uint4 z = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                       pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-            if (len == C)
-              *reinterpret_cast<uint4*>(stage + (((4 * p + e) ^ (row & 7)) << 4)) = z;
-            else if (row < len)
-              *reinterpret_cast<uint4*>(orow + 32 * p + 8 * e) = z;
+          for (int rs = 0; rs < 2; ++rs) {  // rows 0-7, 8-15 of them
+            const int r = 16 * sl + 8 * rs;
+            const bool in = 32 * w + (lane >> 2) + r < len;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {  // channels 32 g .. + 31
+              uint32_t z[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                z[i] = pack_bf16(__uint_as_float(y[4 * (4 * g + i) + 2 * rs]),
+                                 __uint_as_float(y[4 * (4 * g + i) + 2 * rs + 1]));
+              transpose4(z, lane);
+              if (in)
+                *reinterpret_cast<uint4*>(orow + (int64_t)r * a.H * D + 32 * g) =
+                    make_uint4(z[0], z[1], z[2], z[3]);
+            }
           }
         }
-        fence_proxy_async_smem();
-        arrive(bOut + half);
         ++it;
       }
     } else {
@@ -960,7 +986,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // and the pass with outputs starts each segment from its own (also the first, so that hT
 // may be h0: h0 is not read any more when a last segment writes hT).
 __global__ void __launch_bounds__(1024) lin_seg_plan_kernel(LinArgs a, int L, int4* tab,
-                                                            int* first, int* n_segs, int cap) {
+                                                            int* first, int* n_segs, int cap,
+                                                            int* tickets) {
   __shared__ int warp_sums[32];
   __shared__ int carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1009,6 +1036,7 @@ __global__ void __launch_bounds__(1024) lin_seg_plan_kernel(LinArgs a, int L, in
   if (tid == 0) {
     first[a.n_seqs] = min(carry, cap);
     *n_segs = min(carry, cap);
+    tickets[0] = tickets[1] = 0;
   }
 }
 
@@ -1036,7 +1064,7 @@ __global__ void __launch_bounds__(kScanThreads) lin_seg_scan_kernel(
 
 struct SegLayout {
   int4* tab;
-  int *first, *n_segs;
+  int *first, *n_segs, *tickets;
   float *decay, *s_end, *s_in;
   int cap;
   size_t bytes;
@@ -1052,7 +1080,8 @@ SegLayout seg_layout(void* ws, int64_t n_tokens, int n_seqs, int H, int L) {
     return p;
   };
   l.cap = (int)(n_tokens / ((int64_t)L * C) + n_seqs);
-  l.n_segs = reinterpret_cast<int*>(take(sizeof(int)));
+  l.n_segs = reinterpret_cast<int*>(take(3 * sizeof(int)));
+  l.tickets = l.n_segs + 1;  // [2], one a pass
   l.first = reinterpret_cast<int*>(take(sizeof(int) * ((size_t)n_seqs + 1)));
   l.tab = reinterpret_cast<int4*>(take(sizeof(int4) * (size_t)l.cap));
   const size_t units = (size_t)l.cap * H;
@@ -1112,7 +1141,7 @@ cudaError_t run(const CUtensorMap* tm, const LinArgs& a, int64_t items, const ch
   const int sms = sm_count();
   ProfScope prof_scope(name, s);
   lin_tc_kernel<kOut><<<(unsigned)(items < sms ? items : sms), kThreads, kSmemBytes, s>>>(
-      tm[0], tm[1], tm[2], tm[3], a);
+      tm[0], tm[1], tm[2], a);
   return cudaGetLastError();
 }
 
@@ -1153,21 +1182,31 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
   a.o = static_cast<__nv_bfloat16*>(o);
   a.hT = hT;
   a.err = err;
-  CUtensorMap tm[4];
+  CUtensorMap tm[3];
   memset(tm, 0, sizeof(tm));
   cudaError_t e = cudaSuccess;
   if (n_tokens > 0) {  // with no tokens there are no chunks to copy
     e = encode_tiles(&tm[0], q, Hk, n_tokens);
     if (e == cudaSuccess) e = encode_tiles(&tm[1], k, Hk, n_tokens);
     if (e == cudaSuccess) e = encode_tiles(&tm[2], v, H, n_tokens);
-    if (e == cudaSuccess) e = encode_tiles(&tm[3], o, H, n_tokens);
     if (e != cudaSuccess) return e;
   }
-  if (seg_chunks <= 0) return run<true>(tm, a, (int64_t)n_seqs * H, "kda_linear_tc", s);
+  if (seg_chunks <= 0) {
+    // Chains of different lengths, several a CTA: drawn by ticket where a chain is long enough
+    // to make up for clearing the counter.
+    const int64_t chains = (int64_t)n_seqs * H;
+    if (cu && n_seqs > 1 && chains > sm_count() && n_tokens >= (int64_t)n_seqs * 4 * C) {
+      a.ticket = static_cast<int*>(ws);
+      e = cudaMemsetAsync(ws, 0, sizeof(int), s);
+      if (e != cudaSuccess) return e;
+    }
+    return run<true>(tm, a, chains, "kda_linear_tc", s);
+  }
   const SegLayout l = seg_layout(ws, n_tokens, n_seqs, H, seg_chunks);
   {
     ProfScope prof_scope("kda_linear_seg_plan", s);
-    lin_seg_plan_kernel<<<1, 1024, 0, s>>>(a, seg_chunks, l.tab, l.first, l.n_segs, l.cap);
+    lin_seg_plan_kernel<<<1, 1024, 0, s>>>(a, seg_chunks, l.tab, l.first, l.n_segs, l.cap,
+                                              l.tickets);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -1176,6 +1215,7 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
   a.s_in = l.s_in;
   a.s_end = l.s_end;
   a.seg_decay = l.decay;
+  a.ticket = l.tickets;
   e = run<false>(tm, a, (int64_t)l.cap * H, "kda_linear_tc_state", s);
   if (e != cudaSuccess) return e;
   {
@@ -1185,6 +1225,7 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
+  a.ticket = l.tickets + 1;
   return run<true>(tm, a, (int64_t)l.cap * H, "kda_linear_tc", s);
 }
 
