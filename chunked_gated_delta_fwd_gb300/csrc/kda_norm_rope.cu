@@ -8,22 +8,30 @@
 // a fraction of a turn there, and only the fraction goes to the fp32 sine and cosine.
 // One rounding, at the store.
 //
-// Bound by HBM: a row is read and written once.  A CTA owns whole tokens: its threads
-// first put the tokens' F sines and cosines (all heads share them) into shared memory,
-// then a half warp per row holds 8 channels a lane (16-byte accesses for bf16), sums
-// the squares by a half-warp all-reduce and takes the other half of a pair from the
-// lane that holds it by one shuffle.
+// With r = 1 / sqrt(mean(x^2) + eps) a channel's result is r (x_i A_i + x_p B_i), x_p the
+// other channel of its pair, A_i = w_i cos phi and B_i = -+ w_p sin phi: the same for all
+// heads of a token.  So a warp takes eight heads of one token, builds its lanes' A and B
+// once and then needs two multiplications a channel; the pair's other channel travels as
+// raw input, four shuffles a bf16 row.
+//
+// Bound by HBM: a row is read and written once.  A half warp holds a row, 8 channels a lane
+// (16-byte accesses for bf16), four rows of a lane in flight.  The CTAs stay resident and
+// walk the tokens; the next tokens' sines and cosines (fp64, few lanes a clock, shared by
+// all heads) are formed between two barriers' worth of rows.
 #include "kda_internal.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTokens = 16;  // tokens of one CTA (shared sine/cosine table)
-constexpr int kRopeMaxFreq = kD / 2;
+constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kRopeCtas = 4;        // resident CTAs an SM
+constexpr int kRopeMaxTokens = 8;   // tokens of one step of a CTA (sine/cosine table)
+constexpr int kUnitHeads = 8;       // heads of one warp's unit: four rows of a half warp
+constexpr int kBatch = kUnitHeads / 2;
 
-// sin and cos of p * f: the turn count in fp64, its fraction in fp32.
-__device__ __forceinline__ float2 sincos_turns(int32_t p, float f) {
+// cos and sin of p * f: the turn count in fp64, its fraction in fp32.
+__device__ __forceinline__ float2 cos_sin_turns(int32_t p, float f) {
   double u = (double)p * (double)f * 0.15915494309189533577;  // 1 / (2 pi)
   u -= rint(u);
   float s, c;
@@ -40,108 +48,169 @@ struct RopeArgs {
   const float* freq;          // [F]
   int64_t n_tokens;
   int64_t sq, sk, sqo, sko;   // elements between tokens
-  float eps;                  // < 0: no norm
-  int n_axes, F, Hq, Hk, tokens;  // tokens: of one CTA
+  float eps;
+  int n_axes, F, Hq, Hk;
+  int tokens;                 // of one step of a CTA
+  int splits;                 // CTAs that share a step's heads (few tokens)
 };
 
+// The raw words of 8 channels: 4 (bf16 pairs) or 8 (fp32).
+template <typename T> struct Words { static constexpr int n = sizeof(T) * 2; };
+__device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&w)[4]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+}
+__device__ __forceinline__ void load_words(const float* p, uint32_t (&w)[8]) {
+  const uint4 u = reinterpret_cast<const uint4*>(p)[0], v = reinterpret_cast<const uint4*>(p)[1];
+  w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+}
+// channels 2 i and 2 i + 1
+__device__ __forceinline__ float2 pair_of(const uint32_t (&w)[4], int i) {
+  return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t (&w)[8], int i) {
+  return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+}
+
 template <typename T, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(RopeArgs a, int* err) {
-  __shared__ float2 cs[kRopeMaxTokens * kRopeMaxFreq];  // (cos, sin) of (token, frequency)
-  const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
-  const int nt = (int)min((int64_t)a.tokens, a.n_tokens - t0);
-  for (int e = tid; e < nt * a.F; e += kRopeThreads) {
-    const int t = e / a.F, i = e - t * a.F;
-    int ax = a.axis ? __ldg(a.axis + i) : 0;
-    if (ax < 0 || ax >= a.n_axes) {  // reported; axis 0 keeps the read in bounds
-      if (err) atomicExch(err, kDevErrBadAxis);
-      ax = 0;
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(const RopeArgs a,
+                                                                           int* err) {
+  constexpr int kW = Words<T>::n;
+  __shared__ __align__(16) float2 cs[2][kRopeMaxTokens * kD / 2];  // (cos, sin) of (token, freq)
+  __shared__ __align__(16) float ws[2][kD];                        // norm weights of q and k
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = blockIdx.x / a.splits, split = blockIdx.x - group * a.splits;
+  const int64_t step = (int64_t)(gridDim.x / a.splits) * a.tokens;
+  auto table = [&](int64_t t0, int buf) {
+    const int nt = (int)min((int64_t)a.tokens, a.n_tokens - t0);
+    for (int e = tid; e < nt * a.F; e += kRopeThreads) {
+      const int t = e / a.F, i = e - t * a.F;
+      int ax = a.axis ? __ldg(a.axis + i) : 0;
+      if (ax < 0 || ax >= a.n_axes) {  // reported; axis 0 keeps the read in bounds
+        if (err) atomicExch(err, kDevErrBadAxis);
+        ax = 0;
+      }
+      cs[buf][e] = cos_sin_turns(__ldg(a.pos + ax * a.n_tokens + t0 + t), __ldg(a.freq + i));
     }
-    cs[e] = sincos_turns(__ldg(a.pos + ax * a.n_tokens + t0 + t), __ldg(a.freq + i));
-  }
-  const int hl = tid & 15;  // lane of the half warp: channels 8 hl .. 8 hl + 7
-  float wq[8], wk[8];
-  if (kNorm) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wq[i] = wk[i] = 1.f;
-    if (a.wq) load8(a.wq + 8 * hl, wq);
-    if (a.wk) load8(a.wk + 8 * hl, wk);
-  }
+  };
+  int64_t t0 = (int64_t)group * a.tokens;
+  ws[tid >> 7][tid & (kD - 1)] =
+      tid < kD ? (a.wq ? a.wq[tid] : 1.f) : (a.wk ? a.wk[tid - kD] : 1.f);
+  if (t0 < a.n_tokens) table(t0, 0);
   __syncthreads();
-  const int R = a.Hq + a.Hk, rows = nt * R;
-  const int F8 = a.F >> 3;  // lanes of one half of the rotated channels (half-split pairs)
-  constexpr int kHalfWarps = kRopeThreads / 16, kBatch = 4;
-  // every half warp of a warp runs the same number of rounds: the shuffles are uniform
-  for (int base = 0; base < rows; base += kHalfWarps * kBatch) {
-    float x[kBatch][8];
-    int tk[kBatch], hh[kBatch];
+  const int hl = lane & 15, hf = lane >> 4;  // channels 8 hl .. 8 hl + 7 of every other head
+  const int F8 = a.F >> 3;
+  const bool rot = hl < 2 * F8, low = hl < F8;
+  // half-split pairs: the lane (of the half warp) with the other channels
+  const int other = kInter || !rot ? hl : (low ? hl + F8 : hl - F8);
+  const int uq = (a.Hq + kUnitHeads - 1) / kUnitHeads, uk = (a.Hk + kUnitHeads - 1) / kUnitHeads;
+  const int U = uq + uk;
+#pragma unroll 1
+  for (int buf = 0; t0 < a.n_tokens; t0 += step, buf ^= 1) {
+    const int nt = (int)min((int64_t)a.tokens, a.n_tokens - t0);
+#pragma unroll 1
+    for (int u = warp + kRopeWarps * split; u < nt * U; u += kRopeWarps * a.splits) {
+      const int t = u / U, ub = u - t * U;
+      const bool isq = ub < uq;
+      const int H = isq ? a.Hq : a.Hk, h0 = (isq ? ub : ub - uq) * kUnitHeads + hf;
+      const T* src = (isq ? static_cast<const T*>(a.q) + (t0 + t) * a.sq
+                          : static_cast<const T*>(a.k) + (t0 + t) * a.sk) + h0 * kD + 8 * hl;
+      T* dst = (isq ? static_cast<T*>(a.qo) + (t0 + t) * a.sqo
+                    : static_cast<T*>(a.ko) + (t0 + t) * a.sko) + h0 * kD + 8 * hl;
+      uint32_t x[kBatch][kW];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int row = base + b * kHalfWarps + (tid >> 4);
-      tk[b] = row / R;
-      hh[b] = row - tk[b] * R;
-      if (row < rows) {
-        const T* p = hh[b] < a.Hq
-                         ? static_cast<const T*>(a.q) + (t0 + tk[b]) * a.sq + hh[b] * kD
-                         : static_cast<const T*>(a.k) + (t0 + tk[b]) * a.sk + (hh[b] - a.Hq) * kD;
-        load8(p + 8 * hl, x[b]);
-      } else {
-        tk[b] = -1;
+      for (int b = 0; b < kBatch; ++b) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
+        for (int i = 0; i < kW; ++i) x[b][i] = 0u;
+        if (h0 + 2 * b < H) load_words(src + 2 * b * kD, x[b]);
       }
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const bool isq = hh[b] < a.Hq;
-      if (kNorm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[b][i], x[b][i], ss);
-#pragma unroll
-        for (int m = 8; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        const float r = rsqrtf(ss * (1.f / kD) + a.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[b][i] *= r * (isq ? wq[i] : wk[i]);
-      }
-      const float2* c = cs + max(tk[b], 0) * a.F;
-      float y[8];
-      if (kInter) {
+      // this lane's coefficients (pairs of channels)
+      float2 A[4], B[4];
+      {
+        const float2* c = cs[buf] + t * a.F;
+        const float* w = ws[isq ? 0 : 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int f = 4 * hl + i;
-          const float2 w = f < a.F ? c[f] : make_float2(1.f, 0.f);
-          y[2 * i] = x[b][2 * i] * w.x - x[b][2 * i + 1] * w.y;
-          y[2 * i + 1] = x[b][2 * i] * w.y + x[b][2 * i + 1] * w.x;
-        }
-      } else {
-        const bool low = hl < F8, rot = hl < 2 * F8;
-        // lane of the half warp that holds the other half of this lane's pairs
-        const int other = rot ? (low ? hl + F8 : hl - F8) : hl;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float z = __shfl_sync(0xffffffffu, x[b][i], other, 16);
-          const float2 w = rot ? c[8 * (low ? hl : other) + i] : make_float2(1.f, 0.f);
-          y[i] = low ? x[b][i] * w.x - z * w.y : x[b][i] * w.x + z * w.y;
-          if (!rot) y[i] = x[b][i];
+          const float2 wo = *reinterpret_cast<const float2*>(w + 8 * hl + 2 * i);
+          if (!rot) {
+            A[i] = wo;
+            B[i] = make_float2(0.f, 0.f);
+          } else if (kInter) {
+            const float2 z = c[4 * hl + i];
+            A[i] = make_float2(wo.x * z.x, wo.y * z.x);
+            B[i] = make_float2(-wo.y * z.y, wo.x * z.y);
+          } else {
+            const float2 wp = *reinterpret_cast<const float2*>(w + 8 * other + 2 * i);
+            const float4 z = *reinterpret_cast<const float4*>(c + 8 * (low ? hl : other) + 2 * i);
+            const float sg = low ? -1.f : 1.f;
+            A[i] = make_float2(wo.x * z.x, wo.y * z.z);
+            B[i] = make_float2(sg * wp.x * z.y, sg * wp.y * z.w);
+          }
         }
       }
-      if (tk[b] >= 0) {
-        T* p = isq ? static_cast<T*>(a.qo) + (t0 + tk[b]) * a.sqo + hh[b] * kD
-                   : static_cast<T*>(a.ko) + (t0 + tk[b]) * a.sko + (hh[b] - a.Hq) * kD;
-        store8(p + 8 * hl, y);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        float r = 1.f;
+        if (kNorm) {
+          float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 z = pair_of(x[b], i);
+            ss = __ffma2_rn(z, z, ss);
+          }
+          float s = ss.x + ss.y;
+#pragma unroll
+          for (int m = 8; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+          r = rsqrtf(s * (1.f / kD) + a.eps);
+        }
+        uint32_t xp[kW];  // the other channels of this lane's pairs, as they came
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+          xp[i] = x[b][i];
+          if (!kInter) xp[i] = __shfl_sync(0xffffffffu, xp[i], other, 16);
+          if (!rot) xp[i] = 0u;
+        }
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 p = pair_of(xp, i);
+          if (kInter) p = make_float2(p.y, p.x);
+          const float2 z = __fmul2_rn(
+              __ffma2_rn(pair_of(x[b], i), A[i], __fmul2_rn(p, B[i])), make_float2(r, r));
+          y[2 * i] = z.x;
+          y[2 * i + 1] = z.y;
+        }
+        if (h0 + 2 * b < H) store8(dst + 2 * b * kD, y);
       }
     }
+    if (t0 + step < a.n_tokens) table(t0 + step, buf ^ 1);
+    __syncthreads();
   }
 }
 
 template <typename T>
-cudaError_t launch_rope_t(const RopeArgs& a, bool inter, bool norm, int* err, cudaStream_t s) {
-  const int64_t ctas = (a.n_tokens + a.tokens - 1) / a.tokens;
-  using Fn = void (*)(RopeArgs, int*);
+cudaError_t launch_rope_t(RopeArgs a, bool inter, bool norm, int* err, cudaStream_t s) {
+  int sms = 152, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int U = (a.Hq + kUnitHeads - 1) / kUnitHeads + (a.Hk + kUnitHeads - 1) / kUnitHeads;
+  const int64_t most = (int64_t)sms * kRopeCtas;
+  // tokens of a step: the fewest whose units fill the CTA's warps evenly, while there are
+  // steps enough for every CTA
+  a.tokens = 1;
+  while (a.tokens < kRopeMaxTokens && (a.tokens * U) % kRopeWarps != 0 &&
+         a.n_tokens >= 2 * a.tokens * most)
+    a.tokens *= 2;
+  const int64_t steps = (a.n_tokens + a.tokens - 1) / a.tokens;
+  // few tokens: their heads are spread over several CTAs
+  a.splits = 1;
+  while (steps * a.splits * 2 <= most && a.splits * kRopeWarps < a.tokens * U) a.splits *= 2;
+  const int64_t groups = steps < most / a.splits ? steps : most / a.splits;
+  using Fn = void (*)(const RopeArgs, int*);
   static const Fn fn[2][2] = {{norm_rope_kernel<T, false, false>, norm_rope_kernel<T, false, true>},
                               {norm_rope_kernel<T, true, false>, norm_rope_kernel<T, true, true>}};
-  fn[inter][norm]<<<(unsigned)ctas, kRopeThreads, 0, s>>>(a, err);
+  fn[inter][norm]<<<(unsigned)(groups * a.splits), kRopeThreads, 0, s>>>(a, err);
   return cudaGetLastError();
 }
 
@@ -152,11 +221,8 @@ cudaError_t launch_norm_rope(const void* q, const void* k, int bf16, const float
                              const int32_t* axis, const float* freq, int F, int interleaved,
                              void* qo, void* ko, int64_t n_tokens, int Hq, int Hk, int64_t sq,
                              int64_t sk, int64_t sqo, int64_t sko, int* err, cudaStream_t s) {
-  RopeArgs a{q, k, qo, ko, wq, wk, pos, axis, freq, n_tokens, sq, sk, sqo, sko, eps, n_axes, F,
-             Hq, Hk, 1};
-  // about 64 rows a CTA (four a half warp), so that a row's load has others beside it
-  a.tokens = 64 / (Hq + Hk);
-  a.tokens = a.tokens < 1 ? 1 : (a.tokens > kRopeMaxTokens ? kRopeMaxTokens : a.tokens);
+  const RopeArgs a{q, k, qo, ko, wq, wk, pos, axis, freq, n_tokens, sq, sk, sqo, sko, eps, n_axes,
+                   F, Hq, Hk, 1, 1};
   ProfScope prof_scope("kda_qk_norm_rope", s);
   return bf16 ? launch_rope_t<__nv_bfloat16>(a, interleaved != 0, eps >= 0.f, err, s)
               : launch_rope_t<float>(a, interleaved != 0, eps >= 0.f, err, s);
