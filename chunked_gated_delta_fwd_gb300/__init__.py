@@ -414,6 +414,24 @@ def recurrent_multi_step(q, k, v, g, beta, S, n_advance=None, *, out=None,
     return o
 
 
+def _call(fn, dev, *args):
+    """``fn(*args, stream)`` with ``dev`` current, on its current stream; raises on an error.
+    (Small calls are bound by what happens here: the device is switched only if it has to
+    be, pointers and the stream go over as plain integers.)"""
+    index = dev.index
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        raise KdaError(status, lib.kda_last_error_string().decode())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _token_stride(t: torch.Tensor, name: str) -> int:
     """Elements between the tokens of a [..., H, 128] tensor whose heads are contiguous
     and whose leading dimensions step as one (a slice of a packed projection has more
@@ -425,6 +443,8 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     if t.dim() < 3:
         raise ValueError(f"{name} must be [..., H, 128]")
     d, H = t.shape[-1], t.shape[-2]
+    if t.is_contiguous():
+        return H * d
     step = expect = None
     for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
         if size == 1:
@@ -475,25 +495,31 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
             _need(w, name, torch.float32, dev)
             if w.numel() != q.shape[-1]:
                 raise ValueError(f"{name} must have {q.shape[-1]} entries")
-    outs = []
-    for name, x, y in (("q_out", q, q_out), ("k_out", k, k_out)):
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        elif y.shape != x.shape or y.dtype != x.dtype or y.device != dev:
-            raise ValueError(f"{name} must have the shape, dtype and device of its input")
-        outs.append(y)
-    so = [_token_stride(y, name) for y, name in zip(outs, ("q_out", "k_out"))]
     H, Hk, d = q.shape[-2], k.shape[-2], q.shape[-1]
+    soq, sok = H * d, Hk * d
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        soq = _rope_out(q_out, q, "q_out")
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    else:
+        sok = _rope_out(k_out, k, "k_out")
     nt = 1
     for x in lead:
         nt *= x
-    with torch.cuda.device(dev):
-        _check(lib.kda_qk_norm_rope(
-            _ptr(q), _ptr(k), dt, _ptr(q_weight), _ptr(k_weight),
-            -1.0 if eps is None else float(eps), _ptr(positions), n_axes, _ptr(freq_axis),
-            _ptr(inv_freq), inv_freq.numel(), int(interleaved), _ptr(outs[0]), _ptr(outs[1]), nt,
-            H, Hk, d, sq, sk, so[0], so[1], _stream(dev)))
-    return outs[0], outs[1]
+    _call(lib.kda_qk_norm_rope, dev, q.data_ptr(), k.data_ptr(), dt, _addr(q_weight),
+          _addr(k_weight), -1.0 if eps is None else eps, positions.data_ptr(), n_axes,
+          _addr(freq_axis), inv_freq.data_ptr(), inv_freq.numel(), 1 if interleaved else 0,
+          q_out.data_ptr(), k_out.data_ptr(), nt, H, Hk, d, sq, sk, soq, sok)
+    return q_out, k_out
+
+
+def _rope_out(y, x, name):
+    if not isinstance(y, torch.Tensor) or y.shape != x.shape or y.dtype != x.dtype \
+            or y.device != x.device:
+        raise ValueError(f"{name} must have the shape, dtype and device of its input")
+    return _token_stride(y, name)
 
 
 def _linear_inputs(q, k, v, g, lead):
@@ -569,16 +595,29 @@ def linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale: float = 1.0
     if output_final_state:
         hT = _like(final_state_out, "final_state_out", (N, H, dv, dk), torch.float32, dev)
     fl |= int(flags)
-    with torch.cuda.device(dev):
-        if workspace is None:
+    if workspace is None:
+        with torch.cuda.device(dev):
             need = lib.kda_linear_chunk_fwd_workspace_size(NT, N, H, dt, fl)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    else:
         _need(workspace, "workspace", torch.uint8, dev)
-        _check(lib.kda_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), float(scale),
-                                        _ptr(h0), _ptr(cu_seqlens), N, B, T, H, Hk, dk, dv,
-                                        _ptr(o), _ptr(hT), _ptr(workspace), workspace.numel(),
-                                        _stream(dev), fl))
+    _call(_linear_chunk, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(), scale,
+          _addr(h0), _addr(cu_seqlens), N, B, T, H, Hk, dk, dv, o.data_ptr(), _addr(hT),
+          workspace.data_ptr(), workspace.numel(), fl)
     return o, hT
+
+
+# The stream is the last argument but one of these calls.
+def _linear_chunk(*a):
+    return lib.kda_linear_chunk_fwd(*a[:-2], a[-1], a[-2])
+
+
+def _linear_step(*a):
+    return lib.kda_linear_recurrent_step(*a[:-2], a[-1], a[-2])
+
+
+def _linear_multi_step(*a):
+    return lib.kda_linear_recurrent_multi_step(*a[:-2], a[-1], a[-2])
 
 
 def linear_recurrent_step(q, k, v, g, S, *, scale: float = 1.0, out=None):
@@ -591,9 +630,8 @@ def linear_recurrent_step(q, k, v, g, S, *, scale: float = 1.0, out=None):
     dt, H, Hk, dk, dv, fl = _linear_inputs(q, k, v, g, (N,))
     S = _like(S, "S", (N, H, dv, dk), torch.float32, dev)
     o = _like(out, "out", v.shape, v.dtype, dev)
-    with torch.cuda.device(dev):
-        _check(lib.kda_linear_recurrent_step(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(g), float(scale),
-                                             _ptr(S), _ptr(o), N, H, Hk, dk, dv, _stream(dev), fl))
+    _call(_linear_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(), scale,
+          S.data_ptr(), o.data_ptr(), N, H, Hk, dk, dv, fl)
     return o
 
 
@@ -613,11 +651,8 @@ def linear_recurrent_multi_step(q, k, v, g, S, n_advance=None, *, scale: float =
         if n_advance.numel() != N:
             raise ValueError(f"n_advance must have {N} entries")
     o = _like(out, "out", v.shape, v.dtype, dev) if return_outputs else None
-    with torch.cuda.device(dev):
-        _check(lib.kda_linear_recurrent_multi_step(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(g),
-                                                   float(scale), _ptr(S), _ptr(o),
-                                                   _ptr(n_advance), N, T, H, Hk, dk, dv,
-                                                   _stream(dev), fl))
+    _call(_linear_multi_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(),
+          scale, S.data_ptr(), _addr(o), _addr(n_advance), N, T, H, Hk, dk, dv, fl)
     return o
 
 

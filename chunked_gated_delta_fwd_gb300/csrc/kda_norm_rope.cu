@@ -10,12 +10,12 @@
 //
 // With r = 1 / sqrt(mean(x^2) + eps) a channel's result is r (x_i A_i + x_p B_i), x_p the
 // other channel of its pair, A_i = w_i cos phi and B_i = -+ w_p sin phi: the same for all
-// heads of a token.  So a warp takes eight heads of one token, builds its lanes' A and B
+// heads of a token.  So a warp takes sixteen (fp32: eight) heads of one token, builds its lanes' A and B
 // once and then needs two multiplications a channel; the pair's other channel travels as
 // raw input, four shuffles a bf16 row.
 //
 // Bound by HBM: a row is read and written once.  A half warp holds a row, 8 channels a lane
-// (16-byte accesses for bf16), four rows of a lane in flight.  The CTAs stay resident and
+// (16-byte accesses), 128 bytes of a lane in flight.  The CTAs stay resident and
 // walk the tokens; the next tokens' sines and cosines (fp64, few lanes a clock, shared by
 // all heads) are formed between two barriers' worth of rows.
 #include "kda_internal.cuh"
@@ -25,10 +25,10 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeCtas = 4;        // resident CTAs an SM
+constexpr int kRopeCtas = 3;        // resident CTAs an SM
 constexpr int kRopeMaxTokens = 8;   // tokens of one step of a CTA (sine/cosine table)
-constexpr int kUnitHeads = 8;       // heads of one warp's unit: four rows of a half warp
-constexpr int kBatch = kUnitHeads / 2;
+// Heads of one warp's unit: 8 (bf16) or 4 (fp32) rows of a half warp, 128 bytes a lane.
+template <typename T> constexpr int unit_heads() { return 32 / (int)sizeof(T); }
 
 // cos and sin of p * f: the turn count in fp64, its fraction in fp32.
 __device__ __forceinline__ float2 cos_sin_turns(int32_t p, float f) {
@@ -76,12 +76,22 @@ __device__ __forceinline__ float2 pair_of(const uint32_t (&w)[8], int i) {
 template <typename T, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(const RopeArgs a,
                                                                            int* err) {
-  constexpr int kW = Words<T>::n;
-  __shared__ __align__(16) float2 cs[2][kRopeMaxTokens * kD / 2];  // (cos, sin) of (token, freq)
-  __shared__ __align__(16) float ws[2][kD];                        // norm weights of q and k
+  constexpr int kW = Words<T>::n, kUnitHeads = unit_heads<T>(), kBatch = kUnitHeads / 2;
+  // (cos, sin) of (token, frequency) and the norm weights of q and k, both laid out by the
+  // lane that reads them: what lanes read together is contiguous
+  __shared__ __align__(16) float2 cs[2][kRopeMaxTokens * kD / 2];
+  __shared__ __align__(16) float2 ws[2][kD / 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = blockIdx.x / a.splits, split = blockIdx.x - group * a.splits;
+  // steps of a.tokens tokens, strided over the CTAs: what is read at one time lies together
+  // (even shares of adjacent tokens took 137 us against 129 at 8192 tokens x 192 heads)
   const int64_t step = (int64_t)(gridDim.x / a.splits) * a.tokens;
+  int64_t t0 = (int64_t)group * a.tokens;
+  // half-split: lane l takes frequencies 8 l .. + 7 as four pairs; interleaved: 4 l .. + 3
+  auto place = [&](int i) {
+    return kInter ? (i & 3) * (a.F >> 2) + (i >> 2)
+                  : 2 * (((i & 7) >> 1) * (a.F >> 3) + (i >> 3)) + (i & 1);
+  };
   auto table = [&](int64_t t0, int buf) {
     const int nt = (int)min((int64_t)a.tokens, a.n_tokens - t0);
     for (int e = tid; e < nt * a.F; e += kRopeThreads) {
@@ -91,12 +101,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
         if (err) atomicExch(err, kDevErrBadAxis);
         ax = 0;
       }
-      cs[buf][e] = cos_sin_turns(__ldg(a.pos + ax * a.n_tokens + t0 + t), __ldg(a.freq + i));
+      cs[buf][t * a.F + place(i)] =
+          cos_sin_turns(__ldg(a.pos + ax * a.n_tokens + t0 + t), __ldg(a.freq + i));
     }
   };
-  int64_t t0 = (int64_t)group * a.tokens;
-  ws[tid >> 7][tid & (kD - 1)] =
-      tid < kD ? (a.wq ? a.wq[tid] : 1.f) : (a.wk ? a.wk[tid - kD] : 1.f);
+  if (tid < kD) {  // channels 2 c, 2 c + 1 of q (first 64 threads) and k
+    const float* w = tid < kD / 2 ? a.wq : a.wk;
+    const int c = tid & (kD / 2 - 1);
+    ws[tid / (kD / 2)][(c & 3) * 16 + (c >> 2)] =
+        w ? make_float2(w[2 * c], w[2 * c + 1]) : make_float2(1.f, 1.f);
+  }
   if (t0 < a.n_tokens) table(t0, 0);
   __syncthreads();
   const int hl = lane & 15, hf = lane >> 4;  // channels 8 hl .. 8 hl + 7 of every other head
@@ -129,20 +143,20 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
       float2 A[4], B[4];
       {
         const float2* c = cs[buf] + t * a.F;
-        const float* w = ws[isq ? 0 : 1];
+        const float2* w = ws[isq ? 0 : 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 wo = *reinterpret_cast<const float2*>(w + 8 * hl + 2 * i);
+          const float2 wo = w[16 * i + hl];
           if (!rot) {
             A[i] = wo;
             B[i] = make_float2(0.f, 0.f);
           } else if (kInter) {
-            const float2 z = c[4 * hl + i];
+            const float2 z = c[i * (a.F >> 2) + hl];
             A[i] = make_float2(wo.x * z.x, wo.y * z.x);
             B[i] = make_float2(-wo.y * z.y, wo.x * z.y);
           } else {
-            const float2 wp = *reinterpret_cast<const float2*>(w + 8 * other + 2 * i);
-            const float4 z = *reinterpret_cast<const float4*>(c + 8 * (low ? hl : other) + 2 * i);
+            const float2 wp = w[16 * i + other];
+            const float4 z = *reinterpret_cast<const float4*>(c + 2 * (i * F8 + (low ? hl : other)));
             const float sg = low ? -1.f : 1.f;
             A[i] = make_float2(wo.x * z.x, wo.y * z.z);
             B[i] = make_float2(sg * wp.x * z.y, sg * wp.y * z.w);
@@ -194,7 +208,8 @@ cudaError_t launch_rope_t(RopeArgs a, bool inter, bool norm, int* err, cudaStrea
   int sms = 152, dev = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int U = (a.Hq + kUnitHeads - 1) / kUnitHeads + (a.Hk + kUnitHeads - 1) / kUnitHeads;
+  constexpr int n = unit_heads<T>();
+  const int U = (a.Hq + n - 1) / n + (a.Hk + n - 1) / n;
   const int64_t most = (int64_t)sms * kRopeCtas;
   // tokens of a step: the fewest whose units fill the CTA's warps evenly, while there are
   // steps enough for every CTA
