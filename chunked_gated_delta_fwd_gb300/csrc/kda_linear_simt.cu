@@ -18,7 +18,6 @@ namespace {
 
 constexpr int C = kChunk;   // 64
 constexpr int D = kD;       // 128
-constexpr int LD = D + 4;   // padded row of a shared tile
 constexpr float kMinG = -200.f;
 
 // NaN stays NaN
@@ -59,75 +58,114 @@ __device__ __forceinline__ float decay_from_start(const Sums& s, int i) {
   return expf(s.hi[i] + s.lo[i]);
 }
 
-// rows t0 .. t0 + len - 1 of one head, columns c0 .. c0 + W - 1, zero rows up to `rows`
-template <typename T, int W, int LDW, int kThreads>
-__device__ __forceinline__ void load_tile(float (*dst)[LDW], const T* __restrict__ x, int64_t t0,
-                                          int rows, int len, int heads, int head, int c0) {
-  for (int e = threadIdx.x; e < rows * (W / 4); e += kThreads) {
-    const int r = e / (W / 4), c = 4 * (e % (W / 4));
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < len) load4(x + ((t0 + r) * heads + head) * D + c0 + c, y);
-    *reinterpret_cast<float4*>(&dst[r][c]) = make_float4(y[0], y[1], y[2], y[3]);
+// 16-byte chunk c4 of row r of a shared tile whose rows are W floats: chunks are permuted by
+// r / 4, so that lanes that read the same chunk of rows 4 apart do not meet in a bank.
+template <int W>
+__device__ __forceinline__ float4& tile_at(float* tile, int r, int c4) {
+  return reinterpret_cast<float4*>(tile + r * W)[c4 ^ ((r >> 2) & 7)];
+}
+
+// Rows t0 .. t0 + len - 1 of one head, columns c0 .. c0 + W - 1, into a shared tile of R
+// rows (zeros past len).  Every load is in flight before the first store.
+template <typename T, int R, int W, int kThreads>
+__device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ x, int64_t t0, int len,
+                                          int heads, int head, int c0) {
+  constexpr int n = R * (W / 4) / kThreads;
+  static_assert(n * kThreads == R * (W / 4), "whole loads a thread");
+  float y[n][4];
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const int e = threadIdx.x + i * kThreads, r = e / (W / 4), c = 4 * (e % (W / 4));
+    y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
+    if (r < len) load4(x + ((t0 + r) * heads + head) * D + c0 + c, y[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const int e = threadIdx.x + i * kThreads;
+    tile_at<W>(dst, e / (W / 4), e % (W / 4)) = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
   }
 }
 
 // ------------------------------------------------------------------ local states
-// One CTA per (chunk, head, 64 x 64 quarter): quarters let a short prompt with few heads
-// occupy four times the SMs; thread = 8 value rows x 4 key columns.
+// One CTA per (chunk, head, 64 value rows x kW key columns); thread = 8 value rows x 4 key
+// columns of each 64.  kW = 128 reads shared memory least often (4 reads of 16 bytes for 32
+// packed products); kW = 64 gives a short prompt twice the CTAs.
 constexpr int kLocThreads = 128;
 
-template <typename T>
+template <typename T, int kW>
 __global__ void __launch_bounds__(kLocThreads) lin_local_kernel(
     const T* __restrict__ k, const T* __restrict__ v, const float* __restrict__ g, int g_head,
     Plan plan, int H, int Hk, float* __restrict__ local, float* __restrict__ gam) {
-  constexpr int LQ = 64 + 4;
-  __shared__ __align__(16) float Ks[C][LQ], Vs[C][LQ];
+  constexpr int G = kW / 64;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  float* Ks = reinterpret_cast<float*>(smem_raw);  // [C][kW]
+  float* Vs = Ks + C * kW;                         // [C][64]
   __shared__ Sums sums;
   __shared__ double half;
-  const int chunk = blockIdx.x, h = blockIdx.y, v0 = 64 * (blockIdx.z >> 1),
-            k0 = 64 * (blockIdx.z & 1), tid = threadIdx.x;
+  const int chunk = blockIdx.x, h = blockIdx.y, v0 = 64 * (blockIdx.z & 1),
+            k0 = kW * (blockIdx.z >> 1), tid = threadIdx.x;
   if (chunk >= __ldg(plan.chunk_off + plan.n_seqs)) return;
   const int2 e = plan.tab[chunk];
   const int64_t t0 = e.x;
   const int len = e.y, hk = h / (H / Hk);
-  load_tile<T, 64, LQ, kLocThreads>(Ks, k, t0, C, len, Hk, hk, k0);
-  load_tile<T, 64, LQ, kLocThreads>(Vs, v, t0, C, len, H, h, v0);
+  load_tile<T, C, kW, kLocThreads>(Ks, k, t0, len, Hk, hk, k0);
+  load_tile<T, C, 64, kLocThreads>(Vs, v, t0, len, H, h, v0);
   chunk_sums(sums, &half, g, g_head, t0, len, H, h);
-  for (int x = tid; x < C * 16; x += kLocThreads) {
-    const int r = x >> 4, c = 4 * (x & 15);
+  for (int x = tid; x < C * 16; x += kLocThreads) {  // v_j times its decay to the chunk's end
+    const int r = x >> 4;
     const float w = decay(sums, C - 1, r);
-    float4& y = *reinterpret_cast<float4*>(&Ks[r][c]);
+    float4& y = tile_at<64>(Vs, r, x & 15);
     y = make_float4(w * y.x, w * y.y, w * y.z, w * y.w);
   }
   __syncthreads();
-  const int vr = 8 * (tid >> 4), kc = 4 * (tid & 15);
-  float2 acc[8][2] = {};
-#pragma unroll 4
+  const int vr = 8 * (tid >> 4), tx = tid & 15;
+  float2 acc[8][G][2] = {};
+#pragma unroll 2
   for (int j = 0; j < C; ++j) {
-    const float4 kk = *reinterpret_cast<const float4*>(&Ks[j][kc]);
-    const float4 va = *reinterpret_cast<const float4*>(&Vs[j][vr]);
-    const float4 vb = *reinterpret_cast<const float4*>(&Vs[j][vr + 4]);
+    const float4 va = tile_at<64>(Vs, j, vr >> 2);
+    const float4 vb = tile_at<64>(Vs, j, (vr >> 2) + 1);
     const float vv[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 x = make_float2(vv[i], vv[i]);
-      acc[i][0] = __ffma2_rn(x, make_float2(kk.x, kk.y), acc[i][0]);
-      acc[i][1] = __ffma2_rn(x, make_float2(kk.z, kk.w), acc[i][1]);
+    for (int b = 0; b < G; ++b) {
+      const float4 kk = tile_at<kW>(Ks, j, 16 * b + tx);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 x = make_float2(vv[i], vv[i]);
+        acc[i][b][0] = __ffma2_rn(x, make_float2(kk.x, kk.y), acc[i][b][0]);
+        acc[i][b][1] = __ffma2_rn(x, make_float2(kk.z, kk.w), acc[i][b][1]);
+      }
     }
   }
   const int64_t unit = (int64_t)chunk * H + h;
   float* out = local + unit * D * D;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<float4*>(out + (v0 + vr + i) * D + k0 + kc) =
-        make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+#pragma unroll
+    for (int b = 0; b < G; ++b)
+      *reinterpret_cast<float4*>(out + (v0 + vr + i) * D + k0 + 64 * b + 4 * tx) =
+          make_float4(acc[i][b][0].x, acc[i][b][0].y, acc[i][b][1].x, acc[i][b][1].y);
   if (blockIdx.z == 0 && tid == 0) gam[unit] = decay_from_start(sums, C - 1);
 }
 
+template <typename T, int kW>
+cudaError_t launch_local(const void* k, const void* v, const float* g, int g_head,
+                         const Plan& plan, int64_t chunks, int H, int Hk, float* local,
+                         float* gam, cudaStream_t s) {
+  constexpr int smem = C * (kW + 64) * (int)sizeof(float);
+  const cudaError_t e = cudaFuncSetAttribute(lin_local_kernel<T, kW>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  ProfScope prof_scope("kda_linear_local", s);
+  lin_local_kernel<T, kW><<<dim3((unsigned)chunks, (unsigned)H, 2 * (D / kW)), kLocThreads, smem,
+                            s>>>(static_cast<const T*>(k), static_cast<const T*>(v), g, g_head,
+                                 plan, H, Hk, local, gam);
+  return cudaGetLastError();
+}
+
 // ----------------------------------------------------------------------- the scan
-// local[c] becomes the state entering chunk c; one float4 of the state a thread, the next
-// chunks' locals in flight while one is added.
-constexpr int kScanThreads = 256, kScanAhead = 4;
+// local[c] becomes the state entering chunk c; one float4 of the state a thread, eight
+// chunks' locals in flight, the next eight on their way while eight are added.
+constexpr int kScanThreads = 256, kScanAhead = 8;
 
 __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
     const float* __restrict__ h0, Plan plan, int H, float* __restrict__ local,
@@ -141,148 +179,183 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
   auto at = [&](int c) {
     return reinterpret_cast<float4*>(local + ((int64_t)c * H + h) * D * D + e);
   };
-  for (int c = c0; c < c1; c += kScanAhead) {
-    float4 x[kScanAhead];
-    float a[kScanAhead];
+  float4 x[2][kScanAhead];
+  float a[2][kScanAhead];
+  auto fetch = [&](int b, int c) {
 #pragma unroll
     for (int i = 0; i < kScanAhead; ++i)
       if (c + i < c1) {
-        x[i] = *at(c + i);
-        a[i] = __ldg(gam + (int64_t)(c + i) * H + h);
+        x[b][i] = __ldcs(at(c + i));
+        a[b][i] = __ldg(gam + (int64_t)(c + i) * H + h);
       }
+  };
+  fetch(0, c0);
+  for (int c = c0; c < c1; c += 2 * kScanAhead) {
 #pragma unroll
-    for (int i = 0; i < kScanAhead; ++i)
-      if (c + i < c1) {
-        *at(c + i) = s;
-        s = make_float4(fmaf(a[i], s.x, x[i].x), fmaf(a[i], s.y, x[i].y), fmaf(a[i], s.z, x[i].z),
-                        fmaf(a[i], s.w, x[i].w));
-      }
+    for (int b = 0; b < 2; ++b) {
+      const int cb = c + b * kScanAhead;
+      fetch(b ^ 1, cb + kScanAhead);
+#pragma unroll
+      for (int i = 0; i < kScanAhead; ++i)
+        if (cb + i < c1) {
+          *at(cb + i) = s;
+          s = make_float4(fmaf(a[b][i], s.x, x[b][i].x), fmaf(a[b][i], s.y, x[b][i].y),
+                          fmaf(a[b][i], s.z, x[b][i].z), fmaf(a[b][i], s.w, x[b][i].w));
+        }
+    }
   }
   if (hT) *reinterpret_cast<float4*>(hT + unit * D * D + e) = s;
 }
 
 // --------------------------------------------------------------------- the outputs
-// One CTA per (chunk, head, 32 rows of the chunk): scores of its rows (32 x 64 over 128
-// channels), then both products of the output, 64 value columns at a time.
-constexpr int kOutThreads = 256, kOutRows = 32;
+// One CTA per (chunk, head, kR rows of the chunk): scores of its rows over 128 channels, then
+// both products of the output.  A thread owns kR / 16 rows and four adjacent columns of each
+// 64 (keys, then value columns): 16 x 16 threads.  Products over channels run on pairs of
+// channels, products over keys on pairs of columns (packed fp32).  kR = 64 reads each operand
+// from shared memory least often; kR = 16 gives a short prompt four times the CTAs.
+constexpr int kOutThreads = 256;
 
+template <int kR>
 struct OutSmem {
-  float Q[kOutRows][LD];
-  float X[C][LD];              // k, then v, then (as [64][LD]) halves of the state
-  float P[kOutRows][C + 4];
+  float Q[kR * D];
+  float X[C * D];  // k, then halves of the state, then v
+  float P[kR * C];
   Sums sums;
   double half;
 };
 
-template <typename T>
+template <typename T, int kR>
 __global__ void __launch_bounds__(kOutThreads) lin_out_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const float* __restrict__ g, int g_head, float scale, Plan plan, int H, int Hk,
     const float* __restrict__ states, T* __restrict__ o) {
+  constexpr int R = kR / 16;  // rows of a thread: ty + 16 i
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  OutSmem& sm = *reinterpret_cast<OutSmem*>(smem_raw);
-  const int chunk = blockIdx.x, h = blockIdx.y, r0 = kOutRows * blockIdx.z, tid = threadIdx.x;
+  OutSmem<kR>& sm = *reinterpret_cast<OutSmem<kR>*>(smem_raw);
+  const int chunk = blockIdx.x, h = blockIdx.y, r0 = kR * blockIdx.z, tid = threadIdx.x;
   if (chunk >= __ldg(plan.chunk_off + plan.n_seqs)) return;
   const int2 e = plan.tab[chunk];
   const int64_t t0 = e.x;
   const int len = e.y, hk = h / (H / Hk);
   if (r0 >= len) return;
-  const int cols = r0 + kOutRows;  // keys that the CTA's rows may see
-  load_tile<T, D, LD, kOutThreads>(sm.Q, q, t0 + r0, kOutRows, len - r0, Hk, hk, 0);
-  load_tile<T, D, LD, kOutThreads>(sm.X, k, t0, cols, len, Hk, hk, 0);
+  load_tile<T, kR, D, kOutThreads>(sm.Q, q, t0 + r0, len - r0, Hk, hk, 0);
+  load_tile<T, C, D, kOutThreads>(sm.X, k, t0, len, Hk, hk, 0);
   chunk_sums(sm.sums, &sm.half, g, g_head, t0, len, H, h);
-  const int ty = tid >> 4, tx = tid & 15;  // 16 x 16 threads: rows ty, ty + 16; columns tx + 16 c
-  {
-    float acc[2][4] = {};
-    const int nc = cols / 16;  // 2 or 4 column blocks
+  const int ty = tid >> 4, tx = tid & 15;
+  // acc[i][b] = row ty + 16 i of Q . row 4 tx + b of X, over 128 channels
+  auto dot_tile = [&](float (&acc)[R][4]) {
+    float2 a2[R][4] = {};
 #pragma unroll 4
-    for (int c = 0; c < D; c += 4) {
-      float4 qa[2];
+    for (int c = 0; c < D / 4; ++c) {
+      float4 qa[R];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) qa[i] = *reinterpret_cast<const float4*>(&sm.Q[ty + 16 * i][c]);
+      for (int i = 0; i < R; ++i) qa[i] = tile_at<D>(sm.Q, ty + 16 * i, c);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        if (b >= nc) break;
-        const float4 kk = *reinterpret_cast<const float4*>(&sm.X[tx + 16 * b][c]);
+        const float4 x = tile_at<D>(sm.X, 4 * tx + b, c);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          acc[i][b] = fmaf(qa[i].x, kk.x,
-                           fmaf(qa[i].y, kk.y, fmaf(qa[i].z, kk.z, fmaf(qa[i].w, kk.w, acc[i][b]))));
+        for (int i = 0; i < R; ++i)
+          a2[i][b] = __ffma2_rn(make_float2(qa[i].x, qa[i].y), make_float2(x.x, x.y),
+                                __ffma2_rn(make_float2(qa[i].z, qa[i].w), make_float2(x.z, x.w),
+                                           a2[i][b]));
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[i][b] = a2[i][b].x + a2[i][b].y;
+  };
+  {
+    float acc[R][4];
+    dot_tile(acc);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int r = ty + 16 * i;
+      float p[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int r = ty + 16 * i, j = tx + 16 * b;
-        if (b < nc) sm.P[r][j] = j <= r0 + r ? acc[i][b] * decay(sm.sums, r0 + r, j) : 0.f;
+        const int j = 4 * tx + b;
+        p[b] = j <= r0 + r ? acc[i][b] * decay(sm.sums, r0 + r, j) : 0.f;
       }
+      *reinterpret_cast<float4*>(&sm.P[r * C + 4 * tx]) = make_float4(p[0], p[1], p[2], p[3]);
+    }
   }
-  __syncthreads();
-  // O = e^G Q S: 64 value rows of S^T at a time, thread = 2 rows x 4 value columns of each half
-  float out[2][2][4] = {};  // [half][row][column]
+  // O = e^G Q S, 64 value rows of S^T at a time
+  float2 out[2][R][2];
   const float* S = states + ((int64_t)chunk * H + h) * D * D;
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
-    for (int x = tid; x < 64 * (D / 4); x += kOutThreads) {
-      const int r = x / (D / 4), c = 4 * (x % (D / 4));
-      *reinterpret_cast<float4*>(&sm.X[r][c]) =
-          *reinterpret_cast<const float4*>(S + (64 * hf + r) * D + c);
+    float4 y[8];  // C x D floats over 256 threads
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      y[x] = __ldg(reinterpret_cast<const float4*>(S + 64 * hf * D) + tid + x * kOutThreads);
+    __syncthreads();  // the tile's last reads are done
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int f = tid + x * kOutThreads;
+      tile_at<D>(sm.X, f >> 5, f & 31) = y[x];
     }
     __syncthreads();
-#pragma unroll 4
-    for (int c = 0; c < D; c += 4) {
-      float4 qa[2];
+    float acc[R][4];
+    dot_tile(acc);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) qa[i] = *reinterpret_cast<const float4*>(&sm.Q[ty + 16 * i][c]);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float4 ss = *reinterpret_cast<const float4*>(&sm.X[tx + 16 * b][c]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          out[hf][i][b] =
-              fmaf(qa[i].x, ss.x,
-                   fmaf(qa[i].y, ss.y, fmaf(qa[i].z, ss.z, fmaf(qa[i].w, ss.w, out[hf][i][b]))));
-      }
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float w = decay_from_start(sm.sums, r0 + ty + 16 * i);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      out[0][i][b] *= w;
-      out[1][i][b] *= w;
+    for (int i = 0; i < R; ++i) {
+      const float w = decay_from_start(sm.sums, r0 + ty + 16 * i);
+      out[hf][i][0] = make_float2(w * acc[i][0], w * acc[i][1]);
+      out[hf][i][1] = make_float2(w * acc[i][2], w * acc[i][3]);
     }
   }
-  // O += P V
-  load_tile<T, D, LD, kOutThreads>(sm.X, v, t0, cols, len, H, h, 0);
   __syncthreads();
-#pragma unroll 4
-  for (int j = 0; j < cols; ++j) {
-    const float p0 = sm.P[ty][j], p1 = sm.P[ty + 16][j];
+  // O += P V over the keys that these rows may see
+  load_tile<T, C, D, kOutThreads>(sm.X, v, t0, len, H, h, 0);
+  __syncthreads();
+  const int cols = min(C, r0 + kR);
+#pragma unroll 2
+  for (int j = 0; j < cols; j += 4) {
+    float4 p[R];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
+    for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(&sm.P[(ty + 16 * i) * C + j]);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float x = sm.X[j][64 * hf + tx + 16 * b];
-        out[hf][0][b] = fmaf(p0, x, out[hf][0][b]);
-        out[hf][1][b] = fmaf(p1, x, out[hf][1][b]);
+    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float4 x = tile_at<D>(sm.X, j + jj, 16 * hf + tx);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float pj = jj == 0 ? p[i].x : (jj == 1 ? p[i].y : (jj == 2 ? p[i].z : p[i].w));
+          out[hf][i][0] = __ffma2_rn(make_float2(pj, pj), make_float2(x.x, x.y), out[hf][i][0]);
+          out[hf][i][1] = __ffma2_rn(make_float2(pj, pj), make_float2(x.z, x.w), out[hf][i][1]);
+        }
       }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int r = r0 + ty + 16 * i;
     if (r < len) {
-      T* orow = o + ((t0 + r) * H + h) * D;
+      T* orow = o + ((t0 + r) * H + h) * D + 4 * tx;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          orow[64 * hf + tx + 16 * b] = from_f32<T>(scale * out[hf][i][b]);
+      for (int hf = 0; hf < 2; ++hf) {
+        const float y[4] = {scale * out[hf][i][0].x, scale * out[hf][i][0].y,
+                            scale * out[hf][i][1].x, scale * out[hf][i][1].y};
+        store4(orow + 64 * hf, y);
+      }
     }
   }
+}
+
+template <typename T, int kR>
+cudaError_t launch_out(const void* q, const void* k, const void* v, const float* g, int g_head,
+                       float scale, const Plan& plan, int64_t chunks, int H, int Hk,
+                       const float* states, void* o, cudaStream_t s) {
+  const int smem = (int)sizeof(OutSmem<kR>);
+  const cudaError_t e = cudaFuncSetAttribute(
+      lin_out_kernel<T, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  ProfScope prof_scope("kda_linear_out", s);
+  lin_out_kernel<T, kR><<<dim3((unsigned)chunks, (unsigned)H, C / kR), kOutThreads, smem, s>>>(
+      static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, g_head,
+      scale, plan, H, Hk, states, static_cast<T*>(o));
+  return cudaGetLastError();
 }
 
 template <typename T>
@@ -294,11 +367,14 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const float* g
   float* local = reinterpret_cast<float*>(static_cast<char*>(ws) + plan_bytes(n_tokens, n_seqs));
   float* gam = local + (size_t)chunks * H * D * D;
   cudaError_t e;
+  // few chunks and heads (the GPU holds two output CTAs an SM): smaller pieces
+  int sms = 152, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const bool few = chunks * H < 2 * sms;
   if (n_tokens > 0) {
-    ProfScope prof_scope("kda_linear_local", s);
-    lin_local_kernel<T><<<dim3((unsigned)chunks, (unsigned)H, 4), kLocThreads, 0, s>>>(
-        static_cast<const T*>(k), static_cast<const T*>(v), g, g_head, plan, H, Hk, local, gam);
-    e = cudaGetLastError();
+    e = few ? launch_local<T, 64>(k, v, g, g_head, plan, chunks, H, Hk, local, gam, s)
+            : launch_local<T, 128>(k, v, g, g_head, plan, chunks, H, Hk, local, gam, s);
     if (e != cudaSuccess) return e;
   }
   {
@@ -309,15 +385,9 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const float* g
     if (e != cudaSuccess) return e;
   }
   if (n_tokens == 0) return cudaSuccess;
-  e = cudaFuncSetAttribute(lin_out_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sizeof(OutSmem));
-  if (e != cudaSuccess) return e;
-  ProfScope prof_scope("kda_linear_out", s);
-  lin_out_kernel<T><<<dim3((unsigned)chunks, (unsigned)H, C / kOutRows), kOutThreads,
-                      sizeof(OutSmem), s>>>(static_cast<const T*>(q), static_cast<const T*>(k),
-                                            static_cast<const T*>(v), g, g_head, scale, plan, H,
-                                            Hk, local, static_cast<T*>(o));
-  return cudaGetLastError();
+  if (few)
+    return launch_out<T, 16>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
+  return launch_out<T, 64>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
 }
 
 }  // namespace
