@@ -22,18 +22,19 @@
 // reads 128 bytes of operands a clock when both come from shared memory.  So P and both
 // parts of Vw are A operands in tensor memory, k and v tiles are used as the tensor copies
 // left them (128-byte swizzled: the same bytes are a K-major operand where channels are
-// contracted and an MN-major one where tokens are), v reaches the lanes of its channels by
-// transposing matrix loads, and o leaves by a tensor copy from a staged tile instead of
-// 16-byte row pieces.
+// contracted and an MN-major one where tokens are), and v reaches the lanes of its channels
+// by transposing matrix loads.  What is left a chunk: 224 KB of MMA operands, 96 KB of
+// copies, about as much again by the groups below, of 5300 clocks (678 KB) that a chunk takes
+// at one chain an SM; at all SMs busy a chunk takes 5800 and HBM bounds it.
 //
-// o leaves from the tile that held q (its last reader, QS, is done by then), so the ring
-// holds two whole chunks of q, k and v.
+// The ring holds two whole chunks of q, k and v.
 //
-// Warps: copies, MMA issue, decay records, jobs; then groups of four, one warp of each on every SM sub-partition: weighted values, scores
-// -> P, outputs, state.  The record warp decodes the work and hands every chunk to the others
-// as one record in shared memory, and loops stay rolled: five roles run at once, and with
-// 94 KB of code (jobs decoded by every role, unrolled loops) instruction fetch bounded
-// the kernel, at 8500 clocks a chunk.
+// Warps: copies, MMA issue, decay records, jobs; then six groups of four, one warp of each on
+// every SM sub-partition: weighted values, scores -> P (two, half the keys each), outputs
+// (two, half the channels each), state.  The record warp hands every chunk to the others as
+// one record in shared memory.  Loops stay rolled and jobs are decoded once: eight roles run
+// at the same time, and with 94 KB of code instruction fetch bounded the kernel (8500 clocks
+// a chunk).
 //
 // Decays.  With L_i the sum of g inside a 32-token block up to i, U_j the sum behind j in
 // its block and T_b the block totals, every exponent but those inside a diagonal block is
@@ -109,7 +110,8 @@ enum {
   bOs = bQS + 1,       // O scaled
   bPV = bOs + 1,       // outputs complete
   bO = bPV + 1,        // outputs read out
-  bDrain = bO + 1,
+  bZ = bO + 1,         // rows past a sequence's end cleared
+  bDrain = bZ + 1,
   kBars = bDrain + 1
 };
 static_assert(kBars * 8 <= kBarBytes, "barriers");
@@ -357,12 +359,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool done = false;  // this role has come to the end of the work
 
   if (t == 0) {
-    // arrivals a phase: copies, commits and single threads 1, groups one a warp
+    // arrivals a phase: copies, commits and single threads 1, groups one a warp, records one
+    // a warp that reads them
+    constexpr uint32_t k4 = 3u << bVw | 1u << bS | 1u << bZ;
+    constexpr uint32_t k8 = 1u << bP | 1u << bOs | 1u << bO;
+    constexpr uint32_t kRec = 3u << bREmpty;
+#pragma unroll 1
     for (int i = 0; i < kBars; ++i) {
-      const bool group = i >= bVw && i <= bS;
-      const bool outs = i == bOs || i == bO;  // both output groups
-      const bool rec = i == bREmpty || i == bREmpty + 1;  // every warp that reads records
-      mbar_init(bar(i), rec ? (kOut ? 25 : 9) : (outs || i == bP ? 8 : (group ? 4 : (i == bJNext ? 2 : 1))));
+      const uint32_t b = 1u << i;
+      const int n = b & kRec ? (kOut ? 25 : 9) : (b & k8 ? 8 : (b & k4 ? 4 : (i == bJNext ? 2 : 1)));
+      mbar_init(bar(i), (uint32_t)n);
     }
     mbar_fence_init();
   }
@@ -389,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ copies in
     constexpr int kTiles = kOut ? 3 : 2;
     const uint32_t lead = elect_lane();
+    auto tile_at = [](int x) { return x == 0 ? tK : (kOut && x == 1 ? tQ : tV); };
     int it = 0, m = 0;  // chunks, tiles copied
     bool ok = true;
 #pragma unroll 1
@@ -406,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < j.tokens && ok; c += C, ++it) {
         if (c < ask && c + C >= ask) arrive(bJNext);
 #pragma unroll 1
-        for (int i = 0; i < kTiles; ++i) {  // in the order their slots fall free
+        for (int x = 0; x < kTiles; ++x) {  // in the order their slots fall free
+          const int i = tile_at(x);
           ok = it < 2 || wait_warp(empty(i, it), (uint32_t)(it >> 1) - 1);
           if (!ok) break;
           const void* tm = i == tK ? &tm_k : (i == tQ ? &tm_q : &tm_v);
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {  // copies in flight must land before the CTA exits
 #pragma unroll 1
       for (int x = max(0, m - 2 * kTiles); x < m; ++x)
-        wait(full(x % kTiles, x / kTiles), (uint32_t)(x / kTiles >> 1));
+        wait(full(tile_at(x % kTiles), x / kTiles), (uint32_t)(x / kTiles >> 1));
     }
   } else if (warp == 2) {
     // --------------------------------------------------------------------- records
@@ -633,18 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = (warp >> 2) - 1, w = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
     const int row = 32 * w + lane;
-    if (!kOut && group >= 1 && group <= 4) {
-      done = true;  // no scores and no outputs
-    } else if (group == 0) {
+    if (group == 0) {
       // -------------------------------------------------------- weighted values
       // Warp w takes value rows 32 w .. + 31: a transposing load brings 16 rows x 16
       // tokens, a lane holding token pairs of one row, as the 16-lane stores to tensor
-      // memory want them.  Rows of k and v past the sequence's end hold other tokens: they
-      // become zeros (and so do their weighted values), so that nothing of them (a NaN)
-      // meets this sequence.
+      // memory want them.  Rows of k and v past the sequence's end hold other tokens: the
+      // group clears them first, so that nothing of them (a NaN) meets this sequence.
       // matrix m of a load: value rows 8 (m & 1), tokens 8 (m >> 1); this lane's row of it
       const int mrow = (lane & 7) + 8 * (lane >> 4), mdv = (lane >> 3) & 1;
-      int it = 0;
+      int it = 0, cleared = 0;
 #pragma unroll 1
       for (int d = 0;; ++d) {
         if (!wait_warp(bRFull + (d & 1), (uint32_t)(d >> 1))) break;
@@ -656,10 +661,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ph = (uint32_t)(it >> 1);
           bool ok = wait_warp(full(tV, it), ph) &&
                     (it == 0 || wait_warp(bKV, (uint32_t)it - 1));  // the last chunk's are read
-          if (len < C) {
-            ok = ok && wait_warp(full(tK, it), ph) && (!kOut || wait_warp(bQK, (uint32_t)it));
-            // one outcome for the group, which meets at a barrier again below
-            ok = named_sync_and(2, kGroup, ok);
+          if (ok && len < C) {
+            ok = wait_warp(full(tK, it), ph) && (!kOut || wait_warp(bQK, (uint32_t)it));
+            if (!ok) break;
+#pragma unroll 1
+            for (int e = row; e < (C - len) * 16; e += kGroup) {
+              const uint32_t off = (uint32_t)((e >> 3) & 1) * kHalfTile +
+                                   (uint32_t)((len + (e >> 4)) * 128 + (e & 7) * 16);
+              *reinterpret_cast<uint4*>(sm + slot(tV, it) + off) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(sm + slot(tK, it) + off) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            arrive(bZ);
+            ok = wait_warp(bZ, (uint32_t)cleared++);
           }
           if (!ok) break;
           tc_fence_after();
@@ -690,45 +704,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int m = 0; m < 4; ++m)
                   weigh(y[m], wh[2 * i + (m >> 1)], wl[2 * i + (m >> 1)], hi[4 * i + m], lo[4 * i + m]);
               }
-              if (64 * hf + 64 > len) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const int q = pt + 8 * (i >> 1);
-                  const uint32_t keep = (q < len ? 0xffffu : 0u) | (q + 1 < len ? 0xffff0000u : 0u);
-                  hi[i] &= keep;
-                  lo[i] &= keep;
-                }
-              }
               const uint32_t dst = lanes + ((uint32_t)(16 * dh) << 16) + 32u * hf;
               tmem_st_16x128b_x8(dst + kT_Vhi, hi);
               tmem_st_16x128b_x8(dst + kT_Vlo, lo);
             }
-            if (len == C) {
-              tmem_wait_st();
-              tc_fence_before();
-              arrive(bVw + hf);
-            }
-          }
-          if (len < C) {
             tmem_wait_st();
             tc_fence_before();
-            named_sync(2, kGroup);  // the group has read the v tile
-#pragma unroll 1
-            for (int e = row; e < (C - len) * 16; e += kGroup) {
-              const uint32_t off = (uint32_t)((e >> 3) & 1) * kHalfTile +
-                                   (uint32_t)((len + (e >> 4)) * 128 + (e & 7) * 16);
-              *reinterpret_cast<uint4*>(sm + slot(tV, it) + off) = make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4*>(sm + slot(tK, it) + off) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            arrive(bVw);
-            arrive(bVw + 1);
+            arrive(bVw + hf);
           }
           ++it;
         }
         arrive(bREmpty + (d & 1));
       }
     } else if (group <= 2) {
+      if constexpr (kOut) {
       // ------------------------------------------------------------ scores -> P
       // Two groups, thread = token row and 64 of its keys, 32 at a time.  P (packed pairs)
       // overwrites the left half of the group's own scores, behind the scores being read.
@@ -795,7 +784,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         arrive(bREmpty + (d & 1));
       }
+      } else {
+        done = true;
+      }
     } else if (group <= 4) {
+      if constexpr (kOut) {
       // --------------------------------------------------------------- outputs
       // Two groups, thread = token row and 64 of its channels: O *= scale e^{G_i} between QS and PV; then the chunk goes to
       // the q tile's slot for the copy out, a partial one (its rows end inside the tile)
@@ -869,6 +862,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ++it;
+      }
+      } else {
+        done = true;
       }
     } else {
       // ----------------------------------------------------------------- state
