@@ -441,3 +441,47 @@ def test_segments_with_malformed_cu_seqlens(kda):
         chunk(kda, d, flags=kda.segment_chunks(1))
         with pytest.raises(kda.KdaError, match="cu_seqlens"):
             kda.get_device_error()
+
+
+# ---------------------------------------------------------------- how chains are drawn
+@pytest.mark.parametrize("n", [7, 40, 1100])
+def test_long_ragged_batches_against_the_fp32_cores(kda, n):
+    """More chains than SMs, four chunks each on average: drawn by ticket, the longest first
+    (1100 sequences: as they come).  Against the fp32-core path on the same inputs, itself
+    held to the oracle above."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    lens = np.random.default_rng(n).integers(0, 1300, n)
+    lens[0], lens[-1] = 0, 2500
+    H = 160 // n + 1 if n < 160 else 1
+    nt = int(lens.sum())
+    assert n * H > 152 and nt >= n * 512
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, k = unit(r(nt, H, 128)).bfloat16(), unit(r(nt, H, 128)).bfloat16()
+    v, g, h0 = r(nt, H, 128).bfloat16(), -0.2 * r(nt, H).abs(), 0.1 * r(n, H, 128, 128)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device="cuda")
+    kda.get_device_error()
+    o, hT = kda.linear_chunk_fwd(q, k, v, g, h0, cu)
+    ro, rh = kda.linear_chunk_fwd(q, k, v, g, h0, cu, flags=kda.FP32_CORES)
+    kda.get_device_error()
+    for x, y, tol in ((o, ro, 2.0 ** -8), (hT, rh, F32_REL_L2)):
+        rel = float((x.double() - y.double()).norm() / y.double().norm())
+        assert rel <= tol, rel
+        big = (x.double() - y.double()).abs().max() / y.double().square().mean().sqrt()
+        assert float(big) <= 40 * tol, float(big)
+
+
+def test_a_workspace_is_reused_from_call_to_call(kda):
+    """One workspace, full of garbage at first, for calls of all kinds in a row."""
+    ds = [make([700, 90, 1, 0, 512], 48, 48, torch.bfloat16, seed=101, h0=False),
+          make([4100], 2, 2, torch.bfloat16, seed=102), make([130, 70], 3, 3, torch.float32, seed=103)]
+    want = [chunk(kda, d) for d in ds]
+    need = max(kda.linear_chunk_fwd_workspace_size(int(d["cu"][-1]), len(d["cu"]) - 1,
+                                                   d["v"].shape[1], d["v"].dtype) for d in ds)
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for d, (o, hT) in zip(ds, want):
+            o2, h2 = chunk(kda, d, workspace=ws)
+            assert torch.equal(o, o2) and torch.equal(hT, h2)
+    with pytest.raises(kda.KdaError, match="WORKSPACE"):
+        chunk(kda, ds[1], workspace=ws[:256])
