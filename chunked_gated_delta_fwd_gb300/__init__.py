@@ -414,16 +414,16 @@ def recurrent_multi_step(q, k, v, g, beta, S, n_advance=None, *, out=None,
     return o
 
 
-def _call(fn, dev, *args):
-    """``fn(*args, stream)`` with ``dev`` current, on its current stream; raises on an error.
-    (Small calls are bound by what happens here: the device is switched only if it has to
-    be, pointers and the stream go over as plain integers.)"""
+def _call(fn, dev, *args, tail=()):
+    """``fn(*args, stream, *tail)`` with ``dev`` current, on its current stream; raises on an
+    error.  (Small calls are bound by what happens here: the device is switched only if it
+    has to be, pointers and the stream go over as plain integers.)"""
     index = dev.index
     if index == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index), *tail)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index), *tail)
     if status != 0:
         raise KdaError(status, lib.kda_last_error_string().decode())
 
@@ -509,7 +509,7 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     for x in lead:
         nt *= x
     _call(lib.kda_qk_norm_rope, dev, q.data_ptr(), k.data_ptr(), dt, _addr(q_weight),
-          _addr(k_weight), -1.0 if eps is None else eps, positions.data_ptr(), n_axes,
+          _addr(k_weight), -1.0 if eps is None else float(eps), positions.data_ptr(), n_axes,
           _addr(freq_axis), inv_freq.data_ptr(), inv_freq.numel(), 1 if interleaved else 0,
           q_out.data_ptr(), k_out.data_ptr(), nt, H, Hk, d, sq, sk, soq, sok)
     return q_out, k_out
@@ -530,6 +530,9 @@ def _linear_inputs(q, k, v, g, lead):
         _need(t, name, q.dtype, dev)
     _need(g, "g", torch.float32, dev)
     dt = _dtype_code(q)
+    if not lead or v.dim() != len(lead) + 2:
+        raise ValueError(f"q and v must be [..., heads, 128], got {tuple(q.shape)} and "
+                         f"{tuple(v.shape)}")
     Hk, dk, H, dv = q.shape[-2], q.shape[-1], v.shape[-2], v.shape[-1]
     if k.shape != q.shape:
         raise ValueError(f"k must have the shape of q {tuple(q.shape)}, got {tuple(k.shape)}")
@@ -542,9 +545,10 @@ def _linear_inputs(q, k, v, g, lead):
     raise ValueError(f"g must be {lead + (H,)} or ({H},), got {tuple(g.shape)}")
 
 
-def _like(t, name, shape, dtype, device):
-    """``t`` checked against what a result needs, or a new tensor."""
-    if t is None:
+def _like(t, name, shape, dtype, device, given=False):
+    """``t`` checked against what a result needs, or (unless it has to be ``given``) a new
+    tensor."""
+    if t is None and not given:
         return torch.empty(shape, dtype=dtype, device=device)
     _need(t, name, dtype, device)
     if tuple(t.shape) != tuple(shape):
@@ -596,28 +600,18 @@ def linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale: float = 1.0
         hT = _like(final_state_out, "final_state_out", (N, H, dv, dk), torch.float32, dev)
     fl |= int(flags)
     if workspace is None:
-        with torch.cuda.device(dev):
+        if dev.index == torch._C._cuda_getDevice():  # (the size depends on the SM count)
             need = lib.kda_linear_chunk_fwd_workspace_size(NT, N, H, dt, fl)
+        else:
+            with torch.cuda.device(dev):
+                need = lib.kda_linear_chunk_fwd_workspace_size(NT, N, H, dt, fl)
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8, dev)
-    _call(_linear_chunk, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(), scale,
-          _addr(h0), _addr(cu_seqlens), N, B, T, H, Hk, dk, dv, o.data_ptr(), _addr(hT),
-          workspace.data_ptr(), workspace.numel(), fl)
+    _call(lib.kda_linear_chunk_fwd, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
+          g.data_ptr(), float(scale), _addr(h0), _addr(cu_seqlens), N, B, T, H, Hk, dk, dv,
+          o.data_ptr(), _addr(hT), workspace.data_ptr(), workspace.numel(), tail=(fl,))
     return o, hT
-
-
-# The stream is the last argument but one of these calls.
-def _linear_chunk(*a):
-    return lib.kda_linear_chunk_fwd(*a[:-2], a[-1], a[-2])
-
-
-def _linear_step(*a):
-    return lib.kda_linear_recurrent_step(*a[:-2], a[-1], a[-2])
-
-
-def _linear_multi_step(*a):
-    return lib.kda_linear_recurrent_multi_step(*a[:-2], a[-1], a[-2])
 
 
 def linear_recurrent_step(q, k, v, g, S, *, scale: float = 1.0, out=None):
@@ -628,10 +622,10 @@ def linear_recurrent_step(q, k, v, g, S, *, scale: float = 1.0, out=None):
         raise ValueError(f"q must be [N, Hk, D], got {tuple(q.shape)}")
     N, dev = q.shape[0], q.device
     dt, H, Hk, dk, dv, fl = _linear_inputs(q, k, v, g, (N,))
-    S = _like(S, "S", (N, H, dv, dk), torch.float32, dev)
+    _like(S, "S", (N, H, dv, dk), torch.float32, dev, given=True)
     o = _like(out, "out", v.shape, v.dtype, dev)
-    _call(_linear_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(), scale,
-          S.data_ptr(), o.data_ptr(), N, H, Hk, dk, dv, fl)
+    _call(lib.kda_linear_recurrent_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
+          g.data_ptr(), float(scale), S.data_ptr(), o.data_ptr(), N, H, Hk, dk, dv, tail=(fl,))
     return o
 
 
@@ -645,14 +639,15 @@ def linear_recurrent_multi_step(q, k, v, g, S, n_advance=None, *, scale: float =
         raise ValueError(f"q must be [N, T, Hk, D], got {tuple(q.shape)}")
     N, T, dev = q.shape[0], q.shape[1], q.device
     dt, H, Hk, dk, dv, fl = _linear_inputs(q, k, v, g, (N, T))
-    S = _like(S, "S", (N, H, dv, dk), torch.float32, dev)
+    _like(S, "S", (N, H, dv, dk), torch.float32, dev, given=True)
     if n_advance is not None:
         _need(n_advance, "n_advance", torch.int32, dev)
         if n_advance.numel() != N:
             raise ValueError(f"n_advance must have {N} entries")
     o = _like(out, "out", v.shape, v.dtype, dev) if return_outputs else None
-    _call(_linear_multi_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(),
-          scale, S.data_ptr(), _addr(o), _addr(n_advance), N, T, H, Hk, dk, dv, fl)
+    _call(lib.kda_linear_recurrent_multi_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
+          g.data_ptr(), float(scale), S.data_ptr(), _addr(o), _addr(n_advance), N, T, H, Hk, dk,
+          dv, tail=(fl,))
     return o
 
 

@@ -825,7 +825,8 @@ kda_status_t kda_linear_chunk_fwd(const void* q, const void* k, const void* v, i
     NT = (int64_t)B * T;
     T_per_seq = T;
   }
-  if (T < 0 || NT > INT32_MAX - 2 * kda::kChunk || (int64_t)N * H > INT32_MAX)
+  // (room for the kernels' own steps past the last token and the last state)
+  if (T < 0 || NT > INT32_MAX - 65536 || (int64_t)N * H > INT32_MAX - 65536)
     return fail(KDA_ERR_INVALID_ARG, "%s: token or state count out of range", fn);
   if (flags & ~(unsigned)(KDA_LINEAR_HEAD_DECAY | KDA_LINEAR_FP32_CORES | KDA_LINEAR_SEQUENTIAL |
                           0xffff0000u))

@@ -264,6 +264,7 @@ def test_chunk_refusals(kda):
         dict(g=d["g"][0, :3].contiguous()), dict(h0=d["h0"][:, :2].contiguous()),
         dict(cu=d["cu"].long()), dict(cu=None), dict(cu=d["cu"][:1]), dict(v=d["v"].transpose(0, 1)),
         dict(q=d["q"].half(), k=d["k"].half(), v=d["v"].half()), dict(scale=float("nan")),
+        dict(q=d["q"][0], k=d["k"][0]), dict(v=d["v"][0]),
         dict(out=d["v"][:63]), dict(final_state_out=d["h0"][:, :2].contiguous()),
         dict(flags=1 << 12),
     ]
@@ -319,7 +320,7 @@ def test_step_refusals_and_no_sequences(kda):
     d = cuda(make([1] * 3, 4, 2, torch.float32, seed=71))
     S = d["h0"]
     ok = dict(q=d["q"], k=d["k"], v=d["v"], g=d["g"], S=S)
-    for x in (dict(q=d["q"][:2]), dict(k=d["k"].bfloat16()), dict(v=d["v"][:2]), dict(S=S[:2]),
+    for x in (dict(S=None), dict(q=d["q"][:2]), dict(k=d["k"].bfloat16()), dict(v=d["v"][:2]), dict(S=S[:2]),
               dict(S=S.bfloat16()), dict(S=S.transpose(2, 3)), dict(g=d["g"][:2]),
               dict(g=d["g"].bfloat16()), dict(out=d["v"][:2]), dict(scale=float("inf")),
               dict(q=d["q"].unsqueeze(1), k=d["k"].unsqueeze(1))):
