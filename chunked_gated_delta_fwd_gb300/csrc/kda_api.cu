@@ -812,6 +812,9 @@ kda_status_t kda_linear_chunk_fwd(const void* q, const void* k, const void* v, i
   const char* fn = "kda_linear_chunk_fwd";
   kda_status_t st = linear_heads(fn, dtype, scale, H, Hk, dk, dv);
   if (st != KDA_OK) return st;
+  // (room for the kernels' own steps past the last token and the last state)
+  if (T < 0 || T > INT32_MAX - 65536)
+    return fail(KDA_ERR_INVALID_ARG, "%s: token or state count out of range", fn);
   int N;
   int64_t NT, T_per_seq = 0;
   if (cu_seqlens) {
@@ -825,8 +828,7 @@ kda_status_t kda_linear_chunk_fwd(const void* q, const void* k, const void* v, i
     NT = (int64_t)B * T;
     T_per_seq = T;
   }
-  // (room for the kernels' own steps past the last token and the last state)
-  if (T < 0 || NT > INT32_MAX - 65536 || (int64_t)N * H > INT32_MAX - 65536)
+  if (NT > INT32_MAX - 65536 || (int64_t)N * H > INT32_MAX - 65536)
     return fail(KDA_ERR_INVALID_ARG, "%s: token or state count out of range", fn);
   if (flags & ~(unsigned)(KDA_LINEAR_HEAD_DECAY | KDA_LINEAR_FP32_CORES | KDA_LINEAR_SEQUENTIAL |
                           0xffff0000u))

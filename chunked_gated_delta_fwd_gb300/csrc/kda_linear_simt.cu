@@ -87,28 +87,26 @@ __device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ x, i
 }
 
 // ------------------------------------------------------------------ local states
-// One CTA per (chunk, head, 64 value rows x kW key columns); thread = 8 value rows x 4 key
-// columns of each 64.  kW = 128 reads shared memory least often (4 reads of 16 bytes for 32
-// packed products); kW = 64 gives a short prompt twice the CTAs.
+// One CTA per (chunk, head, 64 value rows); thread = 8 value rows x 4 key columns of each
+// 64: 4 shared-memory reads of 16 bytes for 32 packed products.
 constexpr int kLocThreads = 128;
 
-template <typename T, int kW>
+template <typename T>
 __global__ void __launch_bounds__(kLocThreads) lin_local_kernel(
     const T* __restrict__ k, const T* __restrict__ v, const float* __restrict__ g, int g_head,
     Plan plan, int H, int Hk, float* __restrict__ local, float* __restrict__ gam) {
-  constexpr int G = kW / 64;
+  constexpr int G = D / 64;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  float* Ks = reinterpret_cast<float*>(smem_raw);  // [C][kW]
-  float* Vs = Ks + C * kW;                         // [C][64]
+  float* Ks = reinterpret_cast<float*>(smem_raw);  // [C][D]
+  float* Vs = Ks + C * D;                         // [C][64]
   __shared__ Sums sums;
   __shared__ double half;
-  const int chunk = blockIdx.x, h = blockIdx.y, v0 = 64 * (blockIdx.z & 1),
-            k0 = kW * (blockIdx.z >> 1), tid = threadIdx.x;
+  const int chunk = blockIdx.x, h = blockIdx.y, v0 = 64 * blockIdx.z, tid = threadIdx.x;
   if (chunk >= __ldg(plan.chunk_off + plan.n_seqs)) return;
   const int2 e = plan.tab[chunk];
   const int64_t t0 = e.x;
   const int len = e.y, hk = h / (H / Hk);
-  load_tile<T, C, kW, kLocThreads>(Ks, k, t0, len, Hk, hk, k0);
+  load_tile<T, C, D, kLocThreads>(Ks, k, t0, len, Hk, hk, 0);
   load_tile<T, C, 64, kLocThreads>(Vs, v, t0, len, H, h, v0);
   chunk_sums(sums, &half, g, g_head, t0, len, H, h);
   for (int x = tid; x < C * 16; x += kLocThreads) {  // v_j times its decay to the chunk's end
@@ -127,7 +125,7 @@ __global__ void __launch_bounds__(kLocThreads) lin_local_kernel(
     const float vv[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
     for (int b = 0; b < G; ++b) {
-      const float4 kk = tile_at<kW>(Ks, j, 16 * b + tx);
+      const float4 kk = tile_at<D>(Ks, j, 16 * b + tx);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 x = make_float2(vv[i], vv[i]);
@@ -142,21 +140,21 @@ __global__ void __launch_bounds__(kLocThreads) lin_local_kernel(
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int b = 0; b < G; ++b)
-      *reinterpret_cast<float4*>(out + (v0 + vr + i) * D + k0 + 64 * b + 4 * tx) =
+      *reinterpret_cast<float4*>(out + (v0 + vr + i) * D + 64 * b + 4 * tx) =
           make_float4(acc[i][b][0].x, acc[i][b][0].y, acc[i][b][1].x, acc[i][b][1].y);
   if (blockIdx.z == 0 && tid == 0) gam[unit] = decay_from_start(sums, C - 1);
 }
 
-template <typename T, int kW>
+template <typename T>
 cudaError_t launch_local(const void* k, const void* v, const float* g, int g_head,
                          const Plan& plan, int64_t chunks, int H, int Hk, float* local,
                          float* gam, cudaStream_t s) {
-  constexpr int smem = C * (kW + 64) * (int)sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(lin_local_kernel<T, kW>,
+  constexpr int smem = C * (D + 64) * (int)sizeof(float);
+  const cudaError_t e = cudaFuncSetAttribute(lin_local_kernel<T>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   ProfScope prof_scope("kda_linear_local", s);
-  lin_local_kernel<T, kW><<<dim3((unsigned)chunks, (unsigned)H, 2 * (D / kW)), kLocThreads, smem,
+  lin_local_kernel<T><<<dim3((unsigned)chunks, (unsigned)H, D / 64), kLocThreads, smem,
                             s>>>(static_cast<const T*>(k), static_cast<const T*>(v), g, g_head,
                                  plan, H, Hk, local, gam);
   return cudaGetLastError();
@@ -212,7 +210,7 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
 // both products of the output.  A thread owns kR / 16 rows and four adjacent columns of each
 // 64 (keys, then value columns): 16 x 16 threads.  Products over channels run on pairs of
 // channels, products over keys on pairs of columns (packed fp32).  kR = 64 reads each operand
-// from shared memory least often; kR = 16 gives a short prompt four times the CTAs.
+// from shared memory least often; kR = 16 gives the shortest prompts four times the CTAs.
 constexpr int kOutThreads = 256;
 
 template <int kR>
@@ -367,14 +365,11 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const float* g
   float* local = reinterpret_cast<float*>(static_cast<char*>(ws) + plan_bytes(n_tokens, n_seqs));
   float* gam = local + (size_t)chunks * H * D * D;
   cudaError_t e;
-  // few chunks and heads (the GPU holds two output CTAs an SM): smaller pieces
   int sms = 152, dev = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const bool few = chunks * H < 2 * sms;
   if (n_tokens > 0) {
-    e = few ? launch_local<T, 64>(k, v, g, g_head, plan, chunks, H, Hk, local, gam, s)
-            : launch_local<T, 128>(k, v, g, g_head, plan, chunks, H, Hk, local, gam, s);
+    e = launch_local<T>(k, v, g, g_head, plan, chunks, H, Hk, local, gam, s);
     if (e != cudaSuccess) return e;
   }
   {
@@ -385,7 +380,10 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const float* g
     if (e != cudaSuccess) return e;
   }
   if (n_tokens == 0) return cudaSuccess;
-  if (few)
+  // Few chunks and heads: the rows of a chunk are spread over four CTAs, each of which reads
+  // all of its keys, state and values (whole pass, kR = 64 -> 16: 1 and 16 units of a chunk
+  // and head 31.6 -> 26.8 and 32.9 -> 27.8 us; 24 units 34.0 -> 37.3, 64 units 36.0 -> 47.0).
+  if (chunks * H * 8 <= sms)
     return launch_out<T, 16>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
   return launch_out<T, 64>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
 }

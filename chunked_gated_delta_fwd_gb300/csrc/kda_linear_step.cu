@@ -9,10 +9,14 @@
 // state is stored as it is after the first n_advance tokens, the outputs of all T are
 // written (the verify and the commit pass of speculative decoding in one).
 //
-// Bound by HBM: 2 x 64 KiB of state per head.  Eight lanes share a row (four 16-byte
+// Bound by HBM: 2 x 64 KiB of state per head (one token, 512 x 96 states: 930 us, 7.0 TB/s;
+// 5 tokens of 96 x 48 states: 92 us, 6.8 TB/s).  Eight lanes share a row (four 16-byte
 // pieces a lane, each warp access four whole 128-byte segments), a lane keeps kSlots rows in
 // flight, and the rows' dot products meet by a halving exchange inside the eight lanes.
-// Fewer lanes a row than a warp's 32 keep the exchange short: 4 shuffles for 16 rows.
+// Fewer lanes a row than a warp's 32 keep the exchange short: 4 shuffles for 16 rows.  The
+// tokens' vectors sit in shared memory and the products are packed pairs, which keeps the
+// token walk behind the state's traffic (5 tokens: 114 us with v read from global memory
+// row by row, 98 us with single products).
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -29,7 +33,7 @@ __global__ void __launch_bounds__(kLsThreads) linear_step_kernel(
     const float* __restrict__ g, int g_head, float scale, float* __restrict__ S,
     T* __restrict__ o, const int32_t* __restrict__ n_advance, int H, int rep, int Tn) {
   constexpr int kT = kMulti ? kLsMaxT : 1;
-  __shared__ __align__(16) float tq[kT][kD], tk[kT][kD];
+  __shared__ __align__(16) float tq[kT][kD], tk[kT][kD], tv[kT][kD];
   __shared__ float ta[kT];
   const int64_t unit = blockIdx.x;  // n * H + h
   const int n = (int)(unit / H), h = (int)(unit - (int64_t)n * H);
@@ -62,6 +66,8 @@ __global__ void __launch_bounds__(kLsThreads) linear_step_kernel(
         make_float4(scale * x[0], scale * x[1], scale * x[2], scale * x[3]);
     load4(k + row * kD + c, x);
     *reinterpret_cast<float4*>(&tk[t][c]) = make_float4(x[0], x[1], x[2], x[3]);
+    load4(v + (((int64_t)n * nT + t) * H + h) * kD + c, x);
+    *reinterpret_cast<float4*>(&tv[t][c]) = make_float4(x[0], x[1], x[2], x[3]);
   }
   if (tid < nT) ta[tid] = expf(__ldg(g + (g_head ? (int64_t)h : ((int64_t)n * nT + tid) * H + h)));
   __syncthreads();
@@ -71,12 +77,13 @@ __global__ void __launch_bounds__(kLsThreads) linear_step_kernel(
 #pragma unroll 1
     for (int t = 0; t < nT; ++t) {
       const int64_t vrow = (((int64_t)n * nT + t) * H + h) * kD;
-      const float a = ta[t];
+      const float2 aa = make_float2(ta[t], ta[t]);
       float vj[kSlots], d[kSlots];
+      float2 d2[kSlots];  // even and odd channels apart: packed products
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
-        vj[i] = to_f32(v[vrow + row_of(pass, i)]);
-        d[i] = 0.f;
+        vj[i] = tv[t][row_of(pass, i)];
+        d2[i] = make_float2(0.f, 0.f);
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
@@ -85,13 +92,18 @@ __global__ void __launch_bounds__(kLsThreads) linear_step_kernel(
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
           float4& x = s[i][m];
-          x.x = fmaf(vj[i], kk.x, a * x.x);
-          x.y = fmaf(vj[i], kk.y, a * x.y);
-          x.z = fmaf(vj[i], kk.z, a * x.z);
-          x.w = fmaf(vj[i], kk.w, a * x.w);
-          d[i] = fmaf(qq.x, x.x, fmaf(qq.y, x.y, fmaf(qq.z, x.z, fmaf(qq.w, x.w, d[i]))));
+          const float2 vv = make_float2(vj[i], vj[i]);
+          const float2 lo =
+              __ffma2_rn(vv, make_float2(kk.x, kk.y), __fmul2_rn(aa, make_float2(x.x, x.y)));
+          const float2 hi =
+              __ffma2_rn(vv, make_float2(kk.z, kk.w), __fmul2_rn(aa, make_float2(x.z, x.w)));
+          d2[i] = __ffma2_rn(make_float2(qq.x, qq.y), lo,
+                             __ffma2_rn(make_float2(qq.z, qq.w), hi, d2[i]));
+          x = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
       }
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) d[i] = d2[i].x + d2[i].y;
       if (t + 1 == adv) {
 #pragma unroll
         for (int i = 0; i < kSlots; ++i)
@@ -118,8 +130,11 @@ void launch_step_t(const void* q, const void* k, const void* v, const float* g, 
   int sms = 152, dev = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // few states: two CTAs share a state's rows, so that its latency is one pass's
-  const dim3 grid((unsigned)units, units * 4 <= sms ? 2u : 1u);
+  // at most one state an SM: two CTAs share its rows, so that the latency is one pass's
+  // (8, 76, 152 states, one CTA -> two: one token 3.5 -> 2.7, 3.5 -> 2.7, 3.8 -> 3.7 us,
+  // 16 tokens 10.3 -> 6.4, 10.4 -> 6.5, 10.6 -> 8.7); beyond, the second CTA only repeats the
+  // tokens' vectors (2 tokens, 384 states: 7.4 -> 8.0 us)
+  const dim3 grid((unsigned)units, units <= sms ? 2u : 1u);
   const auto fn = multi ? linear_step_kernel<T, true> : linear_step_kernel<T, false>;
   fn<<<grid, kLsThreads, 0, s>>>(static_cast<const T*>(q), static_cast<const T*>(k),
                                  static_cast<const T*>(v), g, g_head, scale, S,

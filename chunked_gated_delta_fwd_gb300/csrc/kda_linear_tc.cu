@@ -1171,13 +1171,18 @@ cudaError_t run(const CUtensorMap* tm, const LinArgs& a, int64_t items, const ch
 
 }  // namespace
 
-// Chunks of a segment, 0: sequences are not cut.
+// Chunks of a segment, 0: sequences are not cut.  Cutting costs two more small launches and
+// reads k and v twice: 8 chunks of one head 28.5 uncut, 38.6 us cut, 16 chunks 47.8 and 39.9,
+// 16 chunks of 38 heads 48 and 44.  Into two segments (51 to 76 chains of 152 SMs) it gains
+// what the state pass saves over a whole one: 64 heads, 16, 32 and 128 chunks 49, 87 and 319
+// uncut, 62, 95 and 292 cut; 76 heads, 64 chunks 166 and 169.
 int linear_segment_chunks(int64_t n_tokens, int n_seqs, int H, int forced, bool sequential) {
   if (sequential || n_tokens == 0) return 0;
   if (forced > 0) return forced;
   const int64_t sms = sm_count(), chains = (int64_t)n_seqs * H;
   const int64_t chunks = (n_tokens / C + n_seqs) / n_seqs;  // of an average sequence
-  if (2 * chains > sms || chunks < 16) return 0;
+  const int64_t at_least = 3 * chains <= sms ? 16 : 96;
+  if (2 * chains > sms || chunks < at_least) return 0;
   int64_t P = sms / chains;
   if (P > chunks / 4) P = chunks / 4;
   return (int)((chunks + P - 1) / P);
@@ -1218,7 +1223,9 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
   }
   if (seg_chunks <= 0) {
     // Chains of different lengths, several a CTA: drawn by ticket where a chain is long enough
-    // to make up for clearing the counter.
+    // to make up for the ordering launch (in the order given -> by ticket: 2 sequences of 300
+    // and 900 tokens, 96 heads 45.8 -> 37.9 us; two of 600 44.5 -> 47.4; 8 of 65 to 975, 48
+    // heads 60 -> 58; 4 of 300, 96 heads 46.4 -> 48.7; from 40 chains an SM no difference).
     const int64_t chains = (int64_t)n_seqs * H;
     if (cu && n_seqs > 1 && chains > sm_count() && n_tokens >= (int64_t)n_seqs * 4 * C) {
       a.ticket = static_cast<int*>(ws);
