@@ -5,7 +5,7 @@
 //     local = sum_j e^{G_C - G_j} k_j v_j^T              (every chunk on its own)
 //     S_in  = running state over the chunks' locals       (elementwise scan)
 //     O_i   = scale (e^{G_i} S_in^T q_i + sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j)
-// Three launches after the plan.  Only the scan walks a sequence in order, and it does
+// Three launches after the plan, each begun while the one before ends.  Only the scan walks a sequence in order, and it does
 // nothing but add: products over the whole prompt run at once, also with one head.
 //
 // Exponents are differences of running sums.  A gate may take g to -inf, so g is held at
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kLocThreads) lin_local_kernel(
   __shared__ Sums sums;
   __shared__ double half;
   const int chunk = blockIdx.x, h = blockIdx.y, v0 = 64 * blockIdx.z, tid = threadIdx.x;
+  wait_previous();
   if (chunk >= __ldg(plan.chunk_off + plan.n_seqs)) return;
   const int2 e = plan.tab[chunk];
   const int64_t t0 = e.x;
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kLocThreads) lin_local_kernel(
       }
     }
   }
+  release_next();
   const int64_t unit = (int64_t)chunk * H + h;
   float* out = local + unit * D * D;
 #pragma unroll
@@ -154,10 +156,9 @@ cudaError_t launch_local(const void* k, const void* v, const float* g, int g_hea
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   ProfScope prof_scope("kda_linear_local", s);
-  lin_local_kernel<T><<<dim3((unsigned)chunks, (unsigned)H, D / 64), kLocThreads, smem,
-                            s>>>(static_cast<const T*>(k), static_cast<const T*>(v), g, g_head,
-                                 plan, H, Hk, local, gam);
-  return cudaGetLastError();
+  return launch_chained(lin_local_kernel<T>, dim3((unsigned)chunks, (unsigned)H, D / 64),
+                        kLocThreads, smem, s, static_cast<const T*>(k), static_cast<const T*>(v),
+                        g, g_head, plan, H, Hk, local, gam);
 }
 
 // ----------------------------------------------------------------------- the scan
@@ -171,6 +172,7 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
   const int64_t unit = blockIdx.x;  // n * H + h
   const int n = (int)(unit / H), h = (int)(unit - (int64_t)n * H);
   const int64_t e = 4 * ((int64_t)blockIdx.y * kScanThreads + threadIdx.x);
+  wait_previous();
   const int c0 = __ldg(plan.chunk_off + n), c1 = __ldg(plan.chunk_off + n + 1);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (h0) s = *reinterpret_cast<const float4*>(h0 + unit * D * D + e);
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
         }
     }
   }
+  release_next();
   if (hT) *reinterpret_cast<float4*>(hT + unit * D * D + e) = s;
 }
 
@@ -231,6 +234,7 @@ __global__ void __launch_bounds__(kOutThreads) lin_out_kernel(
   extern __shared__ __align__(16) unsigned char smem_raw[];
   OutSmem<kR>& sm = *reinterpret_cast<OutSmem<kR>*>(smem_raw);
   const int chunk = blockIdx.x, h = blockIdx.y, r0 = kR * blockIdx.z, tid = threadIdx.x;
+  wait_previous();
   if (chunk >= __ldg(plan.chunk_off + plan.n_seqs)) return;
   const int2 e = plan.tab[chunk];
   const int64_t t0 = e.x;
@@ -350,10 +354,10 @@ cudaError_t launch_out(const void* q, const void* k, const void* v, const float*
       lin_out_kernel<T, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   ProfScope prof_scope("kda_linear_out", s);
-  lin_out_kernel<T, kR><<<dim3((unsigned)chunks, (unsigned)H, C / kR), kOutThreads, smem, s>>>(
-      static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), g, g_head,
-      scale, plan, H, Hk, states, static_cast<T*>(o));
-  return cudaGetLastError();
+  return launch_chained(lin_out_kernel<T, kR>, dim3((unsigned)chunks, (unsigned)H, C / kR),
+                        kOutThreads, smem, s, static_cast<const T*>(q), static_cast<const T*>(k),
+                        static_cast<const T*>(v), g, g_head, scale, plan, H, Hk, states,
+                        static_cast<T*>(o));
 }
 
 template <typename T>
@@ -374,16 +378,16 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const float* g
   }
   {
     ProfScope prof_scope("kda_linear_scan", s);
-    lin_scan_kernel<<<dim3((unsigned)((int64_t)n_seqs * H), D * D / 4 / kScanThreads),
-                      kScanThreads, 0, s>>>(h0, plan, H, local, gam, hT);
-    e = cudaGetLastError();
+    e = launch_chained(lin_scan_kernel,
+                       dim3((unsigned)((int64_t)n_seqs * H), D * D / 4 / kScanThreads),
+                       kScanThreads, 0, s, h0, plan, H, local, gam, hT);
     if (e != cudaSuccess) return e;
   }
   if (n_tokens == 0) return cudaSuccess;
   // Few chunks and heads: the rows of a chunk are spread over four CTAs, each of which reads
-  // all of its keys, state and values (whole pass, kR = 64 -> 16: 1 and 16 units of a chunk
-  // and head 31.6 -> 26.8 and 32.9 -> 27.8 us; 24 units 34.0 -> 37.3, 64 units 36.0 -> 47.0).
-  if (chunks * H * 8 <= sms)
+  // all of its keys, state and values (whole pass, kR = 64 -> 16, by chunks x heads: 2 x 1
+  // 31.2 -> 26.0 us, 2 x 16 32.2 -> 27.7, 2 x 24 33.3 -> 36.8, 5 x 16 35.2 -> 46.4).
+  if (chunks * H * 4 <= sms)
     return launch_out<T, 16>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
   return launch_out<T, 64>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
 }

@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 3) tmem_alloc(smem_addr(tmem_slot), 512);
   tc_fence_before();
+  wait_previous();
+  release_next();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -988,6 +990,7 @@ constexpr int kMaxOrder = 1024;
 __global__ void __launch_bounds__(kMaxOrder) lin_order_kernel(LinArgs a, int* ticket, int* order) {
   __shared__ int len[kMaxOrder];
   const int n = threadIdx.x;
+  release_next();
   if (n == 0) *ticket = 0;
   if (n < a.n_seqs) {
     int64_t t0, t1;
@@ -1015,6 +1018,7 @@ __global__ void __launch_bounds__(1024) lin_seg_plan_kernel(LinArgs a, int L, in
   __shared__ int warp_sums[32];
   __shared__ int carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  release_next();
   if (tid == 0) carry = 0;
   __syncthreads();
   for (int b = 0; b < a.n_seqs; b += blockDim.x) {
@@ -1064,7 +1068,7 @@ __global__ void __launch_bounds__(1024) lin_seg_plan_kernel(LinArgs a, int L, in
   }
 }
 
-constexpr int kScanThreads = 256;
+constexpr int kScanThreads = 256, kScanAhead = 8;
 __global__ void __launch_bounds__(kScanThreads) lin_seg_scan_kernel(
     const int* __restrict__ first, int H, const float* __restrict__ h0,
     const float* __restrict__ s_end,
@@ -1072,17 +1076,30 @@ __global__ void __launch_bounds__(kScanThreads) lin_seg_scan_kernel(
   const int64_t unit = blockIdx.x;
   const int n = (int)(unit / H), h = (int)(unit - (int64_t)n * H);
   const int64_t e = 4 * ((int64_t)blockIdx.y * kScanThreads + threadIdx.x);
+  wait_previous();
+  release_next();
   const int f0 = __ldg(first + n), f1 = __ldg(first + n + 1);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (h0) s = *reinterpret_cast<const float4*>(h0 + unit * D * D + e);
   if (f0 < f1) *reinterpret_cast<float4*>(s_in + ((int64_t)f0 * H + h) * D * D + e) = s;
-  for (int f = f0; f + 1 < f1; ++f) {
-    const int64_t at = ((int64_t)f * H + h) * D * D + e;
-    const float4 x = *reinterpret_cast<const float4*>(s_end + at);
-    const float d = f == f0 ? 0.f : __ldg(decay + (int64_t)f * H + h);
-    s = f == f0 ? x : make_float4(fmaf(d, s.x, x.x), fmaf(d, s.y, x.y), fmaf(d, s.z, x.z),
-                                  fmaf(d, s.w, x.w));
-    *reinterpret_cast<float4*>(s_in + at + (int64_t)H * D * D) = s;
+  for (int fb = f0; fb + 1 < f1; fb += kScanAhead) {
+    float4 x[kScanAhead];
+    float d[kScanAhead];
+#pragma unroll
+    for (int i = 0; i < kScanAhead; ++i)
+      if (fb + i + 1 < f1) {
+        const int64_t unit_f = (int64_t)(fb + i) * H + h;
+        x[i] = *reinterpret_cast<const float4*>(s_end + unit_f * D * D + e);
+        d[i] = __ldg(decay + unit_f);
+      }
+#pragma unroll
+    for (int i = 0; i < kScanAhead; ++i)
+      if (fb + i + 1 < f1) {
+        s = fb + i == f0 ? x[i]
+                         : make_float4(fmaf(d[i], s.x, x[i].x), fmaf(d[i], s.y, x[i].y),
+                                       fmaf(d[i], s.z, x[i].z), fmaf(d[i], s.w, x[i].w));
+        *reinterpret_cast<float4*>(s_in + ((int64_t)(fb + i + 1) * H + h) * D * D + e) = s;
+      }
   }
 }
 
@@ -1157,35 +1174,40 @@ int sm_count() {
 }
 
 template <bool kOut>
-cudaError_t run(const CUtensorMap* tm, const LinArgs& a, int64_t items, const char* name,
-                cudaStream_t s) {
+cudaError_t run(const CUtensorMap* tm, const LinArgs& a, int64_t items, bool chained,
+                const char* name, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(
       lin_tc_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   ProfScope prof_scope(name, s);
-  lin_tc_kernel<kOut><<<(unsigned)(items < sms ? items : sms), kThreads, kSmemBytes, s>>>(
-      tm[0], tm[1], tm[2], a);
+  const dim3 grid((unsigned)(items < sms ? items : sms));
+  if (chained)
+    return launch_chained(lin_tc_kernel<kOut>, grid, kThreads, kSmemBytes, s, tm[0], tm[1], tm[2],
+                          a);
+  lin_tc_kernel<kOut><<<grid, kThreads, kSmemBytes, s>>>(tm[0], tm[1], tm[2], a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Chunks of a segment, 0: sequences are not cut.  Cutting costs two more small launches and
-// reads k and v twice: 8 chunks of one head 28.5 uncut, 38.6 us cut, 16 chunks 47.8 and 39.9,
-// 16 chunks of 38 heads 48 and 44.  Into two segments (51 to 76 chains of 152 SMs) it gains
-// what the state pass saves over a whole one: 64 heads, 16, 32 and 128 chunks 49, 87 and 319
-// uncut, 62, 95 and 292 cut; 76 heads, 64 chunks 166 and 169.
+// Chunks of a segment, 0: sequences are not cut.  As many segments as SMs, if that pays for
+// three more launches and a second trip through k and v (in segments of L chunks it takes
+// about as long as 6 + 2 L uncut ones).  Uncut -> cut: one head, 6, 8, 16 and 64 chunks 24.0 ->
+// 25.0, 28.8 -> 25.0, 47.8 -> 25.3 and 162 -> 32 us; 38 heads, 8 (L = 2), 12 (3), 16 (4) and 32
+// (8) chunks 28.9 -> 32.9, 38.4 -> 37.0, 48.0 -> 42.2 and 86.7 -> 62.8.  Two segments (51 to 76
+// chains of 152 SMs) gain what the state pass saves over a whole one: 64 heads, 32, 48, 64 and
+// 128 chunks 88 -> 93, 126 -> 127, 165 -> 159 and 319 -> 287.
 int linear_segment_chunks(int64_t n_tokens, int n_seqs, int H, int forced, bool sequential) {
   if (sequential || n_tokens == 0) return 0;
   if (forced > 0) return forced;
   const int64_t sms = sm_count(), chains = (int64_t)n_seqs * H;
+  if (2 * chains > sms) return 0;
   const int64_t chunks = (n_tokens / C + n_seqs) / n_seqs;  // of an average sequence
-  const int64_t at_least = 3 * chains <= sms ? 16 : 96;
-  if (2 * chains > sms || chunks < at_least) return 0;
-  int64_t P = sms / chains;
-  if (P > chunks / 4) P = chunks / 4;
-  return (int)((chunks + P - 1) / P);
+  const int64_t P = sms / chains < chunks ? sms / chains : chunks;
+  const int64_t L = (chunks + P - 1) / P;
+  if (chunks < (3 * chains <= sms ? 6 + 2 * L : 64)) return 0;
+  return (int)L;
 }
 
 size_t linear_tc_workspace_bytes(int64_t n_tokens, int n_seqs, int H, int seg_chunks) {
@@ -1240,7 +1262,7 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
       }
       if (e != cudaSuccess) return e;
     }
-    return run<true>(tm, a, chains, "kda_linear_tc", s);
+    return run<true>(tm, a, chains, a.order != nullptr, "kda_linear_tc", s);
   }
   const SegLayout l = seg_layout(ws, n_tokens, n_seqs, H, seg_chunks);
   {
@@ -1256,17 +1278,17 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
   a.s_end = l.s_end;
   a.seg_decay = l.decay;
   a.ticket = l.tickets;
-  e = run<false>(tm, a, (int64_t)l.cap * H, "kda_linear_tc_state", s);
+  e = run<false>(tm, a, (int64_t)l.cap * H, true, "kda_linear_tc_state", s);
   if (e != cudaSuccess) return e;
   {
     ProfScope prof_scope("kda_linear_seg_scan", s);
-    lin_seg_scan_kernel<<<dim3((unsigned)((int64_t)n_seqs * H), D * D / 4 / kScanThreads),
-                          kScanThreads, 0, s>>>(l.first, H, h0, l.s_end, l.decay, l.s_in);
-    e = cudaGetLastError();
+    e = launch_chained(lin_seg_scan_kernel,
+                       dim3((unsigned)((int64_t)n_seqs * H), D * D / 4 / kScanThreads),
+                       kScanThreads, 0, s, l.first, H, h0, l.s_end, l.decay, l.s_in);
     if (e != cudaSuccess) return e;
   }
   a.ticket = l.tickets + 1;
-  return run<true>(tm, a, (int64_t)l.cap * H, "kda_linear_tc", s);
+  return run<true>(tm, a, (int64_t)l.cap * H, true, "kda_linear_tc", s);
 }
 
 }  // namespace kda
