@@ -4,8 +4,10 @@
 //     (a, b) = (y_i, y_{i+F})  or  (y_{2i}, y_{2i+1}),   phi = pos[axis_i][t] * f_i
 //     (a, b) <- (a cos phi - b sin phi, a sin phi + b cos phi),  i < F
 // and the channels from 2F on pass through.  Everything is fp32 but the angle: at
-// position 2^20 an fp32 product is off by 0.06 rad, so it is taken in fp64, reduced to
-// a fraction of a turn there, and only the fraction goes to the fp32 sine and cosine.
+// position 2^20 an fp32 product is off by 0.06 rad.  A CTA takes every f_i / (2 pi) once, in
+// fp64, as a 64-bit fraction of a turn; position times fraction modulo 2^64 is then the
+// fraction of a turn of phi, off by |pos| 2^-64, whole turns gone (an fp64 product and reduction
+// for each angle instead: 39.5 us in the 40-head case below; fp64 has a few lanes an SM).
 // One rounding, at the store.
 //
 // With r = 1 / sqrt(mean(x^2) + eps) a channel's result is r (x_i A_i + x_p B_i), x_p the
@@ -17,8 +19,8 @@
 // Bound by HBM: a row is read and written once (8192 tokens x 192 heads bf16: 127 us, 6.3 TB/s;
 // 10007 tokens of 40 heads out of a packed projection: 39 us, 5.2 TB/s).  A half warp holds
 // a row, 8 channels a lane (16-byte accesses), 128 bytes of a lane in flight.  The CTAs stay
-// resident and walk the tokens; the next tokens' sines and cosines (fp64, few lanes a clock, shared by
-// all heads) are formed between two barriers' worth of rows.
+// resident and walk the tokens; the next tokens' sines and cosines (shared by all heads) are formed
+// between two barriers' worth of rows.
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -31,12 +33,20 @@ constexpr int kRopeMaxTokens = 8;   // tokens of one step of a CTA (sine/cosine 
 // Heads of one warp's unit: 8 (bf16) or 4 (fp32) rows of a half warp, 128 bytes a lane.
 template <typename T> constexpr int unit_heads() { return 32 / (int)sizeof(T); }
 
-// cos and sin of p * f: the turn count in fp64, its fraction in fp32.
-__device__ __forceinline__ float2 cos_sin_turns(int32_t p, float f) {
-  double u = (double)p * (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-  u -= rint(u);
+// The part of f / (2 pi) behind the point, in 2^-64; 1 / (2 pi) as two doubles, so that a
+// position of 2^31 keeps its phase next to any frequency.
+__device__ __forceinline__ uint64_t turns_of(float f) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+  const double u = (double)f * kHi, rest = fma((double)f, kHi, -u) + (double)f * kLo;
+  return __double2ull_rz((u - floor(u)) * 0x1p64) +  // (2^64 saturates)
+         (uint64_t)__double2ll_rn(rest * 0x1p64);
+}
+// cos and sin of p turns: the upper 32 bits, signed, are within half a turn of 0.  `bad` is 0,
+// or NaN for a frequency that is not finite.
+__device__ __forceinline__ float2 cos_sin_turns(int32_t p, uint64_t turns, float bad) {
+  const uint64_t x = (uint64_t)(int64_t)p * turns + 0x80000000ull;
   float s, c;
-  sincospif(2.f * (float)u, &s, &c);
+  sincospif(fmaf((float)(int32_t)(x >> 32), 0x1p-31f, bad), &s, &c);
   return make_float2(c, s);
 }
 
@@ -82,6 +92,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
   // lane that reads them: what lanes read together is contiguous
   __shared__ __align__(16) float2 cs[2][kRopeMaxTokens * kD / 2];
   __shared__ __align__(16) float2 ws[2][kD / 2];
+  struct Freq {
+    uint64_t turns;
+    float bad;
+    int axis, place;
+  };
+  __shared__ Freq fr[kD / 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = blockIdx.x / a.splits, split = blockIdx.x - group * a.splits;
   // steps of a.tokens tokens, strided over the CTAs: what is read at one time lies together
@@ -93,19 +109,26 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
     return kInter ? (i & 3) * (a.F >> 2) + (i >> 2)
                   : 2 * (((i & 7) >> 1) * (a.F >> 3) + (i >> 3)) + (i & 1);
   };
+  const int fi = tid & (kD / 2 - 1);  // this thread's frequency
   auto table = [&](int64_t t0, int buf) {
     const int nt = (int)min((int64_t)a.tokens, a.n_tokens - t0);
-    for (int e = tid; e < nt * a.F; e += kRopeThreads) {
-      const int t = e / a.F, i = e - t * a.F;
-      int ax = a.axis ? __ldg(a.axis + i) : 0;
-      if (ax < 0 || ax >= a.n_axes) {  // reported; axis 0 keeps the read in bounds
-        if (err) atomicExch(err, kDevErrBadAxis);
-        ax = 0;
-      }
-      cs[buf][t * a.F + place(i)] =
-          cos_sin_turns(__ldg(a.pos + ax * a.n_tokens + t0 + t), __ldg(a.freq + i));
-    }
+    if (fi >= a.F) return;
+    const Freq f = fr[fi];
+    const int32_t* pos = a.pos + f.axis * a.n_tokens + t0;
+#pragma unroll 1
+    for (int t = tid / (kD / 2); t < nt; t += kRopeThreads / (kD / 2))
+      cs[buf][t * a.F + f.place] = cos_sin_turns(__ldg(pos + t), f.turns, f.bad);
   };
+  if (tid < a.F) {
+    const float f = __ldg(a.freq + tid);
+    int ax = a.axis ? __ldg(a.axis + tid) : 0;
+    if (ax < 0 || ax >= a.n_axes) {  // reported; axis 0 keeps the read in bounds
+      if (err) atomicExch(err, kDevErrBadAxis);
+      ax = 0;
+    }
+    fr[tid] = Freq{turns_of(f), f - f, ax, place(tid)};
+  }
+  __syncthreads();
   if (tid < kD) {  // channels 2 c, 2 c + 1 of q (first 64 threads) and k
     const float* w = tid < kD / 2 ? a.wq : a.wk;
     const int c = tid & (kD / 2 - 1);

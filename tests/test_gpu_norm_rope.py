@@ -81,6 +81,35 @@ def test_frequencies_and_pairings(kda, dtype, interleaved, F):
     _case(kda, 37, 3, 2, dtype, F=F, interleaved=interleaved, seed=F)
 
 
+@pytest.mark.parametrize("dtype", DT, ids=IDS)
+def test_any_finite_frequency(kda, dtype):
+    """Frequencies below 0, above a turn a token, near 0 and 0; positions of both signs."""
+    gen = torch.Generator().manual_seed(21)
+    q = torch.randn(33, 2, 128, generator=gen).to(dtype)
+    k = torch.randn(33, 1, 128, generator=gen).to(dtype)
+    f = torch.tensor([-0.7, 40.5, 1e-7, 0.0, -1e-30, 6.2831855, 1e5, 1.0])
+    pos = torch.randint(-100000, 100000, (33,), generator=gen).to(torch.int32)
+    pos[:3] = torch.tensor([0, -(1 << 31), (1 << 31) - 1], dtype=torch.int64).to(torch.int32)
+    # at 2^31 x 1e5 rad the oracle's own fp64 angle is off by 2^-6: that frequency stays small there
+    f_far = f.clone()
+    f_far[6] = 0.5
+    for rows, freq in ((slice(0, 3), f_far), (slice(3, 33), f)):
+        qo, ko = kda.qk_norm_rope(q[rows].cuda(), k[rows].cuda(), pos[rows].cuda(), freq.cuda())
+        _check(qo, q[rows], pos[rows], freq, None, 1e-6, None, False)
+        _check(ko, k[rows], pos[rows], freq, None, 1e-6, None, False)
+
+
+@pytest.mark.parametrize("dtype", DT, ids=IDS)
+def test_a_frequency_that_is_not_finite_shows(kda, dtype):
+    q = torch.ones(5, 1, 128, dtype=dtype, device="cuda")
+    f = torch.ones(8, device="cuda")
+    f[3] = float("nan")
+    f[5] = float("inf")
+    qo, _ = kda.qk_norm_rope(q, q.clone(), torch.arange(5, dtype=torch.int32, device="cuda"), f)
+    bad = torch.isnan(qo).any(0).any(0).cpu()
+    assert bad.nonzero().flatten().tolist() == [3, 5, 11, 13]
+
+
 @pytest.mark.parametrize("nt,Hq,Hk", [(1, 1, 1), (1, 96, 96), (17, 2, 1), (5, 33, 11), (3, 64, 1)])
 @pytest.mark.parametrize("dtype", DT, ids=IDS)
 def test_token_and_head_counts(kda, nt, Hq, Hk, dtype):
