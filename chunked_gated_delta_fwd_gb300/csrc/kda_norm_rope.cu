@@ -12,12 +12,13 @@
 //
 // With r = 1 / sqrt(mean(x^2) + eps) a channel's result is r (x_i A_i + x_p B_i), x_p the
 // other channel of its pair, A_i = w_i cos phi and B_i = -+ w_p sin phi: the same for all
-// heads of a token.  So a warp takes sixteen (fp32: eight) heads of one token, builds its lanes' A and B
-// once and then needs two multiplications a channel; the pair's other channel travels as
+// heads of a token.  So a warp takes sixteen (fp32: eight) rows, heads of one token where there
+// are as many, builds its lanes' A and B once a token and then needs two multiplications a channel; the pair's other channel travels as
 // raw input, four shuffles a bf16 row.
 //
 // Bound by HBM: a row is read and written once (8192 tokens x 192 heads bf16: 127 us, 6.3 TB/s;
-// 10007 tokens of 40 heads out of a packed projection: 39 us, 5.2 TB/s).  A half warp holds
+// 10007 tokens of 40 heads out of a packed projection: 37 us, 5.5 TB/s; 65536 tokens of 1 + 1
+// heads 30 us, 2.3 TB/s: there the angles, 64 for two rows, bound it).  A half warp holds
 // a row, 8 channels a lane (16-byte accesses), 128 bytes of a lane in flight.  The CTAs stay
 // resident and walk the tokens; the next tokens' sines and cosines (shared by all heads) are formed
 // between two barriers' worth of rows.
@@ -29,9 +30,20 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeCtas = 3;        // resident CTAs an SM
-constexpr int kRopeMaxTokens = 8;   // tokens of one step of a CTA (sine/cosine table)
-// Heads of one warp's unit: 8 (bf16) or 4 (fp32) rows of a half warp, 128 bytes a lane.
-template <typename T> constexpr int unit_heads() { return 32 / (int)sizeof(T); }
+// Rows of a half warp in one unit of its warp, 128 bytes a lane.  kHeads of them belong to one
+// token: twice the rows (both half warps share a token, every other head each) or fewer (a half
+// warp walks tokens of its own), so that few heads fill a unit too.
+template <typename T> constexpr int unit_rows() { return 16 / (int)sizeof(T); }
+template <typename T, int kHeads> constexpr int unit_tokens() {
+  return 2 * unit_rows<T>() / kHeads;
+}
+// Tokens of one step of a CTA, (token, frequency) entries of its table.
+template <typename T, int kHeads> constexpr int max_tokens() {
+  return unit_tokens<T, kHeads>() == 1 ? 8 : 32;
+}
+template <typename T, int kHeads> constexpr int table_size() {
+  return max_tokens<T, kHeads>() * kD / 2;
+}
 
 // The part of f / (2 pi) behind the point, in 2^-64; 1 / (2 pi) as two doubles, so that a
 // position of 2^31 keeps its phase next to any frequency.
@@ -84,13 +96,16 @@ __device__ __forceinline__ float2 pair_of(const uint32_t (&w)[8], int i) {
   return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
 }
 
-template <typename T, bool kInter, bool kNorm>
+template <typename T, bool kInter, bool kNorm, int kHeads>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(const RopeArgs a,
                                                                            int* err) {
-  constexpr int kW = Words<T>::n, kUnitHeads = unit_heads<T>(), kBatch = kUnitHeads / 2;
+  constexpr int kW = Words<T>::n, kBatch = unit_rows<T>();
+  constexpr bool kShared = kHeads == 2 * kBatch;
+  constexpr int kRun = kShared ? kBatch : kHeads;  // rows of a half warp and token
+  constexpr int kTokens = unit_tokens<T, kHeads>(), kStep = kShared ? 2 : 1;
   // (cos, sin) of (token, frequency) and the norm weights of q and k, both laid out by the
   // lane that reads them: what lanes read together is contiguous
-  __shared__ __align__(16) float2 cs[2][kRopeMaxTokens * kD / 2];
+  __shared__ __align__(16) float2 cs[2][table_size<T, kHeads>()];
   __shared__ __align__(16) float2 ws[2][kD / 2];
   struct Freq {
     uint64_t turns;
@@ -142,31 +157,40 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
   const bool rot = hl < 2 * F8, low = hl < F8;
   // half-split pairs: the lane (of the half warp) with the other channels
   const int other = kInter || !rot ? hl : (low ? hl + F8 : hl - F8);
-  const int uq = (a.Hq + kUnitHeads - 1) / kUnitHeads, uk = (a.Hk + kUnitHeads - 1) / kUnitHeads;
+  const int uq = (a.Hq + kHeads - 1) / kHeads, uk = (a.Hk + kHeads - 1) / kHeads;
   const int U = uq + uk;
 #pragma unroll 1
   for (int buf = 0; t0 < a.n_tokens; t0 += step, buf ^= 1) {
     const int nt = (int)min((int64_t)a.tokens, a.n_tokens - t0);
 #pragma unroll 1
-    for (int u = warp + kRopeWarps * split; u < nt * U; u += kRopeWarps * a.splits) {
-      const int t = u / U, ub = u - t * U;
+    for (int u = warp + kRopeWarps * split; u < (nt + kTokens - 1) / kTokens * U;
+         u += kRopeWarps * a.splits) {
+      const int ut = u / U, ub = u - ut * U;
+      const int t = kShared ? ut : kTokens * ut + hf * (kTokens / 2);
       const bool isq = ub < uq;
-      const int H = isq ? a.Hq : a.Hk, h0 = (isq ? ub : ub - uq) * kUnitHeads + hf;
+      const int H = isq ? a.Hq : a.Hk, h0 = (isq ? ub : ub - uq) * kHeads + (kShared ? hf : 0);
       const T* src = (isq ? static_cast<const T*>(a.q) + (t0 + t) * a.sq
                           : static_cast<const T*>(a.k) + (t0 + t) * a.sk) + h0 * kD + 8 * hl;
       T* dst = (isq ? static_cast<T*>(a.qo) + (t0 + t) * a.sqo
                     : static_cast<T*>(a.ko) + (t0 + t) * a.sko) + h0 * kD + 8 * hl;
+      // row b of a half warp: its token (all in the step where the half warps share one), its head
+      auto row = [&](int b) {
+        return (kShared || t + b / kRun < nt) && h0 + b % kRun * kStep < H;
+      };
+      auto at = [&](int b, int64_t sq, int64_t sk) {
+        return (kRun == kBatch ? 0 : b / kRun * (isq ? sq : sk)) + b % kRun * (kStep * kD);
+      };
       uint32_t x[kBatch][kW];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
 #pragma unroll
         for (int i = 0; i < kW; ++i) x[b][i] = 0u;
-        if (h0 + 2 * b < H) load_words(src + 2 * b * kD, x[b]);
+        if (row(b)) load_words(src + at(b, a.sq, a.sk), x[b]);
       }
-      // this lane's coefficients (pairs of channels)
+      // this lane's coefficients (pairs of channels) for a token's rows
       float2 A[4], B[4];
-      {
-        const float2* c = cs[buf] + t * a.F;
+      auto coefficients = [&](int t) {
+        const float2* c = cs[buf] + (kShared || t < nt ? t : 0) * a.F;
         const float2* w = ws[isq ? 0 : 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -186,9 +210,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
             B[i] = make_float2(sg * wp.x * z.y, sg * wp.y * z.w);
           }
         }
-      }
+      };
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
+        if (b % kRun == 0) coefficients(t + b / kRun);
         float r = 1.f;
         if (kNorm) {
           float2 ss = make_float2(0.f, 0.f);
@@ -219,7 +244,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
           y[2 * i] = z.x;
           y[2 * i + 1] = z.y;
         }
-        if (h0 + 2 * b < H) store8(dst + 2 * b * kD, y);
+        if (row(b)) store8(dst + at(b, a.sqo, a.sko), y);
       }
     }
     if (t0 + step < a.n_tokens) table(t0 + step, buf ^ 1);
@@ -227,32 +252,57 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
   }
 }
 
-template <typename T>
-cudaError_t launch_rope_t(RopeArgs a, bool inter, bool norm, int* err, cudaStream_t s) {
-  int sms = 152, dev = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  constexpr int n = unit_heads<T>();
-  const int U = (a.Hq + n - 1) / n + (a.Hk + n - 1) / n;
-  const int64_t most = (int64_t)sms * kRopeCtas;
+int units_of_token(const RopeArgs& a, int heads) {
+  return (a.Hq + heads - 1) / heads + (a.Hk + heads - 1) / heads;
+}
+
+template <typename T, int kHeads>
+cudaError_t launch_rope_heads(RopeArgs a, bool inter, bool norm, int64_t most, int* err,
+                              cudaStream_t s) {
+  constexpr int kTokens = unit_tokens<T, kHeads>();
+  const int U = units_of_token(a, kHeads);
+  auto units = [&](int tokens) { return (tokens + kTokens - 1) / kTokens * U; };
   // tokens of a step: the fewest whose units fill the CTA's warps evenly, while there are
   // steps enough for every CTA (32 + 8 heads, one token a step -> this rule: 1024 tokens 8.6 ->
   // 7.6 us, 16384 tokens 106 -> 61.5)
   a.tokens = 1;
-  while (a.tokens < kRopeMaxTokens && (a.tokens * U) % kRopeWarps != 0 &&
+  while (a.tokens < max_tokens<T, kHeads>() &&
+         (a.tokens < kTokens || units(a.tokens) % kRopeWarps != 0) &&
          a.n_tokens >= 2 * a.tokens * most)
     a.tokens *= 2;
   const int64_t steps = (a.n_tokens + a.tokens - 1) / a.tokens;
   // few tokens: their heads are spread over several CTAs (one token, 96 + 96 heads: 5.3 us in
   // one CTA, 3.9 spread)
   a.splits = 1;
-  while (steps * a.splits * 2 <= most && a.splits * kRopeWarps < a.tokens * U) a.splits *= 2;
+  while (steps * a.splits * 2 <= most && a.splits * kRopeWarps < units(a.tokens)) a.splits *= 2;
   const int64_t groups = steps < most / a.splits ? steps : most / a.splits;
   using Fn = void (*)(const RopeArgs, int*);
-  static const Fn fn[2][2] = {{norm_rope_kernel<T, false, false>, norm_rope_kernel<T, false, true>},
-                              {norm_rope_kernel<T, true, false>, norm_rope_kernel<T, true, true>}};
+  static const Fn fn[2][2] = {
+      {norm_rope_kernel<T, false, false, kHeads>, norm_rope_kernel<T, false, true, kHeads>},
+      {norm_rope_kernel<T, true, false, kHeads>, norm_rope_kernel<T, true, true, kHeads>}};
   fn[inter][norm]<<<(unsigned)(groups * a.splits), kRopeThreads, 0, s>>>(a, err);
   return cudaGetLastError();
+}
+
+// Heads of a token in a unit: as many as fit (every row of a warp shares one token's
+// coefficients), or fewer where that leaves enough fewer rows of units empty and there are
+// tokens for them.  bf16, 16 -> 8 heads: 8 + 1 heads x 16384 tokens (16 of 32 rows) 29.6 -> 18.9
+// us, 16 + 2 (24 of 32) 38 -> 33, 24 + 4 (32 of 48) 48.5 -> 45, but 32 + 8 (40 of 48) 58 -> 63;
+// 8 -> 2 heads: 1 + 1 x 65536 55 -> 31, 4 + 2 (6 of 16) 62 -> 48, 6 + 3 x 40000 (10 of 16) 47 -> 55.
+template <typename T>
+cudaError_t launch_rope_t(const RopeArgs& a, bool inter, bool norm, int* err, cudaStream_t s) {
+  int sms = 152, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t most = (int64_t)sms * kRopeCtas;
+  constexpr int R = unit_rows<T>();
+  const int64_t all = (int64_t)units_of_token(a, 2 * R) * 2 * R,
+                half = (int64_t)units_of_token(a, R) * R, two = (int64_t)units_of_token(a, 2) * 2;
+  if (5 * two <= 2 * half && a.n_tokens >= unit_tokens<T, 2>() * most)
+    return launch_rope_heads<T, 2>(a, inter, norm, most, err, s);
+  if (4 * half <= 3 * all && a.n_tokens >= 2 * most)
+    return launch_rope_heads<T, R>(a, inter, norm, most, err, s);
+  return launch_rope_heads<T, 2 * R>(a, inter, norm, most, err, s);
 }
 
 }  // namespace

@@ -82,6 +82,16 @@ def test_frequencies_and_pairings(kda, dtype, interleaved, F):
 
 
 @pytest.mark.parametrize("dtype", DT, ids=IDS)
+@pytest.mark.parametrize("nt,Hq,Hk,F,interleaved,packed", [
+    (3701, 2, 1, 64, False, False), (3655, 1, 1, 24, True, True), (5003, 4, 2, 32, True, True),
+    (7301, 1, 1, 64, False, False), (1001, 8, 1, 64, False, True), (1537, 6, 3, 40, True, False),
+    (1825, 24, 4, 64, False, False), (3649, 3, 3, 8, False, True)])
+def test_few_heads_of_many_tokens(kda, dtype, nt, Hq, Hk, F, interleaved, packed):
+    """The units that hold rows of several tokens, with token counts that end inside one."""
+    _case(kda, nt, Hq, Hk, dtype, F=F, interleaved=interleaved, packed=packed, start=1000, seed=nt)
+
+
+@pytest.mark.parametrize("dtype", DT, ids=IDS)
 def test_any_finite_frequency(kda, dtype):
     """Frequencies below 0, above a turn a token, near 0 and 0; positions of both signs."""
     gen = torch.Generator().manual_seed(21)
