@@ -486,3 +486,59 @@ def test_a_workspace_is_reused_from_call_to_call(kda):
             assert torch.equal(o, o2) and torch.equal(hT, h2)
     with pytest.raises(kda.KdaError, match="WORKSPACE"):
         chunk(kda, ds[1], workspace=ws[:256])
+
+
+def test_every_path_captured_and_replayed_back_to_back(kda):
+    """Uncut, drawn by ticket, cut into segments and fp32 cores, one after another in one graph
+    on one workspace, replayed without a pause: a kernel that begins while the one before it
+    ends sees all that its call wrote, and leaves the next call's part alone."""
+    ds = [make([700, 90, 1, 0, 1300], 40, 40, torch.bfloat16, seed=111),
+          make([1300, 90, 1, 0, 1300], 40, 40, torch.bfloat16, seed=116),
+          make([3000], 2, 1, torch.bfloat16, seed=112), make([200], 3, 3, torch.bfloat16, seed=113),
+          make([130, 70], 3, 3, torch.float32, seed=114), make([900], 8, 8, torch.float32, seed=115)]
+    kda.profile_enable(True)
+    want = [chunk(kda, d) for d in ds]
+    ran = kda.profile_collect()
+    kda.profile_enable(False)
+    assert {"kda_linear_order", "kda_linear_tc_state", "kda_linear_out"} <= set(ran)
+    cs = [cuda(d) for d in ds]
+    need = max(kda.linear_chunk_fwd_workspace_size(int(d["cu"][-1]), len(d["cu"]) - 1,
+                                                   d["v"].shape[1], d["v"].dtype) for d in ds)
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda")
+    call = lambda c: kda.linear_chunk_fwd(c["q"], c["k"], c["v"], c["g"], c["h0"], c["cu"],  # noqa: E731
+                                          workspace=ws)
+    kda.get_device_error()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [call(c) for c in cs + cs[::-1]]
+    for _ in range(20):
+        graph.replay()
+    for (o, hT), (ro, rh) in zip(got, want + want[::-1]):
+        assert torch.equal(o, ro) and torch.equal(hT, rh)
+    for o, hT in got:
+        o.fill_(float("nan"))
+        hT.fill_(float("nan"))
+    graph.replay()
+    for (o, hT), (ro, rh) in zip(got, want + want[::-1]):
+        assert torch.equal(o, ro) and torch.equal(hT, rh)
+    kda.get_device_error()
+
+
+@pytest.mark.parametrize("T,H,cut", [(1024, 1, True), (1100, 19, False), (1500, 38, True),
+                                     (2300, 50, True), (8300, 51, True)])
+def test_lengths_around_the_cut(kda, T, H, cut):
+    """Prompts about as long as it takes to be cut (segments of one chunk and more), against the
+    uncut run."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v = unit(r(1, T, H, 128)).bfloat16(), unit(r(1, T, H, 128)).bfloat16(), r(1, T, H, 128).bfloat16()
+    g, h0 = -0.05 * r(1, T, H).abs(), 0.1 * r(1, H, 128, 128)
+    kda.profile_enable(True)
+    o, hT = kda.linear_chunk_fwd(q, k, v, g, h0)
+    ran = kda.profile_collect()
+    kda.profile_enable(False)
+    assert ("kda_linear_tc_state" in ran) == cut
+    ro, rh = kda.linear_chunk_fwd(q, k, v, g, h0, flags=kda.SEQUENTIAL)
+    kda.get_device_error()
+    assert errors(o, to64(ro))[0] <= 2.0 ** -8 and errors(hT, to64(rh))[0] <= F32_REL_L2

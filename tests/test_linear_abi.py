@@ -58,6 +58,7 @@ def test_linear_chunk_rejects_bad_arguments(kda):
     assert f(scale=float("nan")) == 1 and f(scale=float("inf")) == 1
     assert f(cu=FAKE, n_seqs=0) == 1 and f(cu=FAKE, n_seqs=2, B=2) == 1
     assert f(B=0) == 1 and f(T=-1) == 1 and f(T=1 << 31) == 1
+    assert f(B=4, T=1 << 62) == 1  # (their product is 0 in 64 bits)
     assert f(q=None) == 1 and f(g=None) == 1 and f(o=None) == 1 and f(ws=None) == 1
     assert f(q=FAKE + 8) == 4 and f(h0=FAKE + 4) == 4 and f(ws=FAKE + 16) == 4
     assert f(dtype=0, ws_bytes=16) == 5
