@@ -86,6 +86,32 @@ __device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ x, i
   }
 }
 
+// The same for fp32 without a stop in registers: the copies are on their way when this returns
+// (bf16 is converted, and is in place).
+template <int R, int kThreads>
+__device__ __forceinline__ void start_tile(float* dst, const float* __restrict__ x, int64_t t0,
+                                           int len, int heads, int head) {
+#pragma unroll
+  for (int i = 0; i < R * (D / 4) / kThreads; ++i) {
+    const int e = threadIdx.x + i * kThreads, r = e / (D / 4), c4 = e % (D / 4);
+    const float* src = x + ((t0 + (r < len ? r : 0)) * heads + head) * D + 4 * c4;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(&tile_at<D>(dst, r, c4));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src),
+                 "r"(r < len ? 16 : 0)  // no bytes read: zeros
+                 : "memory");
+  }
+}
+template <int R, int kThreads>
+__device__ __forceinline__ void start_tile(float* dst, const __nv_bfloat16* __restrict__ x,
+                                           int64_t t0, int len, int heads, int head) {
+  load_tile<__nv_bfloat16, R, D, kThreads>(dst, x, t0, len, heads, head, 0);
+}
+__device__ __forceinline__ void commit_tiles() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void wait_tiles() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 // ------------------------------------------------------------------ local states
 // One CTA per (chunk, head, 64 value rows); thread = 8 value rows x 4 key columns of each
 // 64: 4 shared-memory reads of 16 bytes for 32 packed products.
@@ -212,21 +238,25 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
 // One CTA per (chunk, head, kR rows of the chunk): scores of its rows over 128 channels, then
 // both products of the output.  A thread owns kR / 16 rows and four adjacent columns of each
 // 64 (keys, then value columns): 16 x 16 threads.  Products over channels run on pairs of
-// channels, products over keys on pairs of columns (packed fp32).  kR = 64 reads each operand
+// channels, products over keys on pairs of columns (packed fp32).  The next tile is copied
+// while one is multiplied
+// (1024 chunks x heads, the whole pass: 205 us with loads and products in turn, 199 like this).
+// What bounds it is shared memory: 8 reads of 16 bytes a lane for 32 packed products, at half
+// the rate of the products.  kR = 64 reads each operand
 // from shared memory least often; kR = 16 gives the shortest prompts four times the CTAs.
 constexpr int kOutThreads = 256;
 
 template <int kR>
 struct OutSmem {
   float Q[kR * D];
-  float X[C * D];  // k, then halves of the state, then v
+  float X[2][C * D];  // k and half a state's rows, then the other half and v
   float P[kR * C];
   Sums sums;
   double half;
 };
 
 template <typename T, int kR>
-__global__ void __launch_bounds__(kOutThreads) lin_out_kernel(
+__global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const float* __restrict__ g, int g_head, float scale, Plan plan, int H, int Hk,
     const float* __restrict__ states, T* __restrict__ o) {
@@ -240,21 +270,25 @@ __global__ void __launch_bounds__(kOutThreads) lin_out_kernel(
   const int64_t t0 = e.x;
   const int len = e.y, hk = h / (H / Hk);
   if (r0 >= len) return;
-  load_tile<T, kR, D, kOutThreads>(sm.Q, q, t0 + r0, len - r0, Hk, hk, 0);
-  load_tile<T, C, D, kOutThreads>(sm.X, k, t0, len, Hk, hk, 0);
+  const float* S = states + ((int64_t)chunk * H + h) * D * D;
+  start_tile<kR, kOutThreads>(sm.Q, q, t0 + r0, len - r0, Hk, hk);
+  start_tile<C, kOutThreads>(sm.X[0], k, t0, len, Hk, hk);
+  commit_tiles();
+  start_tile<C, kOutThreads>(sm.X[1], S, 0, C, 1, 0);
+  commit_tiles();
   chunk_sums(sm.sums, &sm.half, g, g_head, t0, len, H, h);
   const int ty = tid >> 4, tx = tid & 15;
   // acc[i][b] = row ty + 16 i of Q . row 4 tx + b of X, over 128 channels
-  auto dot_tile = [&](float (&acc)[R][4]) {
+  auto dot_tile = [&](float (&acc)[R][4], float* X) {
     float2 a2[R][4] = {};
-#pragma unroll 4
+#pragma unroll 2
     for (int c = 0; c < D / 4; ++c) {
       float4 qa[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) qa[i] = tile_at<D>(sm.Q, ty + 16 * i, c);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const float4 x = tile_at<D>(sm.X, 4 * tx + b, c);
+        const float4 x = tile_at<D>(X, 4 * tx + b, c);
 #pragma unroll
         for (int i = 0; i < R; ++i)
           a2[i][b] = __ffma2_rn(make_float2(qa[i].x, qa[i].y), make_float2(x.x, x.y),
@@ -267,9 +301,11 @@ __global__ void __launch_bounds__(kOutThreads) lin_out_kernel(
 #pragma unroll
       for (int b = 0; b < 4; ++b) acc[i][b] = a2[i][b].x + a2[i][b].y;
   };
+  wait_tiles<1>();
+  __syncthreads();
   {
     float acc[R][4];
-    dot_tile(acc);
+    dot_tile(acc, sm.X[0]);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int r = ty + 16 * i;
@@ -284,22 +320,17 @@ __global__ void __launch_bounds__(kOutThreads) lin_out_kernel(
   }
   // O = e^G Q S, 64 value rows of S^T at a time
   float2 out[2][R][2];
-  const float* S = states + ((int64_t)chunk * H + h) * D * D;
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
-    float4 y[8];  // C x D floats over 256 threads
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-      y[x] = __ldg(reinterpret_cast<const float4*>(S + 64 * hf * D) + tid + x * kOutThreads);
-    __syncthreads();  // the tile's last reads are done
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const int f = tid + x * kOutThreads;
-      tile_at<D>(sm.X, f >> 5, f & 31) = y[x];
-    }
-    __syncthreads();
+    wait_tiles<0>();
+    __syncthreads();  // a tile has landed, the other's last reads are done
+    if (hf == 0)
+      start_tile<C, kOutThreads>(sm.X[0], S + C * D, 0, C, 1, 0);
+    else
+      start_tile<C, kOutThreads>(sm.X[1], v, t0, len, H, h);
+    commit_tiles();
     float acc[R][4];
-    dot_tile(acc);
+    dot_tile(acc, sm.X[hf ^ 1]);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float w = decay_from_start(sm.sums, r0 + ty + 16 * i);
@@ -307,9 +338,8 @@ __global__ void __launch_bounds__(kOutThreads) lin_out_kernel(
       out[hf][i][1] = make_float2(w * acc[i][2], w * acc[i][3]);
     }
   }
-  __syncthreads();
   // O += P V over the keys that these rows may see
-  load_tile<T, C, D, kOutThreads>(sm.X, v, t0, len, H, h, 0);
+  wait_tiles<0>();
   __syncthreads();
   const int cols = min(C, r0 + kR);
 #pragma unroll 2
@@ -321,7 +351,7 @@ __global__ void __launch_bounds__(kOutThreads) lin_out_kernel(
     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const float4 x = tile_at<D>(sm.X, j + jj, 16 * hf + tx);
+        const float4 x = tile_at<D>(sm.X[1], j + jj, 16 * hf + tx);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const float pj = jj == 0 ? p[i].x : (jj == 1 ? p[i].y : (jj == 2 ? p[i].z : p[i].w));
