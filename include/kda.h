@@ -446,11 +446,11 @@ enum {
  *          included (the state is dropped there).
  *   scale  finite.
  * KDA_BF16 inputs run on the tensor cores in 128-token chunks (fp32 accumulation and state;
- * o within about one more bf16 rounding of the fp32 result, hT to fp32 accuracy), KDA_F32
- * inputs on fp32 CUDA cores.  When few (sequence, head) pairs would leave SMs idle, long
- * bf16 sequences are cut into segments that run at once (the result equals the
- * uncut one up to rounding); KDA_CHUNK_SEGMENT_CHUNKS(n) forces segments of n 128-token
- * chunks, KDA_LINEAR_SEQUENTIAL turns them off.  A non-finite q, k or v reaches outputs
+ * o within about one more bf16 rounding of the fp32 result; hT sums k v^T with each weighted
+ * v to 17 bits, 2e-6 relative), KDA_F32 inputs on fp32 CUDA cores.  Where (sequence, head)
+ * pairs alone would leave SMs idle, long bf16 sequences are cut into segments that run at
+ * once (the result equals the uncut one up to rounding); KDA_CHUNK_SEGMENT_CHUNKS(n) forces
+ * segments of n 128-token chunks, KDA_LINEAR_SEQUENTIAL turns them off.  A non-finite q, k or v reaches outputs
  * of its own sequence and head only; which rows of its 128-token chunk it reaches is not
  * specified.  cu_seqlens that does not run from 0 to NT without decreasing is reported by
  * kda_get_device_error; the outputs are then unspecified, nothing outside o and hT is
