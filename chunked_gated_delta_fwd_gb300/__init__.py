@@ -440,13 +440,14 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() < 3:
+    shape = t.shape
+    if len(shape) < 3:
         raise ValueError(f"{name} must be [..., H, 128]")
-    d, H = t.shape[-1], t.shape[-2]
+    H, d = shape[-2:]
     if t.is_contiguous():
         return H * d
     step = expect = None
-    for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+    for size, stride in zip(reversed(shape[:-2]), reversed(t.stride()[:-2])):
         if size == 1:
             continue
         if step is None:
@@ -472,37 +473,38 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     Returns ``(q_out, k_out)``; ``q_out=q, k_out=k`` works in place.
     """
     sq, sk = _token_stride(q, "q"), _token_stride(k, "k")
-    dev, lead = q.device, tuple(q.shape[:-2])
+    dev, shape, shape_k = q.device, q.shape, k.shape
+    lead = tuple(shape[:-2])
+    H, d = shape[-2:]
+    Hk, dk = shape_k[-2:]
     if k.device != dev or k.dtype != q.dtype:
         raise ValueError("q and k must have one dtype and device")
-    if tuple(k.shape[:-2]) != lead or k.shape[-1] != q.shape[-1]:
-        raise ValueError(f"k must be {lead} + (Hk, {q.shape[-1]}), got {tuple(k.shape)}")
+    if shape_k[:-2] != lead or dk != d:
+        raise ValueError(f"k must be {lead} + (Hk, {d}), got {tuple(shape_k)}")
     dt = _dtype_code(q)
     _need(positions, "positions", torch.int32, dev)
     _need(inv_freq, "inv_freq", torch.float32, dev)
-    n_axes = 1
-    if tuple(positions.shape) != lead:
-        if positions.dim() < 1 or tuple(positions.shape[1:]) != lead:
-            raise ValueError(f"positions must be {lead} or (n_axes,) + {lead}, got "
-                             f"{tuple(positions.shape)}")
-        n_axes = positions.shape[0]
+    n_axes, n_freq, at = 1, inv_freq.numel(), positions.shape
+    if at != lead:
+        if len(at) < 1 or at[1:] != lead:
+            raise ValueError(f"positions must be {lead} or (n_axes,) + {lead}, got {tuple(at)}")
+        n_axes = at[0]
     if freq_axis is not None:
         _need(freq_axis, "freq_axis", torch.int32, dev)
-        if freq_axis.numel() != inv_freq.numel():
+        if freq_axis.numel() != n_freq:
             raise ValueError("freq_axis must have one entry a frequency")
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
             _need(w, name, torch.float32, dev)
-            if w.numel() != q.shape[-1]:
-                raise ValueError(f"{name} must have {q.shape[-1]} entries")
-    H, Hk, d = q.shape[-2], k.shape[-2], q.shape[-1]
+            if w.numel() != d:
+                raise ValueError(f"{name} must have {d} entries")
     soq, sok = H * d, Hk * d
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         soq = _rope_out(q_out, q, "q_out")
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     else:
         sok = _rope_out(k_out, k, "k_out")
     nt = 1
@@ -510,7 +512,7 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
         nt *= x
     _call(lib.kda_qk_norm_rope, dev, q.data_ptr(), k.data_ptr(), dt, _addr(q_weight),
           _addr(k_weight), -1.0 if eps is None else float(eps), positions.data_ptr(), n_axes,
-          _addr(freq_axis), inv_freq.data_ptr(), inv_freq.numel(), 1 if interleaved else 0,
+          _addr(freq_axis), inv_freq.data_ptr(), n_freq, 1 if interleaved else 0,
           q_out.data_ptr(), k_out.data_ptr(), nt, H, Hk, d, sq, sk, soq, sok)
     return q_out, k_out
 
@@ -525,24 +527,26 @@ def _rope_out(y, x, name):
 def _linear_inputs(q, k, v, g, lead):
     """Checks what the linear-attention calls share: q, k ``lead`` + [Hk, dk], v ``lead``
     + [H, dv], g ``lead`` + [H] or [H].  Returns (dtype code, H, Hk, dk, dv, flag of g)."""
-    dev = q.device
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, q.dtype, dev)
+    dev, dtype = q.device, q.dtype
+    _need(q, "q", dtype, dev)
+    _need(k, "k", dtype, dev)
+    _need(v, "v", dtype, dev)
     _need(g, "g", torch.float32, dev)
     dt = _dtype_code(q)
-    if not lead or v.dim() != len(lead) + 2:
-        raise ValueError(f"q and v must be [..., heads, 128], got {tuple(q.shape)} and "
-                         f"{tuple(v.shape)}")
-    Hk, dk, H, dv = q.shape[-2], q.shape[-1], v.shape[-2], v.shape[-1]
-    if k.shape != q.shape:
-        raise ValueError(f"k must have the shape of q {tuple(q.shape)}, got {tuple(k.shape)}")
-    if tuple(v.shape[:-2]) != lead:
-        raise ValueError(f"v must be {lead} + (H, dv), got {tuple(v.shape)}")
-    if tuple(g.shape) == lead + (H,):
+    qs, vs, gs = q.shape, v.shape, g.shape
+    if not lead or len(vs) != len(lead) + 2:
+        raise ValueError(f"q and v must be [..., heads, 128], got {tuple(qs)} and {tuple(vs)}")
+    Hk, dk = qs[-2:]
+    H, dv = vs[-2:]
+    if k.shape != qs:
+        raise ValueError(f"k must have the shape of q {tuple(qs)}, got {tuple(k.shape)}")
+    if vs[:-2] != lead:
+        raise ValueError(f"v must be {lead} + (H, dv), got {tuple(vs)}")
+    if gs == lead + (H,):
         return dt, H, Hk, dk, dv, 0
-    if tuple(g.shape) == (H,):
+    if gs == (H,):
         return dt, H, Hk, dk, dv, _HEAD_DECAY
-    raise ValueError(f"g must be {lead + (H,)} or ({H},), got {tuple(g.shape)}")
+    raise ValueError(f"g must be {lead + (H,)} or ({H},), got {tuple(gs)}")
 
 
 def _like(t, name, shape, dtype, device, given=False):
@@ -551,7 +555,7 @@ def _like(t, name, shape, dtype, device, given=False):
     if t is None and not given:
         return torch.empty(shape, dtype=dtype, device=device)
     _need(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -594,7 +598,7 @@ def linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale: float = 1.0
         _need(h0, "h0", torch.float32, dev)
         if tuple(h0.shape) != (N, H, dv, dk):
             raise ValueError(f"h0 must be [{N}, {H}, {dv}, {dk}], got {tuple(h0.shape)}")
-    o = _like(out, "out", v.shape, v.dtype, dev)
+    o = torch.empty_like(v) if out is None else _like(out, "out", v.shape, v.dtype, dev)
     hT = None
     if output_final_state:
         hT = _like(final_state_out, "final_state_out", (N, H, dv, dk), torch.float32, dev)
@@ -623,7 +627,7 @@ def linear_recurrent_step(q, k, v, g, S, *, scale: float = 1.0, out=None):
     N, dev = q.shape[0], q.device
     dt, H, Hk, dk, dv, fl = _linear_inputs(q, k, v, g, (N,))
     _like(S, "S", (N, H, dv, dk), torch.float32, dev, given=True)
-    o = _like(out, "out", v.shape, v.dtype, dev)
+    o = torch.empty_like(v) if out is None else _like(out, "out", v.shape, v.dtype, dev)
     _call(lib.kda_linear_recurrent_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
           g.data_ptr(), float(scale), S.data_ptr(), o.data_ptr(), N, H, Hk, dk, dv, tail=(fl,))
     return o
