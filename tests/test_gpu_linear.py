@@ -542,3 +542,50 @@ def test_lengths_around_the_cut(kda, T, H, cut):
     ro, rh = kda.linear_chunk_fwd(q, k, v, g, h0, flags=kda.SEQUENTIAL)
     kda.get_device_error()
     assert errors(o, to64(ro))[0] <= 2.0 ** -8 and errors(hT, to64(rh))[0] <= F32_REL_L2
+
+
+# ------------------------------------------------------------------- offsets past 32 bits
+@pytest.mark.parametrize("flags", ["tensor cores", "fp32 cores"])
+def test_a_prompt_whose_offsets_pass_32_bits(kda, flags):
+    """The last sequence of a batch with over 2^31 elements equals the same sequence by itself."""
+    fl = kda.FP32_CORES if flags == "fp32 cores" else 0
+    H, lens = 96, [180000, 300]
+    nt = sum(lens)
+    assert nt * H * 128 > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k, v = 0.1 * r(nt, H, 128), 0.1 * r(nt, H, 128), r(nt, H, 128)
+    g = -0.1 * torch.rand(nt, H, generator=gen, device="cuda")
+    h0 = 0.1 * torch.randn(2, H, 128, 128, generator=gen, device="cuda")
+    cu = torch.tensor([0, lens[0], nt], dtype=torch.int32, device="cuda")
+    o, hT = kda.linear_chunk_fwd(q, k, v, g, h0, cu, flags=fl)
+    tail = lambda x: x[lens[0]:].clone()  # noqa: E731
+    ro, rh = kda.linear_chunk_fwd(tail(q), tail(k), tail(v), tail(g), h0[1:].clone(), cu[1:] - lens[0],
+                                  flags=fl | kda.SEQUENTIAL)
+    kda.get_device_error()
+    assert torch.equal(o[lens[0]:], ro) and torch.equal(hT[1:], rh)
+    del q, k, v, o
+    torch.cuda.empty_cache()
+
+
+def test_steps_whose_states_pass_32_bits(kda):
+    N, H = 1400, 96
+    assert N * H * 128 * 128 > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    S = torch.zeros(N, H, 128, 128, device="cuda")
+    S[-1] = torch.randn(H, 128, 128, generator=gen, device="cuda")
+    one = S[-1:].clone()
+    for T in (1, 3):
+        q, k, v = r(N, T, H, 128), r(N, T, H, 128), r(N, T, H, 128)
+        g = -torch.rand(N, T, H, generator=gen, device="cuda")
+        last = [x[-1:].clone() for x in (q, k, v, g)]
+        if T == 1:
+            o = kda.linear_recurrent_step(*(x[:, 0] for x in (q, k, v, g)), S)
+            ro = kda.linear_recurrent_step(*(x[:, 0] for x in last), one)
+        else:
+            o = kda.linear_recurrent_multi_step(q, k, v, g, S)
+            ro = kda.linear_recurrent_multi_step(*last, one)
+        assert torch.equal(o[-1:], ro) and torch.equal(S[-1:], one)
+    del S
+    torch.cuda.empty_cache()

@@ -225,3 +225,23 @@ def test_captured_and_replayed_on_another_stream(kda):
     graph.replay()
     rq, rk = kda.qk_norm_rope(q, k, pos, f)
     assert torch.equal(qo, rq) and torch.equal(ko, rk)
+
+
+@pytest.mark.parametrize("Hq,Hk,nt", [(4, 2, 600), (2, 1, 4000)])
+def test_offsets_past_32_bits(kda, Hq, Hk, nt):
+    """Tokens far apart in one large buffer, in place, against the same rows side by side."""
+    step = -(-(2 ** 31 + 2 ** 28) // nt // 8) * 8
+    base = torch.zeros(nt * step, dtype=torch.bfloat16, device="cuda")
+    assert base.numel() > 2 ** 31
+    q = base.as_strided((nt, Hq, 128), (step, 128, 1))
+    k = base.as_strided((nt, Hk, 128), (step, 128, 1), Hq * 128)
+    gen = torch.Generator(device="cuda").manual_seed(nt)
+    q.copy_(torch.randn(nt, Hq, 128, generator=gen, device="cuda"))
+    k.copy_(torch.randn(nt, Hk, 128, generator=gen, device="cuda"))
+    pos, f = torch.arange(nt, dtype=torch.int32, device="cuda"), _inv_freq(64).cuda()
+    rq, rk = kda.qk_norm_rope(q.contiguous(), k.contiguous(), pos, f)
+    kda.qk_norm_rope(q, k, pos, f, q_out=q, k_out=k)
+    assert torch.equal(q, rq) and torch.equal(k, rk)
+    assert not base[-(step - (Hq + Hk) * 128):].any()  # behind the last row
+    del base, q, k
+    torch.cuda.empty_cache()
