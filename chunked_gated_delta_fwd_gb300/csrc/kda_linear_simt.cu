@@ -8,7 +8,7 @@
 // Three launches after the plan, each begun while the one before ends.  Only the scan walks a sequence in order, and it does
 // nothing but add: products over the whole prompt run at once, also with one head.  Measured:
 // 2102 tokens in five sequences, 16 heads: 118 us (plan 4, local 33, scan 19, outputs 68 one by
-// one), 28 TFLOP/s; 64 tokens of one head 25 us, four launches' latency.
+// one), 28 TFLOP/s; 64 tokens of one head 22 us, four launches' latency.
 //
 // Exponents are differences of running sums.  A gate may take g to -inf, so g is held at
 // -200 at least (e^-200 is 0 in fp32) and the sums as an exact pair of floats (a multiple
@@ -238,15 +238,15 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
 
 // --------------------------------------------------------------------- the outputs
 // One CTA per (chunk, head, kR rows of the chunk): scores of its rows over 128 channels, then
-// both products of the output.  A thread owns kR / 16 rows and four adjacent columns of each
-// 64 (keys, then value columns): 16 x 16 threads.  Products over channels run on pairs of
+// both products of the output.  A thread owns kR / 8 rows and four adjacent columns of each
+// 64 (keys, then value columns): 8 x 16 threads.  Products over channels run on pairs of
 // channels, products over keys on pairs of columns (packed fp32).  The next tile is copied
-// while one is multiplied
-// (1024 chunks x heads, the whole pass: 205 us with loads and products in turn, 199 like this).
-// What bounds it is shared memory: 8 reads of 16 bytes a lane for 32 packed products, at half
-// the rate of the products.  kR = 64 reads each operand
-// from shared memory least often; kR = 16 gives the shortest prompts four times the CTAs.
-constexpr int kOutThreads = 256;
+// while one is multiplied.  1024 chunks x heads, the whole pass: 205 us with copies and
+// products in turn and 16 x 16 threads of four rows, 199 with copies ahead, 195 like this: 12
+// reads of 16 bytes a lane feed 64 packed products, about what shared memory gives.  kR = 64
+// reads each operand from shared memory least often; kR = 16 gives the shortest prompts four
+// times the CTAs.
+constexpr int kOutThreads = 128;
 
 template <int kR>
 struct OutSmem {
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const float* __restrict__ g, int g_head, float scale, Plan plan, int H, int Hk,
     const float* __restrict__ states, T* __restrict__ o) {
-  constexpr int R = kR / 16;  // rows of a thread: ty + 16 i
+  constexpr int R = kR / 8;  // rows of a thread: ty + 8 i
   extern __shared__ __align__(16) unsigned char smem_raw[];
   OutSmem<kR>& sm = *reinterpret_cast<OutSmem<kR>*>(smem_raw);
   const int chunk = blockIdx.x, h = blockIdx.y, r0 = kR * blockIdx.z, tid = threadIdx.x;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
     for (int c = 0; c < D / 4; ++c) {
       float4 qa[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) qa[i] = tile_at<D>(sm.Q, ty + 16 * i, c);
+      for (int i = 0; i < R; ++i) qa[i] = tile_at<D>(sm.Q, ty + 8 * i, c);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const float4 x = tile_at<D>(X, 4 * tx + b, c);
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
     dot_tile(acc, sm.X[0]);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int r = ty + 16 * i;
+      const int r = ty + 8 * i;
       float p[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
     dot_tile(acc, sm.X[hf ^ 1]);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const float w = decay_from_start(sm.sums, r0 + ty + 16 * i);
+      const float w = decay_from_start(sm.sums, r0 + ty + 8 * i);
       out[hf][i][0] = make_float2(w * acc[i][0], w * acc[i][1]);
       out[hf][i][1] = make_float2(w * acc[i][2], w * acc[i][3]);
     }
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
   for (int j = 0; j < cols; j += 4) {
     float4 p[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(&sm.P[(ty + 16 * i) * C + j]);
+    for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(&sm.P[(ty + 8 * i) * C + j]);
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int r = r0 + ty + 16 * i;
+    const int r = r0 + ty + 8 * i;
     if (r < len) {
       T* orow = o + ((t0 + r) * H + h) * D + 4 * tx;
 #pragma unroll
@@ -418,8 +418,9 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const float* g
   if (n_tokens == 0) return cudaSuccess;
   // Few chunks and heads: the rows of a chunk are spread over four CTAs, each of which reads
   // all of its keys, state and values (whole pass, kR = 64 -> 16, by chunks x heads: 2 x 1
-  // 31.2 -> 26.0 us, 2 x 16 32.2 -> 27.7, 2 x 24 33.3 -> 36.8, 5 x 16 35.2 -> 46.4).
-  if (chunks * H * 4 <= sms)
+  // 32.4 -> 22.2 us, 5 x 16 36.1 -> 30.0, 7 x 16 37.0 -> 39.0, 2 x 76 40.8 -> 35.8, 13 x 16
+  // 52.7 -> 58.9, 17 x 16 57.3 -> 74.6).
+  if (chunks * H <= sms)
     return launch_out<T, 16>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
   return launch_out<T, 64>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
 }
