@@ -297,9 +297,12 @@ cudaError_t launch_rope_t(const RopeArgs& a, bool inter, bool norm, int* err, cu
   const int64_t most = (int64_t)sms * kRopeCtas;
   constexpr int R = unit_rows<T>();
   const int64_t all = (int64_t)units_of_token(a, 2 * R) * 2 * R,
-                half = (int64_t)units_of_token(a, R) * R, two = (int64_t)units_of_token(a, 2) * 2;
-  if (5 * two <= 2 * half && a.n_tokens >= unit_tokens<T, 2>() * most)
-    return launch_rope_heads<T, 2>(a, inter, norm, most, err, s);
+                half = (int64_t)units_of_token(a, R) * R;
+  if constexpr (R == 8) {  // (of fp32's 4 heads 2 never leave enough fewer rows empty)
+    const int64_t two = (int64_t)units_of_token(a, 2) * 2;
+    if (5 * two <= 2 * half && a.n_tokens >= unit_tokens<T, 2>() * most)
+      return launch_rope_heads<T, 2>(a, inter, norm, most, err, s);
+  }
   if (4 * half <= 3 * all && a.n_tokens >= 2 * most)
     return launch_rope_heads<T, R>(a, inter, norm, most, err, s);
   return launch_rope_heads<T, 2 * R>(a, inter, norm, most, err, s);
