@@ -16,7 +16,7 @@
 // are as many, builds its lanes' A and B once a token and then needs two multiplications a channel; the pair's other channel travels as
 // raw input, four shuffles a bf16 row.
 //
-// Bound by HBM: a row is read and written once (8192 tokens x 192 heads bf16: 127 us, 6.3 TB/s;
+// Bound by HBM: a row is read and written once (8192 tokens x 192 heads bf16: 125 us, 6.4 TB/s;
 // 10007 tokens of 40 heads out of a packed projection: 37 us, 5.5 TB/s; 65536 tokens of 1 + 1
 // heads 30 us, 2.3 TB/s: there the angles, 64 for two rows, bound it).  A half warp holds
 // a row, 8 channels a lane (16-byte accesses), 128 bytes of a lane in flight.  The CTAs stay
@@ -173,9 +173,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) norm_rope_kernel(cons
                           : static_cast<const T*>(a.k) + (t0 + t) * a.sk) + h0 * kD + 8 * hl;
       T* dst = (isq ? static_cast<T*>(a.qo) + (t0 + t) * a.sqo
                     : static_cast<T*>(a.ko) + (t0 + t) * a.sko) + h0 * kD + 8 * hl;
+      const int left = H - h0;
       // row b of a half warp: its token (all in the step where the half warps share one), its head
       auto row = [&](int b) {
-        return (kShared || t + b / kRun < nt) && h0 + b % kRun * kStep < H;
+        return (kShared || t + b / kRun < nt) && b % kRun * kStep < left;
       };
       auto at = [&](int b, int64_t sq, int64_t sk) {
         return (kRun == kBatch ? 0 : b / kRun * (isq ? sq : sk)) + b % kRun * (kStep * kD);
