@@ -400,8 +400,8 @@ kda_status_t kda_recurrent_multi_step(const void* q, const void* k, const void* 
  *     phi_i = positions[axis_i][t] * inv_freq[i],  i < n_freq
  *     (a, b) <- (a cos phi_i - b sin phi_i, a sin phi_i + b cos phi_i)
  * on the pairs (a, b) = (y[i], y[i + n_freq]), or (y[2i], y[2i + 1]) with `interleaved`;
- * channels from 2 n_freq on are y.  Everything is fp32 (the angle fp64, so that far
- * positions keep their phase), rounded once at the store.
+ * channels from 2 n_freq on are y.  Everything is fp32 but the angle (a 64-bit fraction of a
+ * turn, so that any int32 position keeps its phase), rounded once at the store.
  *   q, k      rows of Hq (Hk) x 128 channels of `dtype`, token t at t * q_stride
  *             (k_stride) elements: slices of one packed projection need no copy.
  *             Strides are at least Hq * 128 (Hk * 128) and multiples of 16 bytes.
@@ -413,7 +413,8 @@ kda_status_t kda_recurrent_multi_step(const void* q, const void* k, const void* 
  *   freq_axis int32 [n_freq], the axis of every frequency, 0 <= axis < n_axes (sections or
  *             any interleaving); NULL: axis 0, allowed with n_axes = 1 only.  An entry out
  *             of range is read as 0 and reported by kda_get_device_error.
- *   inv_freq  fp32 [n_freq], n_freq a multiple of 8 from 8 to 64 (64: the whole head turns).
+ *   inv_freq  fp32 [n_freq], n_freq a multiple of 8 from 8 to 64 (64: the whole head turns);
+ *             any sign and size; where one is not finite its channels are NaN.
  *   q_out, k_out  written, token strides q_out_stride, k_out_stride.  q_out may be q with
  *             the same stride (in place), k_out may be k; any other overlap of an output
  *             with an input or the other output is not allowed.
