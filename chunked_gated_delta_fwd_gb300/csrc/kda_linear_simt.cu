@@ -7,8 +7,8 @@
 //     O_i   = scale (e^{G_i} S_in^T q_i + sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j)
 // Three launches after the plan, each begun while the one before ends.  Only the scan walks a sequence in order, and it does
 // nothing but add: products over the whole prompt run at once, also with one head.  Measured:
-// 2102 tokens in five sequences, 16 heads: 118 us (plan 4, local 33, scan 19, outputs 68 one by
-// one), 28 TFLOP/s; 64 tokens of one head 22 us, four launches' latency.
+// 2102 tokens in five sequences, 16 heads: 106 us (plan 4, local 33, scan 19, outputs 57 one by
+// one), 31 TFLOP/s; 64 tokens of one head 22 us, four launches' latency.
 //
 // Exponents are differences of running sums.  A gate may take g to -inf, so g is held at
 // -200 at least (e^-200 is 0 in fp32) and the sums as an exact pair of floats (a multiple
@@ -62,14 +62,15 @@ __device__ __forceinline__ float decay_from_start(const Sums& s, int i) {
 
 // 16-byte chunk c4 of row r of a shared tile whose rows are W floats: chunks are permuted by
 // r / 4, so that lanes that read the same chunk of rows 4 apart do not meet in a bank.
-template <int W>
+// kShift 0 permutes by r for lanes that read adjacent rows.
+template <int W, int kShift = 2>
 __device__ __forceinline__ float4& tile_at(float* tile, int r, int c4) {
-  return reinterpret_cast<float4*>(tile + r * W)[c4 ^ ((r >> 2) & 7)];
+  return reinterpret_cast<float4*>(tile + r * W)[c4 ^ ((r >> kShift) & 7)];
 }
 
 // Rows t0 .. t0 + len - 1 of one head, columns c0 .. c0 + W - 1, into a shared tile of R
 // rows (zeros past len).  Every load is in flight before the first store.
-template <typename T, int R, int W, int kThreads>
+template <typename T, int R, int W, int kThreads, int kShift = 2>
 __device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ x, int64_t t0, int len,
                                           int heads, int head, int c0) {
   constexpr int n = R * (W / 4) / kThreads;
@@ -84,29 +85,30 @@ __device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ x, i
 #pragma unroll
   for (int i = 0; i < n; ++i) {
     const int e = threadIdx.x + i * kThreads;
-    tile_at<W>(dst, e / (W / 4), e % (W / 4)) = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
+    tile_at<W, kShift>(dst, e / (W / 4), e % (W / 4)) =
+        make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
   }
 }
 
 // The same for fp32 without a stop in registers: the copies are on their way when this returns
 // (bf16 is converted, and is in place).
-template <int R, int kThreads>
+template <int R, int kThreads, int kShift = 2>
 __device__ __forceinline__ void start_tile(float* dst, const float* __restrict__ x, int64_t t0,
                                            int len, int heads, int head) {
 #pragma unroll
   for (int i = 0; i < R * (D / 4) / kThreads; ++i) {
     const int e = threadIdx.x + i * kThreads, r = e / (D / 4), c4 = e % (D / 4);
     const float* src = x + ((t0 + (r < len ? r : 0)) * heads + head) * D + 4 * c4;
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(&tile_at<D>(dst, r, c4));
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(&tile_at<D, kShift>(dst, r, c4));
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src),
                  "r"(r < len ? 16 : 0)  // no bytes read: zeros
                  : "memory");
   }
 }
-template <int R, int kThreads>
+template <int R, int kThreads, int kShift = 2>
 __device__ __forceinline__ void start_tile(float* dst, const __nv_bfloat16* __restrict__ x,
                                            int64_t t0, int len, int heads, int head) {
-  load_tile<__nv_bfloat16, R, D, kThreads>(dst, x, t0, len, heads, head, 0);
+  load_tile<__nv_bfloat16, R, D, kThreads, kShift>(dst, x, t0, len, heads, head, 0);
 }
 __device__ __forceinline__ void commit_tiles() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
@@ -242,10 +244,10 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
 // 64 (keys, then value columns): 8 x 16 threads.  Products over channels run on pairs of
 // channels, products over keys on pairs of columns (packed fp32).  The next tile is copied
 // while one is multiplied.  1024 chunks x heads, the whole pass: 205 us with copies and
-// products in turn and 16 x 16 threads of four rows, 199 with copies ahead, 195 like this: 12
-// reads of 16 bytes a lane feed 64 packed products, about what shared memory gives.  kR = 64
-// reads each operand from shared memory least often; kR = 16 gives the shortest prompts four
-// times the CTAs.
+// products in turn and 16 x 16 threads of four rows, 199 with copies ahead, 195 with eight rows
+// a thread (12 reads of 16 bytes a lane feed 64 packed products), 178 with the products above
+// the diagonal left out by blocks of 8 rows x 16 keys.  kR = 64 reads each operand from shared
+// memory least often; kR = 16 gives the shortest prompts four times the CTAs.
 constexpr int kOutThreads = 128;
 
 template <int kR>
@@ -256,6 +258,35 @@ struct OutSmem {
   Sums sums;
   double half;
 };
+
+// acc[i][b] = row ty + 8 i of Q . row 4 tx + b of X, over 128 channels.  For scores it is row
+// tx + 16 b: all lanes then skip the keys that none of their rows i may see (12 of the 32
+// products of a whole chunk).
+template <int kR, bool kScores>
+__device__ __forceinline__ void dot_tile(float (&acc)[kR / 8][4], float* Q, float* X, int ty,
+                                         int tx) {
+  constexpr int R = kR / 8;
+  float2 a2[R][4] = {};
+#pragma unroll 2
+  for (int c = 0; c < D / 4; ++c) {
+    float4 qa[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) qa[i] = tile_at<D>(Q, ty + 8 * i, c);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const float4 x = kScores ? tile_at<D, 0>(X, tx + 16 * b, c) : tile_at<D>(X, 4 * tx + b, c);
+#pragma unroll
+      for (int i = kScores && kR == C ? 2 * b : 0; i < R; ++i)
+        a2[i][b] = __ffma2_rn(make_float2(qa[i].x, qa[i].y), make_float2(x.x, x.y),
+                              __ffma2_rn(make_float2(qa[i].z, qa[i].w), make_float2(x.z, x.w),
+                                         a2[i][b]));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[i][b] = a2[i][b].x + a2[i][b].y;
+}
 
 template <typename T, int kR>
 __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
@@ -274,51 +305,26 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
   if (r0 >= len) return;
   const float* S = states + ((int64_t)chunk * H + h) * D * D;
   start_tile<kR, kOutThreads>(sm.Q, q, t0 + r0, len - r0, Hk, hk);
-  start_tile<C, kOutThreads>(sm.X[0], k, t0, len, Hk, hk);
+  start_tile<C, kOutThreads, 0>(sm.X[0], k, t0, len, Hk, hk);
   commit_tiles();
   start_tile<C, kOutThreads>(sm.X[1], S, 0, C, 1, 0);
   commit_tiles();
   chunk_sums(sm.sums, &sm.half, g, g_head, t0, len, H, h);
   const int ty = tid >> 4, tx = tid & 15;
-  // acc[i][b] = row ty + 16 i of Q . row 4 tx + b of X, over 128 channels
-  auto dot_tile = [&](float (&acc)[R][4], float* X) {
-    float2 a2[R][4] = {};
-#pragma unroll 2
-    for (int c = 0; c < D / 4; ++c) {
-      float4 qa[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) qa[i] = tile_at<D>(sm.Q, ty + 8 * i, c);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float4 x = tile_at<D>(X, 4 * tx + b, c);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          a2[i][b] = __ffma2_rn(make_float2(qa[i].x, qa[i].y), make_float2(x.x, x.y),
-                                __ffma2_rn(make_float2(qa[i].z, qa[i].w), make_float2(x.z, x.w),
-                                           a2[i][b]));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) acc[i][b] = a2[i][b].x + a2[i][b].y;
-  };
+  const int cols = min(C, r0 + kR);  // keys that these rows may see
   wait_tiles<1>();
   __syncthreads();
   {
     float acc[R][4];
-    dot_tile(acc, sm.X[0]);
+    dot_tile<kR, true>(acc, sm.Q, sm.X[0], ty, tx);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int r = ty + 8 * i;
-      float p[4];
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int j = 4 * tx + b;
-        p[b] = j <= r0 + r ? acc[i][b] * decay(sm.sums, r0 + r, j) : 0.f;
+        if (kR == C && i < 2 * b) continue;  // not read either
+        const int r = ty + 8 * i, j = tx + 16 * b;
+        sm.P[r * C + j] = j <= r0 + r ? acc[i][b] * decay(sm.sums, r0 + r, j) : 0.f;
       }
-      *reinterpret_cast<float4*>(&sm.P[r * C + 4 * tx]) = make_float4(p[0], p[1], p[2], p[3]);
-    }
   }
   // O = e^G Q S, 64 value rows of S^T at a time
   float2 out[2][R][2];
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
       start_tile<C, kOutThreads>(sm.X[1], v, t0, len, H, h);
     commit_tiles();
     float acc[R][4];
-    dot_tile(acc, sm.X[hf ^ 1]);
+    dot_tile<kR, false>(acc, sm.Q, sm.X[hf ^ 1], ty, tx);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float w = decay_from_start(sm.sums, r0 + ty + 8 * i);
@@ -340,27 +346,30 @@ __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
       out[hf][i][1] = make_float2(w * acc[i][2], w * acc[i][3]);
     }
   }
-  // O += P V over the keys that these rows may see
+  // O += P V over the keys that these rows may see, 16 at a time
   wait_tiles<0>();
   __syncthreads();
-  const int cols = min(C, r0 + kR);
+#pragma unroll
+  for (int m = 0; m < (kR == C ? C / 16 : 1); ++m) {
+    const int first = 2 * m, end = kR == C ? 16 * (m + 1) : cols;  // rows i < first see none
 #pragma unroll 2
-  for (int j = 0; j < cols; j += 4) {
-    float4 p[R];
+    for (int j = 16 * m; j < end; j += 4) {
+      float4 p[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(&sm.P[(ty + 8 * i) * C + j]);
+      for (int i = first; i < R; ++i) p[i] = *reinterpret_cast<const float4*>(&sm.P[(ty + 8 * i) * C + j]);
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj)
+      for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float4 x = tile_at<D>(sm.X[1], j + jj, 16 * hf + tx);
+        for (int hf = 0; hf < 2; ++hf) {
+          const float4 x = tile_at<D>(sm.X[1], j + jj, 16 * hf + tx);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const float pj = jj == 0 ? p[i].x : (jj == 1 ? p[i].y : (jj == 2 ? p[i].z : p[i].w));
-          out[hf][i][0] = __ffma2_rn(make_float2(pj, pj), make_float2(x.x, x.y), out[hf][i][0]);
-          out[hf][i][1] = __ffma2_rn(make_float2(pj, pj), make_float2(x.z, x.w), out[hf][i][1]);
+          for (int i = first; i < R; ++i) {
+            const float pj = jj == 0 ? p[i].x : (jj == 1 ? p[i].y : (jj == 2 ? p[i].z : p[i].w));
+            out[hf][i][0] = __ffma2_rn(make_float2(pj, pj), make_float2(x.x, x.y), out[hf][i][0]);
+            out[hf][i][1] = __ffma2_rn(make_float2(pj, pj), make_float2(x.z, x.w), out[hf][i][1]);
+          }
         }
-      }
+    }
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -417,10 +426,10 @@ cudaError_t launch_t(const void* q, const void* k, const void* v, const float* g
   }
   if (n_tokens == 0) return cudaSuccess;
   // Few chunks and heads: the rows of a chunk are spread over four CTAs, each of which reads
-  // all of its keys, state and values (whole pass, kR = 64 -> 16, by chunks x heads: 2 x 1
-  // 32.4 -> 22.2 us, 5 x 16 36.1 -> 30.0, 7 x 16 37.0 -> 39.0, 2 x 76 40.8 -> 35.8, 13 x 16
-  // 52.7 -> 58.9, 17 x 16 57.3 -> 74.6).
-  if (chunks * H <= sms)
+  // all of its keys, state and values, while all of them run at once, two an SM (whole pass,
+  // kR = 64 -> 16, by chunks x heads: 2 x 1 29.1 -> 21.8 us, 2 x 16 30.1 -> 23.5, 2 x 38 32.2 ->
+  // 28.8, but 6 x 16 34.2 -> 37.8, 9 x 16 34.7 -> 43.0).
+  if (2 * chunks * H <= sms)
     return launch_out<T, 16>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
   return launch_out<T, 64>(q, k, v, g, g_head, scale, plan, chunks, H, Hk, local, o, s);
 }
