@@ -7,8 +7,8 @@
 //     O_i   = scale (e^{G_i} S_in^T q_i + sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j)
 // Three launches after the plan, each begun while the one before ends.  Only the scan walks a sequence in order, and it does
 // nothing but add: products over the whole prompt run at once, also with one head.  Measured:
-// 2102 tokens in five sequences, 16 heads: 106 us (plan 4, local 33, scan 19, outputs 57 one by
-// one), 31 TFLOP/s; 64 tokens of one head 22 us, four launches' latency.
+// 2102 tokens in five sequences, 16 heads: 104 us (plan 4, local 31, scan 19, outputs 56 one by
+// one), 32 TFLOP/s; 64 tokens of one head 22 us, four launches' latency.
 //
 // Exponents are differences of running sums.  A gate may take g to -inf, so g is held at
 // -200 at least (e^-200 is 0 in fp32) and the sums as an exact pair of floats (a multiple

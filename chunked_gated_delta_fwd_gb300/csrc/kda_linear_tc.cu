@@ -30,7 +30,7 @@
 // copies, about as much again by the groups below, of 5300 clocks (678 KB) that a chunk takes
 // at one chain an SM; at all SMs busy a chunk takes 5800 and HBM bounds it.  Measured: 8192
 // tokens x 96 heads (96 of 152 SMs have a chain) 177 us, 4.6 TB/s; 14 ragged sequences of 17589
-// tokens x 48 heads 183 us, 5.2 TB/s; 131072 tokens x 16 heads in segments 515 us.
+// tokens x 48 heads 183 us, 5.2 TB/s; 131072 tokens x 16 heads in segments 509 us.
 //
 // The ring holds two whole chunks of q, k and v.
 //
