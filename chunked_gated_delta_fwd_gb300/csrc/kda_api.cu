@@ -109,70 +109,74 @@ Plan plan_in(void* ws, int64_t n_tokens, int n_seqs) {
   return plan;
 }
 
+// Inclusive scan over a CTA of 1024 threads; 0 is the neutral value.  `per_warp` may be used
+// again behind the next barrier.
+template <typename Op>
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* per_warp, Op op) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto warp_scan = [&](int32_t x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = op(x, y);
+    }
+    return x;
+  };
+  v = warp_scan(v);
+  if (lane == 31) per_warp[warp] = v;
+  __syncthreads();
+  if (warp == 0) per_warp[lane] = warp_scan(per_warp[lane]);
+  __syncthreads();
+  return warp > 0 ? op(v, per_warp[warp - 1]) : v;
+}
+
 // One CTA: writes cu[N+1] (copied from cu_seqlens, or n*T_per_seq), the
 // exclusive prefix sum of ceil(len/64) into chunk_off[N+1], and for every chunk
 // its first token and token count into tab.  Invalid sequence
-// offsets (decreasing, outside [0, NT], cu[0] != 0 or cu[N] != NT) are clamped so
-// that no later kernel can index outside the inputs, and flag an error.
+// offsets (decreasing, outside [0, NT], cu[0] != 0 or cu[N] != NT) flag an error and are
+// clamped, those below one before them to that one: what cu holds runs upwards within
+// [0, NT], so the lengths add up to NT at most and the chunks stay within
+// chunks_upper_bound, for which every table and workspace is sized.
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ cu_in, int n_seqs,
                                                     int64_t T_per_seq, int64_t n_tokens,
                                                     int32_t* __restrict__ cu_out,
                                                     int32_t* __restrict__ chunk_off,
                                                     int2* __restrict__ tab, int* err_flag) {
-  __shared__ int32_t warp_sums[32];
-  __shared__ int32_t carry;
+  __shared__ int32_t per_warp[32];
+  __shared__ int32_t carry, top;  // chunks and largest offset of the sequences before this round
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    carry = 0;
-  }
+  if (tid == 0) carry = top = 0;
   __syncthreads();
-  bool bad = false;
+  bool bad = false, falls = false;  // falls: some offset so far is below one before it
   for (int base = 0; base <= n_seqs; base += blockDim.x) {
     const int n = base + tid;
-    int32_t cu_n = 0, nchunks = 0;
+    int32_t cu_n = 0, next = 0;
+    auto offset = [&](int i) {
+      const int64_t x = cu_in ? (int64_t)cu_in[i] : (int64_t)i * T_per_seq;
+      if ((i == 0 && x != 0) || (i == n_seqs && x != n_tokens) || x < 0 || x > n_tokens) bad = true;
+      return (int32_t)(x < 0 ? 0 : (x > n_tokens ? n_tokens : x));
+    };
+    if (n <= n_seqs) cu_n = next = offset(n);
+    if (n < n_seqs) next = offset(n + 1);
+    if (__syncthreads_or(next < cu_n)) falls = bad = true;
+    if (falls) {  // the running maximum instead
+      cu_n = max(top, block_scan(cu_n, per_warp, [](int32_t a, int32_t b) { return max(a, b); }));
+      next = max(next, cu_n);
+      __syncthreads();
+    }
+    const int32_t nchunks = n < n_seqs ? (next - cu_n + kChunk - 1) / kChunk : 0;
+    const int32_t incl = block_scan(nchunks, per_warp, [](int32_t a, int32_t b) { return a + b; });
     if (n <= n_seqs) {
-      int64_t x = cu_in ? (int64_t)cu_in[n] : (int64_t)n * T_per_seq;
-      if (n == 0 && x != 0) bad = true;
-      if (n == n_seqs && x != n_tokens) bad = true;
-      if (x < 0) { x = 0; bad = true; }
-      if (x > n_tokens) { x = n_tokens; bad = true; }
-      cu_n = (int32_t)x;
       cu_out[n] = cu_n;
+      chunk_off[n] = carry + incl - nchunks;
     }
     __syncthreads();
-    if (n < n_seqs) {
-      int64_t nx = cu_in ? (int64_t)cu_in[n + 1] : (int64_t)(n + 1) * T_per_seq;
-      if (nx > n_tokens) nx = n_tokens;
-      if (nx < cu_n) { nx = cu_n; bad = true; }
-      nchunks = (int32_t)((nx - cu_n + kChunk - 1) / kChunk);
+    if (tid == blockDim.x - 1) {
+      carry += incl;
+      top = cu_n;
     }
-    // block-wide exclusive scan of nchunks
-    int32_t v = nchunks;
-    const int lane = tid & 31, warp = tid >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      int32_t w = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
-      }
-      warp_sums[lane] = w;
-    }
-    __syncthreads();
-    const int32_t incl = v + (warp > 0 ? warp_sums[warp - 1] : 0);
-    if (n <= n_seqs) chunk_off[n] = carry + incl - nchunks;
-    __syncthreads();
-    if (tid == blockDim.x - 1) carry += incl;
     __syncthreads();
   }
-  __syncthreads();
   const int total = chunk_off[n_seqs];
   for (int j = tid; j < total; j += blockDim.x) {
     int lo = 0, hi = n_seqs - 1;  // the last sequence whose chunks start at or before j
