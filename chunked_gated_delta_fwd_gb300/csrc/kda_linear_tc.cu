@@ -1017,11 +1017,13 @@ __global__ void __launch_bounds__(kMaxOrder) lin_order_kernel(LinArgs a, int* ti
 //     S_in(0) = h0,   S_in(1) = S_end(0),   S_in(k+1) = S_end(k) + (segment k's decay) S_in(k),
 // and the pass with outputs starts each segment from its own (also the first, so that hT
 // may be h0: h0 is not read any more when a last segment writes hT).
+// A malformed cu_seqlens may ask for any number of segments (sequences that overlap): the sums
+// are 64 bits and what is past the table is dropped.
 __global__ void __launch_bounds__(1024) lin_seg_plan_kernel(LinArgs a, int L, int4* tab,
                                                             int* first, int* n_segs, int cap,
                                                             int* tickets) {
-  __shared__ int warp_sums[32];
-  __shared__ int carry;
+  __shared__ int64_t warp_sums[32];
+  __shared__ int64_t carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   release_next();
   if (tid == 0) carry = 0;
@@ -1035,27 +1037,27 @@ __global__ void __launch_bounds__(1024) lin_seg_plan_kernel(LinArgs a, int L, in
       const int64_t per = (int64_t)L * C;
       P = t1 > t0 ? (int)((t1 - t0 + per - 1) / per) : 1;
     }
-    int v = P;
+    int64_t v = P;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += y;
     }
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
     if (warp == 0) {
-      int w = warp_sums[lane];
+      int64_t w = warp_sums[lane];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
       }
       warp_sums[lane] = w;
     }
     __syncthreads();
-    const int f = carry + v - P + (warp > 0 ? warp_sums[warp - 1] : 0);
+    const int64_t f = carry + v - P + (warp > 0 ? warp_sums[warp - 1] : 0);
     if (n < a.n_seqs) {
-      first[n] = min(f, cap);
+      first[n] = (int)min(f, (int64_t)cap);
       for (int k = 0; k < P && f + k < cap; ++k) {
         const int64_t s0 = t0 + (int64_t)k * L * C;
         const int64_t s1 = min(t1, s0 + (int64_t)L * C);
@@ -1067,8 +1069,7 @@ __global__ void __launch_bounds__(1024) lin_seg_plan_kernel(LinArgs a, int L, in
     __syncthreads();
   }
   if (tid == 0) {
-    first[a.n_seqs] = min(carry, cap);
-    *n_segs = min(carry, cap);
+    first[a.n_seqs] = *n_segs = (int)min(carry, (int64_t)cap);
     tickets[0] = tickets[1] = 0;
   }
 }

@@ -109,3 +109,24 @@ def test_a_good_batch_of_many_sequences_after_a_bad_one(kda, dtype):
     big = ((q[:, 0].double().abs() @ k[:, 0].double().abs().T) * w) @ v[:, 0].double().abs()
     half = 2.0 ** -8 * ref.abs() if dtype == torch.bfloat16 else 0.0
     assert bool(((o[:, 0].double() - ref).abs() <= 512 * 2.0 ** -24 * big + half + 1e-30).all())
+
+
+def test_segments_whose_count_passes_32_bits(kda):
+    """Overlapping sequences that ask for over 2^31 segments between them."""
+    nt, n = 5932032, 92700
+    flags = kda.segment_chunks(1)
+    assert (n // 2) * (nt // 128) > 2 ** 31
+    q = torch.zeros(nt, 1, 128, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(1, device="cuda")
+    need = kda.linear_chunk_fwd_workspace_size(nt, n, 1, torch.bfloat16, flags)
+    ws, o = Watched(need), Watched(2 * q.numel())
+    kda.get_device_error()
+    kda.linear_chunk_fwd(q, q, q, g, None, sawtooth(nt, n).cuda(), flags=flags,
+                         workspace=ws.view((ws.n,), torch.uint8), output_final_state=False,
+                         out=o.view(q.shape, torch.bfloat16))
+    with pytest.raises(kda.KdaError, match="cu_seqlens"):
+        kda.get_device_error()
+    assert ws.untouched() and o.untouched()
+    assert not bool(o.view(q.shape, torch.bfloat16).any())
+    del q, ws, o
+    torch.cuda.empty_cache()
