@@ -75,6 +75,9 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float* out) {
 // one still runs (launch_chained): it calls wait_previous, in every CTA, before it touches what
 // the call's earlier kernels wrote or writes anything.  A kernel calls release_next after its
 // own wait_previous, so the next one starts when all kernels before this one are complete.
+// What the call's earlier kernels wrote is not read-only for as long as the kernel lives: it is
+// read by plain loads through pointers without __restrict__, never by __ldg or other loads that
+// the compiler may take for constant and move above the wait.
 // (A prompt of 64 tokens in fp32, four launches: 28.0 -> 27.0 us.)
 __device__ __forceinline__ void wait_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -93,8 +93,8 @@ __device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ x, i
 // The same for fp32 without a stop in registers: the copies are on their way when this returns
 // (bf16 is converted, and is in place).
 template <int R, int kThreads, int kShift = 2>
-__device__ __forceinline__ void start_tile(float* dst, const float* __restrict__ x, int64_t t0,
-                                           int len, int heads, int head) {
+__device__ __forceinline__ void start_tile(float* dst, const float* x, int64_t t0, int len,
+                                           int heads, int head) {
 #pragma unroll
   for (int i = 0; i < R * (D / 4) / kThreads; ++i) {
     const int e = threadIdx.x + i * kThreads, r = e / (D / 4), c4 = e % (D / 4);
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kLocThreads) lin_local_kernel(
   __shared__ double half;
   const int chunk = blockIdx.x, h = blockIdx.y, v0 = 64 * blockIdx.z, tid = threadIdx.x;
   wait_previous();
-  if (chunk >= __ldg(plan.chunk_off + plan.n_seqs)) return;
+  if (chunk >= plan.chunk_off[plan.n_seqs]) return;
   const int2 e = plan.tab[chunk];
   const int64_t t0 = e.x;
   const int len = e.y, hk = h / (H / Hk);
@@ -208,13 +208,12 @@ cudaError_t launch_local(const void* k, const void* v, const float* g, int g_hea
 constexpr int kScanThreads = 256, kScanAhead = 8;
 
 __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
-    const float* __restrict__ h0, Plan plan, int H, float* __restrict__ local,
-    const float* __restrict__ gam, float* __restrict__ hT) {
+    const float* h0, Plan plan, int H, float* local, const float* gam, float* hT) {
   const int64_t unit = blockIdx.x;  // n * H + h
   const int n = (int)(unit / H), h = (int)(unit - (int64_t)n * H);
   const int64_t e = 4 * ((int64_t)blockIdx.y * kScanThreads + threadIdx.x);
   wait_previous();
-  const int c0 = __ldg(plan.chunk_off + n), c1 = __ldg(plan.chunk_off + n + 1);
+  const int c0 = plan.chunk_off[n], c1 = plan.chunk_off[n + 1];
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (h0) s = *reinterpret_cast<const float4*>(h0 + unit * D * D + e);
   auto at = [&](int c) {
@@ -226,8 +225,8 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(
 #pragma unroll
     for (int i = 0; i < kScanAhead; ++i)
       if (c + i < c1) {
-        x[b][i] = __ldcs(at(c + i));
-        a[b][i] = __ldg(gam + (int64_t)(c + i) * H + h);
+        x[b][i] = *at(c + i);
+        a[b][i] = gam[(int64_t)(c + i) * H + h];
       }
   };
   fetch(0, c0);
@@ -303,13 +302,13 @@ template <typename T, int kR>
 __global__ void __launch_bounds__(kOutThreads, 2) lin_out_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const float* __restrict__ g, int g_head, float scale, Plan plan, int H, int Hk,
-    const float* __restrict__ states, T* __restrict__ o) {
+    const float* states, T* __restrict__ o) {
   constexpr int R = kR / 8;  // rows of a thread: ty + 8 i
   extern __shared__ __align__(16) unsigned char smem_raw[];
   OutSmem<kR>& sm = *reinterpret_cast<OutSmem<kR>*>(smem_raw);
   const int chunk = blockIdx.x, h = blockIdx.y, r0 = kR * blockIdx.z, tid = threadIdx.x;
   wait_previous();
-  if (chunk >= __ldg(plan.chunk_off + plan.n_seqs)) return;
+  if (chunk >= plan.chunk_off[plan.n_seqs]) return;
   const int2 e = plan.tab[chunk];
   const int64_t t0 = e.x;
   const int len = e.y, hk = h / (H / Hk);

@@ -189,7 +189,7 @@ __device__ __forceinline__ void seq_range(const LinArgs& a, int n, int64_t& t0, 
 
 template <bool kOut>
 __device__ __forceinline__ int job_count(const LinArgs& a) {
-  return (a.tab ? __ldg(a.n_segs) : a.n_seqs) * a.H;
+  return (a.tab ? *a.n_segs : a.n_seqs) * a.H;
 }
 
 template <bool kOut>
@@ -198,7 +198,7 @@ __device__ __forceinline__ Job get_job(const LinArgs& a, int item) {
   int u = item / a.H;
   j.h = item - u * a.H;
   if (a.order) {
-    u = __ldg(a.order + u);
+    u = a.order[u];
     item = u * a.H + j.h;
   }
   if (!a.tab) {
@@ -1076,15 +1076,14 @@ __global__ void __launch_bounds__(1024) lin_seg_plan_kernel(LinArgs a, int L, in
 
 constexpr int kScanThreads = 256, kScanAhead = 8;
 __global__ void __launch_bounds__(kScanThreads) lin_seg_scan_kernel(
-    const int* __restrict__ first, int H, const float* __restrict__ h0,
-    const float* __restrict__ s_end,
-    const float* __restrict__ decay, float* __restrict__ s_in) {
+    const int* first, int H, const float* __restrict__ h0, const float* s_end, const float* decay,
+    float* s_in) {
   const int64_t unit = blockIdx.x;
   const int n = (int)(unit / H), h = (int)(unit - (int64_t)n * H);
   const int64_t e = 4 * ((int64_t)blockIdx.y * kScanThreads + threadIdx.x);
   wait_previous();
   release_next();
-  const int f0 = __ldg(first + n), f1 = __ldg(first + n + 1);
+  const int f0 = first[n], f1 = first[n + 1];
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (h0) s = *reinterpret_cast<const float4*>(h0 + unit * D * D + e);
   if (f0 < f1) *reinterpret_cast<float4*>(s_in + ((int64_t)f0 * H + h) * D * D + e) = s;
@@ -1096,7 +1095,7 @@ __global__ void __launch_bounds__(kScanThreads) lin_seg_scan_kernel(
       if (fb + i + 1 < f1) {
         const int64_t unit_f = (int64_t)(fb + i) * H + h;
         x[i] = *reinterpret_cast<const float4*>(s_end + unit_f * D * D + e);
-        d[i] = __ldg(decay + unit_f);
+        d[i] = decay[unit_f];
       }
 #pragma unroll
     for (int i = 0; i < kScanAhead; ++i)
