@@ -43,8 +43,9 @@ SEQUENTIAL = 2  # flag of chunk_fwd: never split a sequence's chain into segment
 UNBOUNDED_GATE = 4  # flag of chunk_fwd: any g <= 0 (range-robust fp32-core evaluation)
 SCALAR_GATE = 8  # flag of chunk_fwd: g is [..., H], one log-decay per token and head
 CHECK_INPUTS = 16  # flag of chunk_fwd: check g and beta against their ranges on the device
-_HEAD_DECAY = 4  # flag of the linear-attention calls, set from g's shape
 PRECISE = 32  # flag of chunk_fwd (bf16 tensor cores): the state update at tf32 precision
+_HEAD_DECAY = 64  # flag of the linear-attention calls, set from g's shape
+_LINEAR_FLAGS = FP32_CORES | SEQUENTIAL | 0xffff0000  # what a user may give linear_chunk_fwd
 
 _STATUS = {
     0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED_SHAPE",
@@ -580,6 +581,8 @@ def linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale: float = 1.0
     ``segment_chunks(n)`` (segments of n 128-token chunks).  Returns ``(o, hT)``; hT is
     the S of :func:`linear_recurrent_step`.
     """
+    if int(flags) & ~_LINEAR_FLAGS:
+        raise ValueError(f"flags 0x{int(flags):x}: only FP32_CORES, SEQUENTIAL and segment_chunks(n)")
     lead = tuple(q.shape[:-2])
     dt, H, Hk, dk, dv, fl = _linear_inputs(q, k, v, g, lead)
     dev = q.device

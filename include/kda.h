@@ -428,11 +428,12 @@ kda_status_t kda_qk_norm_rope(const void* q, const void* k, int dtype, const flo
                               int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
                               kda_stream_t stream);
 
-/* Flags of the linear-attention entries. */
+/* Flags of the linear-attention entries.  The first two mean what KDA_CHUNK_FP32_CORES and
+ * KDA_CHUNK_SEQUENTIAL do; no other bit is one of kda_chunk_fwd_ex's, which are refused. */
 enum {
   KDA_LINEAR_FP32_CORES = 1u, /* prompt pass: fp32 CUDA cores even for bf16 inputs */
   KDA_LINEAR_SEQUENTIAL = 2u, /* prompt pass: never cut a sequence into segments */
-  KDA_LINEAR_HEAD_DECAY = 4u  /* g is [H]: one constant log-decay a head */
+  KDA_LINEAR_HEAD_DECAY = 64u /* g is [H]: one constant log-decay a head */
 };
 
 /*
