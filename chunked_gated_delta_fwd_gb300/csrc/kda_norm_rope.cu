@@ -6,7 +6,7 @@
 // and the channels from 2F on pass through.  Everything is fp32 but the angle: at
 // position 2^20 an fp32 product is off by 0.06 rad.  A CTA takes every f_i / (2 pi) once, in
 // fp64, as a 64-bit fraction of a turn; position times fraction modulo 2^64 is then the
-// fraction of a turn of phi, off by |pos| 2^-64, whole turns gone (an fp64 product and reduction
+// fraction of a turn of phi, whole turns gone, off by |pos| (2^-63 + |f_i| 2^-107) (an fp64 product and reduction
 // for each angle instead: 39.5 us in the 40-head case below; fp64 has a few lanes an SM).
 // One rounding, at the store.
 //
@@ -45,13 +45,17 @@ template <typename T, int kHeads> constexpr int table_size() {
   return max_tokens<T, kHeads>() * kD / 2;
 }
 
-// The part of f / (2 pi) behind the point, in 2^-64; 1 / (2 pi) as two doubles, so that a
-// position of 2^31 keeps its phase next to any frequency.
+// The part of f / (2 pi) behind the point, in 2^-64 and modulo 1.  1 / (2 pi) as two doubles, off
+// by 2^-110, so the part is off by less than 2^-63 + |f| 2^-107: a position of 2^31 keeps its phase
+// next to any frequency up to 2^40.  Taken of |f|, whose point the double u holds exactly, and
+// negated; `rest`, which passes 1 from |f| = 2^54 on, loses its whole turns as well.
 __device__ __forceinline__ uint64_t turns_of(float f) {
   constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
-  const double u = (double)f * kHi, rest = fma((double)f, kHi, -u) + (double)f * kLo;
-  return __double2ull_rz((u - floor(u)) * 0x1p64) +  // (2^64 saturates)
-         (uint64_t)__double2ll_rn(rest * 0x1p64);
+  const double x = fabs((double)f), u = x * kHi;
+  double rest = fma(x, kHi, -u) + x * kLo;
+  rest -= rint(rest);
+  const uint64_t t = __double2ull_rz((u - floor(u)) * 0x1p64) + (uint64_t)__double2ll_rn(rest * 0x1p64);
+  return f < 0.f ? 0ull - t : t;
 }
 // cos and sin of p turns: the upper 32 bits, signed, are within half a turn of 0.  `bad` is 0,
 // or NaN for a frequency that is not finite.

@@ -414,7 +414,9 @@ kda_status_t kda_recurrent_multi_step(const void* q, const void* k, const void* 
  *             any interleaving); NULL: axis 0, allowed with n_axes = 1 only.  An entry out
  *             of range is read as 0 and reported by kda_get_device_error.
  *   inv_freq  fp32 [n_freq], n_freq a multiple of 8 from 8 to 64 (64: the whole head turns);
- *             any sign and size; where one is not finite its channels are NaN.
+ *             any sign and size; where one is not finite its channels are NaN.  An angle is
+ *             off by up to |position| (2^-63 + |inv_freq| 2^-107) turns before its rounding to
+ *             fp32: nothing next to any frequency up to 2^40, all of it near 2^100.
  *   q_out, k_out  written, token strides q_out_stride, k_out_stride.  q_out may be q with
  *             the same stride (in place), k_out may be k; any other overlap of an output
  *             with an input or the other output is not allowed.
