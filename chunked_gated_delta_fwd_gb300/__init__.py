@@ -466,13 +466,17 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     """Per-head RMSNorm of q and k and the rotation by position, in one pass.
 
     q [..., Hq, 128], k [..., Hk, 128] (bf16/fp32, the same leading dimensions); both may be
-    slices of a packed projection (heads contiguous, tokens one stride apart).  ``eps`` None
-    turns the norm off; ``q_weight``/``k_weight`` fp32 [128] or None.  ``positions`` int32
+    slices of a packed projection (heads contiguous, tokens one stride apart).  ``eps`` >= 0, or
+    None to turn the norm off; ``q_weight``/``k_weight`` fp32 [128] or None.  ``positions`` int32
     [...] (the leading dimensions of q), or [n_axes, ...] with ``freq_axis`` int32 [n_freq],
     the axis of every frequency.  ``inv_freq`` fp32 [n_freq], n_freq a multiple of 8 up to 64:
     the first 2 n_freq channels turn, as pairs (i, i + n_freq) or, ``interleaved``, (2i, 2i+1).
     Returns ``(q_out, k_out)``; ``q_out=q, k_out=k`` works in place.
     """
+    if eps is None:
+        eps = -1.0  # the library's sign for no norm, which is not taken from a caller
+    elif not eps >= 0:
+        raise ValueError(f"eps must be 0 or above, or None for no norm; got {eps}")
     sq, sk = _token_stride(q, "q"), _token_stride(k, "k")
     dev, shape, shape_k = q.device, q.shape, k.shape
     lead = tuple(shape[:-2])
@@ -512,7 +516,7 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     for x in lead:
         nt *= x
     _call(lib.kda_qk_norm_rope, dev, q.data_ptr(), k.data_ptr(), dt, _addr(q_weight),
-          _addr(k_weight), -1.0 if eps is None else float(eps), positions.data_ptr(), n_axes,
+          _addr(k_weight), float(eps), positions.data_ptr(), n_axes,
           _addr(freq_axis), inv_freq.data_ptr(), n_freq, 1 if interleaved else 0,
           q_out.data_ptr(), k_out.data_ptr(), nt, H, Hk, d, sq, sk, soq, sok)
     return q_out, k_out
