@@ -582,8 +582,11 @@ def linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale: float = 1.0
     multiple of Hk (value head h uses key head h // (H // Hk)); bf16 or fp32.  g fp32
     log-decays <= 0, [..., H] (one a token and head) or [H].  h0, cu_seqlens, outputs and
     ``workspace`` as :func:`chunk_fwd`; ``flags``: ``FP32_CORES``, ``SEQUENTIAL`` and
-    ``segment_chunks(n)`` (segments of n 128-token chunks).  Returns ``(o, hT)``; hT is
-    the S of :func:`linear_recurrent_step`.
+    ``segment_chunks(n)`` (segments of n 128-token chunks).  ``out`` must not overlap an input;
+    ``final_state_out`` may be h0.  bf16 inputs run on the tensor cores, where scores and the
+    state that q meets are rounded to bf16 and what a token adds to the state keeps 16 bits
+    (hT 4e-6 off); ``FP32_CORES`` keeps fp32 sums throughout (2e-7) at some ten times the time.
+    Returns ``(o, hT)``; hT is the S of :func:`linear_recurrent_step`.
     """
     if int(flags) & ~_LINEAR_FLAGS:
         raise ValueError(f"flags 0x{int(flags):x}: only FP32_CORES, SEQUENTIAL and segment_chunks(n)")

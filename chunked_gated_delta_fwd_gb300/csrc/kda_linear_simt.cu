@@ -5,8 +5,9 @@
 //     local = sum_j e^{G_C - G_j} k_j v_j^T              (every chunk on its own)
 //     S_in  = running state over the chunks' locals       (elementwise scan)
 //     O_i   = scale (e^{G_i} S_in^T q_i + sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j)
-// Three launches after the plan, each begun while the one before ends.  Only the scan walks a sequence in order, and it does
-// nothing but add: products over the whole prompt run at once, also with one head.  Measured:
+// Three launches after the plan, each begun while the one before ends.  Only the scan walks a
+// sequence in order, and it does nothing but add: products over the whole prompt run at once, also
+// with one head.  Measured:
 // 2102 tokens in five sequences, 16 heads: 104 us (plan 4, local 31, scan 19, outputs 56 one by
 // one), 32 TFLOP/s; 64 tokens of one head 22 us, four launches' latency.
 //

@@ -16,10 +16,11 @@
 //     PV   O += P V with P = scale * decay * scores, bf16
 // Rounding: P and the copy of S to bf16 (o is bf16 as well, each adds an error of the size
 // of o's own rounding).  The final state is fp32, so Vw is kept as two bf16 parts, hi + lo
-// (17 bits of each weighted value: hT is off by 2e-6 where fp32 sums are by 2e-7), and KV is
-// issued for both.  A third part costs more than it gives: tensor memory has no room for it but
-// the outputs' columns, which makes the weighted values wait for the last chunk's outputs (8192
-// tokens x 96 heads 173 -> 244 us for 18 bits, 268 with an fp32 split for all 24).
+// (16 bits of each weighted value: off by 2^-14.9 at most and 4.4e-6 rms, so hT is off by 4.2e-6
+// where fp32 sums are by 2e-7), and KV is issued for both.  A third part costs more than it gives:
+// tensor memory has no room for it but the outputs' columns, which makes the weighted values wait
+// for the last chunk's outputs (8192 tokens x 96 heads, when it was tried, 173 -> 244 us for 18
+// bits, 268 with an fp32 split for all 24).
 //
 // What bounds a chunk is shared-memory bandwidth (128 bytes a clock): an M = N = 128 MMA
 // reads 128 bytes of operands a clock when both come from shared memory.  So P and both
@@ -29,8 +30,10 @@
 // by transposing matrix loads.  What is left a chunk: 224 KB of MMA operands, 96 KB of
 // copies, about as much again by the groups below, of 5300 clocks (678 KB) that a chunk takes
 // at one chain an SM; at all SMs busy a chunk takes 5800 and HBM bounds it.  Measured: 8192
-// tokens x 96 heads (96 of 152 SMs have a chain) 177 us, 4.6 TB/s; 14 ragged sequences of 17589
-// tokens x 48 heads 183 us, 5.2 TB/s; 131072 tokens x 16 heads in segments 509 us.
+// tokens x 96 heads (96 of 152 SMs have a chain) 178 us, 4.6 TB/s; 14 ragged sequences of 17589
+// tokens x 48 heads 183 us, 5.2 TB/s; 131072 tokens x 16 heads in segments 498 to 520 us.  Handing
+// chains out as jobs of a warp of their own, by ticket where there are several a CTA, cost the
+// first case 174 -> 178 us and brought the second from 235 to 199.
 //
 // The ring holds two whole chunks of q, k and v.
 //
@@ -44,8 +47,10 @@
 // Decays.  With L_i the sum of g inside a 32-token block up to i, U_j the sum behind j in
 // its block and T_b the block totals, every exponent but those inside a diagonal block is
 // a sum of non-positive terms: e^{G_i - G_j} = e^{L_i + T between} e^{U_j}, so a decay is
-// as exact as fp32 addition next to any g.  Inside a block it is e^{L_i - L_j}.  g is held
-// at -100 at least (e^-100 is 0 in fp32), which also makes -inf drop the state.
+// as exact as fp32 addition next to any g.  Inside a block it is e^{L_i - L_j}, two sums that
+// start at the block: behind several g of -100 in it the difference keeps about 3e-4, next to the
+// rounding of P (2^-8).  g is held at -100 at least (e^-100 is 0 in fp32), which also makes -inf
+// drop the state.
 #include <cuda.h>
 #include <string.h>
 
@@ -126,7 +131,9 @@ constexpr uint32_t kT_S = 0, kT_P = 128, kT_O = 256, kT_Vhi = 384, kT_Vlo = 448;
 
 constexpr int kGroup = 128;
 constexpr int kThreads = 128 + 6 * kGroup;  // scores and outputs take two groups each
-// A wait gives up after this many polls, each of which suspends for up to a microsecond.
+// A wait gives up after this many polls.  A poll that nothing ends was measured to take 3.8 us
+// (at this hint of 1 us), so a wait ends after 16 s; the longest that is meant to be waited for is
+// a chain's end, 2.4 us a chunk: 8e8 tokens of one head, more than the memory holds.
 constexpr uint32_t kPolls = 1u << 22, kPollNs = 1000;
 
 // Waits for the phase of `parity` to complete; 0 if it has not after kPolls polls.  (The loop
@@ -802,9 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (group <= 4) {
       if constexpr (kOut) {
       // --------------------------------------------------------------- outputs
-      // Two groups, thread = token row and 64 of its channels: O *= scale e^{G_i} between QS and PV; then the chunk goes to
-      // the q tile's slot for the copy out, a partial one (its rows end inside the tile)
-      // straight to memory.
+      // Two groups, thread = token row and 64 of its channels: O *= scale e^{G_i} between QS and
+      // PV; then the rows that the sequence has go from the registers to memory.
       const int half = group - 3;
       const uint32_t col = lanes + kT_O + 64 * half;
       int it = 0;
@@ -1203,6 +1209,9 @@ cudaError_t run(const CUtensorMap* tm, const LinArgs& a, int64_t items, bool cha
 // (8) chunks 28.9 -> 32.9, 38.4 -> 37.0, 48.0 -> 42.2 and 86.7 -> 62.8.  Two segments (51 to 76
 // chains of 152 SMs) gain what the state pass saves over a whole one: 64 heads, 32, 48, 64 and
 // 128 chunks 88 -> 93, 126 -> 127, 165 -> 159 and 319 -> 287.
+// The rule sees the number of sequences and their average length alone: short ones count as long
+// ones do, and a long prompt packed with them may stay uncut (131072 tokens x 16 heads 0.50 ms by
+// themselves, 2.46 with four one-token sequences).
 int linear_segment_chunks(int64_t n_tokens, int n_seqs, int H, int forced, bool sequential) {
   if (sequential || n_tokens == 0) return 0;
   if (forced > 0) return forced;
@@ -1253,6 +1262,7 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
     // to make up for the ordering launch (in the order given -> by ticket: 2 sequences of 300
     // and 900 tokens, 96 heads 45.8 -> 37.9 us; two of 600 44.5 -> 47.4; 8 of 65 to 975, 48
     // heads 60 -> 58; 4 of 300, 96 heads 46.4 -> 48.7; from 40 chains an SM no difference).
+    // Long is meant of the average: one long sequence among many short ones draws no tickets.
     const int64_t chains = (int64_t)n_seqs * H;
     if (cu && n_seqs > 1 && chains > sm_count() && n_tokens >= (int64_t)n_seqs * 4 * C) {
       a.ticket = static_cast<int*>(ws);

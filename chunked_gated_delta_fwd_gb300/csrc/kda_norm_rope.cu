@@ -6,19 +6,20 @@
 // and the channels from 2F on pass through.  Everything is fp32 but the angle: at
 // position 2^20 an fp32 product is off by 0.06 rad.  A CTA takes every f_i / (2 pi) once, in
 // fp64, as a 64-bit fraction of a turn; position times fraction modulo 2^64 is then the
-// fraction of a turn of phi, whole turns gone, off by |pos| (2^-63 + |f_i| 2^-107) (an fp64 product and reduction
-// for each angle instead: 39.5 us in the 40-head case below; fp64 has a few lanes an SM).
-// One rounding, at the store.
+// fraction of a turn of phi, whole turns gone, off by |pos| (2^-63 + |f_i| 2^-107).  (An fp64
+// product and reduction for each angle instead: 39.5 us in the 40-head case below against 37.5,
+// both replayed from a graph; fp64 has a few lanes an SM.)  One rounding, at the store.
 //
 // With r = 1 / sqrt(mean(x^2) + eps) a channel's result is r (x_i A_i + x_p B_i), x_p the
 // other channel of its pair, A_i = w_i cos phi and B_i = -+ w_p sin phi: the same for all
 // heads of a token.  So a warp takes sixteen (fp32: eight) rows, heads of one token where there
-// are as many, builds its lanes' A and B once a token and then needs two multiplications a channel; the pair's other channel travels as
-// raw input, four shuffles a bf16 row.
+// are as many, builds its lanes' A and B once a token and then needs two multiplications a
+// channel; the pair's other channel travels as raw input, four shuffles a bf16 row.
 //
-// Bound by HBM: a row is read and written once (8192 tokens x 192 heads bf16: 125 us, 6.4 TB/s;
-// 10007 tokens of 40 heads out of a packed projection: 37 us, 5.5 TB/s; 65536 tokens of 1 + 1
-// heads 30 us, 2.3 TB/s: there the angles, 64 for two rows, bound it).  A half warp holds
+// Bound by HBM: a row is read and written once (8192 tokens x 192 heads bf16: 127 us, 6.3 TB/s;
+// 10007 tokens of 40 heads out of a packed projection: 39 us, 5.3 TB/s; 65536 tokens of 1 + 1
+// heads 30 us, 2.3 TB/s: there the angles, 64 for two rows, bound it; fp32, twice the bytes: 281 us,
+// 5.7 TB/s, and 76 us, 5.4 TB/s, in the first two cases).  A half warp holds
 // a row, 8 channels a lane (16-byte accesses), 128 bytes of a lane in flight.  The CTAs stay
 // resident and walk the tokens; the next tokens' sines and cosines (shared by all heads) are formed
 // between two barriers' worth of rows.

@@ -451,12 +451,17 @@ enum {
  *   scale  finite.
  * KDA_BF16 inputs run on the tensor cores in 128-token chunks (fp32 accumulation and state;
  * o within about one more bf16 rounding of the fp32 result; hT sums k v^T with each weighted
- * v to 17 bits, 2e-6 relative), KDA_F32 inputs on fp32 CUDA cores.  Where (sequence, head)
- * pairs alone would leave SMs idle, long bf16 sequences are cut into segments that run at
- * once (the result equals the uncut one up to rounding); KDA_CHUNK_SEGMENT_CHUNKS(n) forces
- * segments of n 128-token chunks, KDA_LINEAR_SEQUENTIAL turns them off.  A non-finite q, k or v reaches outputs
- * of its own sequence and head only; which rows of its 128-token chunk it reaches is not
- * specified.  cu_seqlens that does not run from 0 to NT without decreasing is reported by
+ * v to 16 bits, every term within 2^-14 of itself at worst, 4.3e-6 of hT in the 2-norm as
+ * measured), KDA_F32 inputs on fp32 CUDA cores; KDA_LINEAR_FP32_CORES keeps bf16 inputs to fp32
+ * sums as well (hT 2e-7).  On the tensor cores the decay between two tokens of one 32-token
+ * block that follow several g near or below -100 in it is exact to about 3e-4.  Where there
+ * are at most half as many (sequence, head) pairs as SMs and sequences are long on average,
+ * bf16 sequences are cut into segments that run at once (the result equals the uncut one up to
+ * rounding); KDA_CHUNK_SEGMENT_CHUNKS(n) forces segments of n 128-token chunks,
+ * KDA_LINEAR_SEQUENTIAL turns them off.  The rule assumes lengths of one order: a long prompt
+ * packed with many short ones is cut only where segments are forced.  A non-finite q, k or v
+ * reaches outputs of its own sequence and head only; which rows of its 128-token chunk it
+ * reaches is not specified.  cu_seqlens that does not run from 0 to NT without decreasing is reported by
  * kda_get_device_error; the outputs are then unspecified, nothing outside o and hT is
  * written.
  * kda_linear_chunk_fwd_workspace_size: bytes of workspace (0 for invalid arguments).
