@@ -15,7 +15,13 @@ Entry points (same names as the C calls, without the ``kda_`` prefix):
 * :func:`recurrent_step` -- one decode token per sequence, state in place,
 * :func:`qk_norm_rope` -- per-head RMSNorm of q and k with the rotation by position,
 * :func:`linear_chunk_fwd`, :func:`linear_recurrent_step`,
-  :func:`linear_recurrent_multi_step` -- linear attention with a decay for each head.
+  :func:`linear_recurrent_multi_step` -- linear attention with a decay for each head,
+* :func:`causal_conv_fwd`, :func:`causal_conv_step`, :func:`causal_conv_multi_step` -- the short
+  causal convolution in front of a recurrent layer,
+* :func:`selective_scan_fwd`, :func:`selective_step`, :func:`selective_multi_step` -- the
+  selective state space scan,
+* :func:`verify_draft` -- how many drafted tokens are kept, the ``n_advance`` of the multi-step
+  calls.
 """
 
 from __future__ import annotations
@@ -34,7 +40,9 @@ __all__ = ["KdaError", "gate", "chunk_fwd", "chunk_fwd_gated", "chunk_fwd_worksp
            "chunk_fwd_fused", "gate_softplus", "UNBOUNDED_GATE",
            "output_gate", "SCALAR_GATE", "CHECK_INPUTS", "PRECISE", "selftest_wait_timeout",
            "qk_norm_rope", "linear_chunk_fwd", "linear_chunk_fwd_workspace_size",
-           "linear_recurrent_step", "linear_recurrent_multi_step"]
+           "linear_recurrent_step", "linear_recurrent_multi_step",
+           "causal_conv_fwd", "causal_conv_step", "causal_conv_multi_step",
+           "selective_scan_fwd", "selective_step", "selective_multi_step", "verify_draft"]
 
 G_MIN = -5.0
 F32, BF16 = 0, 1
@@ -101,6 +109,18 @@ def _load() -> ctypes.CDLL:
                                             i32, vp, u32]
     L.kda_linear_recurrent_multi_step.argtypes = [vp, vp, vp, i32, vp, f32, vp, vp, vp, i32, i32,
                                                   i32, i32, i32, i32, vp, u32]
+    conv = [vp, i32, vp, vp, vp]
+    L.kda_causal_conv_fwd.argtypes = conv + [vp, i32, i32, i64, i32, i32, i64, vp, i64, vp, vp, u32]
+    L.kda_causal_conv_step.argtypes = conv + [vp, i32, i32, i32, i64, i64, vp, u32]
+    L.kda_causal_conv_multi_step.argtypes = conv + [vp, vp, i32, i32, i32, i32, i64, i64, vp, u32]
+    scan = [vp, vp, vp, vp, vp, i32, vp, vp, vp]
+    L.kda_selective_scan_fwd.argtypes = scan + [vp, vp, i32, i32, i64, i32, i32, i32, i64, i64, i64,
+                                                i64, i64, vp, i64, vp, vp, u32]
+    L.kda_selective_step.argtypes = scan + [vp, vp, i32, i32, i32, i32, i64, i64, i64, i64, i64,
+                                            i64, vp, u32]
+    L.kda_selective_multi_step.argtypes = scan + [vp, vp, vp, i32, i32, i32, i32, i32, i64, i64,
+                                                  i64, i64, i64, i64, vp, u32]
+    L.kda_verify_draft.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp]
     L.kda_selftest_wait_timeout.argtypes = [u32, ctypes.POINTER(i32), vp]
     L.kda_selftest_wait_timeout.restype = ctypes.c_int
     L.kda_last_error_string.restype = ctypes.c_char_p
@@ -663,6 +683,273 @@ def linear_recurrent_multi_step(q, k, v, g, S, n_advance=None, *, scale: float =
           g.data_ptr(), float(scale), S.data_ptr(), _addr(o), _addr(n_advance), N, T, H, Hk, dk,
           dv, tail=(fl,))
     return o
+
+
+def _row_stride(t: torch.Tensor, name: str, tail: tuple, dtype=None, device=None) -> int:
+    """Elements between the tokens of a [..., *tail] tensor whose tokens are contiguous in
+    themselves and one stride apart (a slice of a packed projection has more elements a token
+    than its own); ``t`` is checked on the way."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    shape, k = t.shape, len(tail)
+    if len(shape) <= k or shape[len(shape) - k:] != tail:
+        raise ValueError(f"{name} must be [..., {', '.join(map(str, tail))}], got {tuple(shape)}")
+    row = tail[0] if k == 1 else tail[0] * tail[1]
+    if t.is_contiguous():
+        return row
+    stride = t.stride()
+    inner = 1
+    for size, s in zip(reversed(shape[-k:]), reversed(stride[-k:])):
+        if size > 1 and s != inner:
+            raise ValueError(f"{name}: the elements of a token must be contiguous")
+        inner *= size
+    step = expect = None
+    for size, s in zip(reversed(shape[:-k]), reversed(stride[:-k])):
+        if size == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != expect:
+            raise ValueError(f"{name}: the tokens must be one stride apart")
+        expect = s * size
+    return row if step is None else step
+
+
+def _packed(lead, cu_seqlens, dev, name):
+    """(N, B, T) of a prompt call whose tokens have the leading dimensions ``lead``."""
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if len(lead) not in (1, 2) or (len(lead) == 2 and lead[0] != 1):
+            raise ValueError(f"with cu_seqlens, {name} must be packed as [1, NT, C] or [NT, C]")
+        return cu_seqlens.numel() - 1, 1, lead[-1]
+    if len(lead) != 2:
+        raise ValueError(f"{name} must be [B, T, C] without cu_seqlens")
+    return lead[0], lead[0], lead[1]
+
+
+def _conv_inputs(x, weight, bias):
+    """(row stride, C, W, dtype code) of a convolution's checked inputs."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x must be a tensor [..., C]")
+    C, dev = x.shape[-1], x.device
+    sx = _row_stride(x, "x", (C,))
+    _need(weight, "weight", torch.float32, dev)
+    if weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError(f"weight must be [{C}, W], got {tuple(weight.shape)}")
+    if bias is not None:
+        _need(bias, "bias", torch.float32, dev)
+        if bias.shape != (C,):
+            raise ValueError(f"bias must be [{C}], got {tuple(bias.shape)}")
+    return sx, C, weight.shape[1], _dtype_code(x)
+
+
+def _rows_out(out, x, C):
+    """``out`` (or a new contiguous tensor) of x's shape, and its token stride."""
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), C
+    s = _row_stride(out, "out", (C,), x.dtype, x.device)
+    if out.shape != x.shape:
+        raise ValueError(f"out must be {tuple(x.shape)}, got {tuple(out.shape)}")
+    return out, s
+
+
+def causal_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, silu: bool = True,
+                    output_final_state=True, out=None, final_state_out=None):
+    """Short causal depthwise convolution over whole sequences,
+    ``y_t[c] = act(bias[c] + sum_j weight[c, j] x_{t-W+1+j}[c])``, act SiLU or (``silu=False``)
+    the identity.
+
+    x [B, T, C] or packed [NT, C] (with ``cu_seqlens``), bf16 or fp32, C a multiple of 8; its
+    tokens may be slices of a packed projection.  weight fp32 [C, W], W 2 to 4, bias fp32 [C].
+    state [N, W-1, C] (dtype of x): the inputs before each sequence, oldest first, or None.
+    ``out`` must not overlap x; ``final_state_out`` may be ``state``.
+    Returns ``(y, final_state)``; final_state (None if not asked) is the state of
+    :func:`causal_conv_step`.
+    """
+    sx, C, W, dt = _conv_inputs(x, weight, bias)
+    dev = x.device
+    N, B, T = _packed(x.shape[:-1], cu_seqlens, dev, "x")
+    shape = (N, W - 1, C)
+    if state is not None:
+        _like(state, "state", shape, x.dtype, dev)
+    last = _like(final_state_out, "final_state_out", shape, x.dtype, dev) \
+        if output_final_state else None
+    y, sy = _rows_out(out, x, C)
+    _call(lib.kda_causal_conv_fwd, dev, x.data_ptr(), dt, weight.data_ptr(), _addr(bias),
+          _addr(state), _addr(cu_seqlens), N, B, T, C, W, sx, y.data_ptr(), sy, _addr(last),
+          tail=(1 if silu else 0,))
+    return y, last
+
+
+def causal_conv_step(x, weight, state, bias=None, *, silu: bool = True, out=None):
+    """One new token of :func:`causal_conv_fwd` for N sequences: x [N, C], state [N, W-1, C]
+    updated in place.  Returns y [N, C]."""
+    sx, C, W, dt = _conv_inputs(x, weight, bias)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N, C], got {tuple(x.shape)}")
+    N, dev = x.shape[0], x.device
+    _like(state, "state", (N, W - 1, C), x.dtype, dev, given=True)
+    y, sy = _rows_out(out, x, C)
+    _call(lib.kda_causal_conv_step, dev, x.data_ptr(), dt, weight.data_ptr(), _addr(bias),
+          state.data_ptr(), y.data_ptr(), N, C, W, sx, sy, tail=(1 if silu else 0,))
+    return y
+
+
+def _advance(n_advance, N, dev):
+    if n_advance is not None:
+        _need(n_advance, "n_advance", torch.int32, dev)
+        if n_advance.numel() != N:
+            raise ValueError(f"n_advance must have {N} entries")
+    return _addr(n_advance)
+
+
+def causal_conv_multi_step(x, weight, state, n_advance=None, bias=None, *, silu: bool = True,
+                           out=None, return_outputs=True):
+    """T <= 16 new tokens a sequence: x [N, T, C], state [N, W-1, C] left as it is behind the
+    first n_advance[n] tokens (int32 [N] on the device; None = all T).  Returns y [N, T, C] (of
+    all T tokens), or None when return_outputs is False."""
+    sx, C, W, dt = _conv_inputs(x, weight, bias)
+    if x.dim() != 3:
+        raise ValueError(f"x must be [N, T, C], got {tuple(x.shape)}")
+    N, T, dev = x.shape[0], x.shape[1], x.device
+    _like(state, "state", (N, W - 1, C), x.dtype, dev, given=True)
+    adv = _advance(n_advance, N, dev)
+    y, sy = _rows_out(out, x, C) if return_outputs else (None, C)
+    _call(lib.kda_causal_conv_multi_step, dev, x.data_ptr(), dt, weight.data_ptr(), _addr(bias),
+          state.data_ptr(), _addr(y), adv, N, T, C, W, sx, sy, tail=(1 if silu else 0,))
+    return y
+
+
+def _scan_inputs(x, dt, A, B, C, D, z, dt_bias):
+    """(channels, states, groups, dtype code, strides of x, dt, B, C, z) of a scan's checked
+    inputs."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x must be a tensor [..., channels]")
+    n, dev, dtype, lead = x.shape[-1], x.device, x.dtype, x.shape[:-1]
+    _need(A, "A", torch.float32, dev)
+    if A.dim() != 2 or A.shape[0] != n:
+        raise ValueError(f"A must be [{n}, states], got {tuple(A.shape)}")
+    S = A.shape[1]
+    G = B.shape[-2] if isinstance(B, torch.Tensor) and B.dim() > 2 else 1
+    sx = _row_stride(x, "x", (n,))
+    strides = [sx]
+    for name, t, tail in (("dt", dt, (n,)), ("B", B, (G, S)), ("C", C, (G, S))):
+        strides.append(_row_stride(t, name, tail, dtype, dev))
+        if t.shape[:len(t.shape) - len(tail)] != lead:
+            raise ValueError(f"{name} must be {tuple(lead) + tail}, got {tuple(t.shape)}")
+    sz = n
+    if z is not None:
+        sz = _row_stride(z, "z", (n,), dtype, dev)
+        if z.shape != x.shape:
+            raise ValueError(f"z must be {tuple(x.shape)}, got {tuple(z.shape)}")
+    strides.append(sz)
+    for name, t in (("D", D), ("dt_bias", dt_bias)):
+        if t is not None:
+            _need(t, name, torch.float32, dev)
+            if t.shape != (n,):
+                raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
+    return n, S, G, _dtype_code(x), strides
+
+
+def selective_scan_fwd(x, dt, A, B, C, h0=None, cu_seqlens=None, *, D=None, z=None, dt_bias=None,
+                       softplus: bool = True, output_final_state=True, out=None,
+                       final_state_out=None):
+    """Prompt pass of the selective state space scan: with delta_t = softplus(dt_t + dt_bias)
+    (``softplus=False``: dt_t + dt_bias),
+    ``h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t``, ``y_t = (C_t . h_t + D x_t) SiLU(z_t)``.
+
+    x, dt, z [B, T, channels] or packed [NT, channels] (with ``cu_seqlens``), B, C
+    [..., groups, states] (states 8, 16 or 32; a group's channels, a multiple of 8, are
+    neighbours), bf16 or fp32; their tokens may be slices of packed projections.  A fp32
+    [channels, states], D and dt_bias fp32 [channels] or None, z None for no gate.  h0 fp32
+    [N, channels, states] or None.  ``out`` must not overlap an input; ``final_state_out`` may be
+    h0.  Returns ``(y, hT)``; hT (None if not asked) is the h of :func:`selective_step`.
+    """
+    n, S, G, code, (sx, sdt, sB, sC, sz) = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
+    dev = x.device
+    N, batch, T = _packed(x.shape[:-1], cu_seqlens, dev, "x")
+    if h0 is not None:
+        _like(h0, "h0", (N, n, S), torch.float32, dev)
+    hT = _like(final_state_out, "final_state_out", (N, n, S), torch.float32, dev) \
+        if output_final_state else None
+    y, sy = _rows_out(out, x, n)
+    _call(lib.kda_selective_scan_fwd, dev, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
+          C.data_ptr(), code, _addr(D), _addr(z), _addr(dt_bias), _addr(h0), _addr(cu_seqlens), N,
+          batch, T, n, S, G, sx, sdt, sB, sC, sz, y.data_ptr(), sy, _addr(hT),
+          tail=(1 if softplus else 0,))
+    return y, hT
+
+
+def selective_step(x, dt, A, B, C, h, *, D=None, z=None, dt_bias=None, softplus: bool = True,
+                   out=None):
+    """One new token of :func:`selective_scan_fwd` for N sequences: x, dt, z [N, channels], B, C
+    [N, groups, states], h fp32 [N, channels, states] updated in place.  Returns y [N, channels]."""
+    n, S, G, code, (sx, sdt, sB, sC, sz) = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N, channels], got {tuple(x.shape)}")
+    N, dev = x.shape[0], x.device
+    _like(h, "h", (N, n, S), torch.float32, dev, given=True)
+    y, sy = _rows_out(out, x, n)
+    _call(lib.kda_selective_step, dev, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
+          C.data_ptr(), code, _addr(D), _addr(z), _addr(dt_bias), h.data_ptr(), y.data_ptr(), N, n, S,
+          G, sx, sdt, sB, sC, sz, sy, tail=(1 if softplus else 0,))
+    return y
+
+
+def selective_multi_step(x, dt, A, B, C, h, n_advance=None, *, D=None, z=None, dt_bias=None,
+                         softplus: bool = True, out=None, return_outputs=True):
+    """T <= 16 new tokens a sequence: x, dt, z [N, T, channels], B, C [N, T, groups, states], h fp32
+    [N, channels, states] advanced in place by n_advance[n] tokens (int32 [N] on the device;
+    None = all T).  Returns y [N, T, channels] (of all T tokens), or None when return_outputs is
+    False."""
+    n, S, G, code, (sx, sdt, sB, sC, sz) = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
+    if x.dim() != 3:
+        raise ValueError(f"x must be [N, T, channels], got {tuple(x.shape)}")
+    N, T, dev = x.shape[0], x.shape[1], x.device
+    _like(h, "h", (N, n, S), torch.float32, dev, given=True)
+    adv = _advance(n_advance, N, dev)
+    y, sy = _rows_out(out, x, n) if return_outputs else (None, n)
+    _call(lib.kda_selective_multi_step, dev, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+          B.data_ptr(), C.data_ptr(), code, _addr(D), _addr(z), _addr(dt_bias), h.data_ptr(),
+          _addr(y), adv, N, T, n, S, G, sx, sdt, sB, sC, sz, sy, tail=(1 if softplus else 0,))
+    return y
+
+
+def verify_draft(draft_tokens, draft_probs, target_probs, accept_uniforms, sample_uniforms, *,
+                 tokens_out=None, n_advance_out=None):
+    """Decides how many drafted tokens every sequence keeps and draws the token behind them.
+
+    draft_tokens int32 [N, T] (T <= 15; an entry outside the vocabulary ends a draft), the
+    distributions they were drawn from draft_probs [N, T, V], the target's target_probs
+    [N, T+1, V] (bf16 or fp32), accept_uniforms fp32 [N, T] and sample_uniforms fp32 [N] in [0, 1).
+    Token i is accepted while ``accept_uniforms[i] * q_i(d_i) < p_i(d_i)``; the next one is drawn
+    from max(p - q, 0) where one was rejected, else from p.  Returns ``(tokens, n_advance)``: int32
+    [N, T+1], the accepted tokens, the drawn one, then -1, and int32 [N], how many they are: the
+    n_advance of the multi-step calls over the last token before the draft and the draft.
+    """
+    dev = target_probs.device if isinstance(target_probs, torch.Tensor) else None
+    _need(target_probs, "target_probs")
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        raise ValueError(f"target_probs must be [N, T+1, V], got {tuple(target_probs.shape)}")
+    N, T, V = target_probs.shape
+    T -= 1
+    dt = _dtype_code(target_probs)
+    _like(draft_tokens, "draft_tokens", (N, T), torch.int32, dev, given=True)
+    _like(draft_probs, "draft_probs", (N, T, V), target_probs.dtype, dev, given=True)
+    _like(accept_uniforms, "accept_uniforms", (N, T), torch.float32, dev, given=True)
+    _like(sample_uniforms, "sample_uniforms", (N,), torch.float32, dev, given=True)
+    tokens = _like(tokens_out, "tokens_out", (N, T + 1), torch.int32, dev)
+    count = _like(n_advance_out, "n_advance_out", (N,), torch.int32, dev)
+    _call(lib.kda_verify_draft, dev, draft_tokens.data_ptr(), draft_probs.data_ptr(),
+          target_probs.data_ptr(), dt, accept_uniforms.data_ptr(), sample_uniforms.data_ptr(),
+          tokens.data_ptr(), count.data_ptr(), N, T, V)
+    return tokens, count
 
 
 def profile_enable(on: bool = True):

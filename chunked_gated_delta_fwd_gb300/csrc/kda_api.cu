@@ -886,3 +886,280 @@ kda_status_t kda_linear_recurrent_multi_step(const void* q, const void* k, const
 }
 
 }  // extern "C"
+
+namespace {
+
+// Counts that the prompt passes share: N sequences of NT tokens in all.
+kda_status_t packed_counts(const char* fn, const int32_t* cu_seqlens, int n_seqs, int B, int64_t T,
+                           int* N, int64_t* NT) {
+  if (T < 0 || T > INT32_MAX - 65536)
+    return fail(KDA_ERR_INVALID_ARG, "%s: T=%lld", fn, (long long)T);
+  if (cu_seqlens) {
+    if (B != 1) return fail(KDA_ERR_INVALID_ARG, "%s: B must be 1 with cu_seqlens", fn);
+    if (n_seqs < 1) return fail(KDA_ERR_INVALID_ARG, "%s: n_seqs=%d", fn, n_seqs);
+    *N = n_seqs;
+    *NT = T;
+  } else {
+    if (B < 1) return fail(KDA_ERR_INVALID_ARG, "%s: B=%d", fn, B);
+    *N = B;
+    *NT = (int64_t)B * T;
+  }
+  if (*NT > INT32_MAX - 65536)
+    return fail(KDA_ERR_INVALID_ARG, "%s: token count out of range", fn);
+  return KDA_OK;
+}
+
+// A tensor whose tokens are `stride` elements apart and hold `row` elements each.
+struct Rows {
+  const void* p;
+  int64_t stride, row;
+  const char* name;
+};
+template <int kN>
+kda_status_t check_rows(const char* fn, int dtype, const Rows (&rows)[kN]) {
+  const int per16 = dtype == KDA_BF16 ? 8 : 4;
+  for (const Rows& r : rows) {
+    if (!r.p) continue;
+    if (r.stride < r.row || r.stride > ((int64_t)1 << 31))
+      return fail(KDA_ERR_INVALID_ARG, "%s: %s: a token stride of %lld for %lld elements", fn, r.name,
+                  (long long)r.stride, (long long)r.row);
+    if (!aligned16(r.p) || r.stride % per16 != 0)
+      return fail(KDA_ERR_MISALIGNED, "%s: %s: tokens must begin on 16-byte boundaries", fn, r.name);
+  }
+  return KDA_OK;
+}
+
+kda_status_t conv_shape(const char* fn, int dtype, int C, int W, unsigned flags) {
+  if (dtype != KDA_F32 && dtype != KDA_BF16)
+    return fail(KDA_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d", fn, dtype);
+  if (C < 8 || C % 8 != 0 || C > (1 << 24))
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: C=%d (a multiple of 8)", fn, C);
+  if (W < 2 || W > 4) return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: W=%d (2, 3 or 4)", fn, W);
+  if (flags & ~(unsigned)KDA_CONV_SILU)
+    return fail(KDA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
+  return KDA_OK;
+}
+
+kda_status_t conv_step_impl(const char* fn, const void* x, int dtype, const float* weight,
+                            const float* bias, void* state, void* y, const int32_t* n_advance,
+                            int N, int T, int C, int W, int64_t x_stride, int64_t y_stride,
+                            kda_stream_t stream, unsigned flags, bool multi) {
+  kda_status_t st = conv_shape(fn, dtype, C, W, flags);
+  if (st != KDA_OK) return st;
+  if (N < 0 || T < 1 || T > KDA_MULTI_STEP_MAX_T)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: N=%d T=%d", fn, N, T);
+  if ((int64_t)N * T > INT32_MAX - 65536)
+    return fail(KDA_ERR_INVALID_ARG, "%s: N*T too large", fn);
+  if (N == 0) return KDA_OK;
+  if (!x || !weight || !state || (!y && !multi))
+    return fail(KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned16(weight) || (bias && !aligned16(bias)) || !aligned16(state))
+    return fail(KDA_ERR_MISALIGNED, "%s: pointers must be 16-byte aligned", fn);
+  const Rows rows[] = {{x, x_stride, C, "x"}, {y, y_stride, C, "y"}};
+  if ((st = check_rows(fn, dtype, rows)) != KDA_OK) return st;
+  if ((st = check_device()) != KDA_OK) return st;
+  cudaError_t e = kda::launch_conv_step(x, dtype == KDA_BF16, weight, bias, state, y, n_advance, N, T,
+                                        C, W, x_stride, y_stride, (flags & KDA_CONV_SILU) != 0,
+                                        reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return KDA_OK;
+}
+
+kda_status_t scan_shape(const char* fn, int dtype, int channels, int states, int groups,
+                        unsigned flags) {
+  if (dtype != KDA_F32 && dtype != KDA_BF16)
+    return fail(KDA_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d", fn, dtype);
+  if (states != 8 && states != 16 && states != 32)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: %d states a channel (8, 16 or 32)", fn, states);
+  if (groups < 1 || channels < 8 || channels > (1 << 24) || channels % groups != 0 ||
+      channels / groups % 8 != 0)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE,
+                "%s: %d channels in %d groups (a multiple of 8 in each)", fn, channels, groups);
+  if (flags & ~(unsigned)KDA_SCAN_SOFTPLUS)
+    return fail(KDA_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
+  return KDA_OK;
+}
+
+// Pointers and strides of a scan over tokens (`need_y`: y has to be given).
+kda_status_t scan_tensors(const char* fn, int dtype, int states, const kda::ScanArgs& a,
+                          const float* state, bool need_y) {
+  if (!a.x || !a.dt || !a.A || !a.B || !a.Cm || (need_y && !a.y))
+    return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
+  const void* ptrs[] = {a.A, a.D, a.bias, a.h0, a.hT, state};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p))
+      return fail(KDA_ERR_MISALIGNED, "%s: pointers must be 16-byte aligned", fn);
+  const int64_t bc = (int64_t)a.G * states;
+  const Rows rows[] = {{a.x, a.sx, a.C, "x"}, {a.dt, a.sdt, a.C, "dt"}, {a.B, a.sB, bc, "B"},
+                       {a.Cm, a.sC, bc, "C"}, {a.z, a.sz, a.C, "z"},    {a.y, a.sy, a.C, "y"}};
+  return check_rows(fn, dtype, rows);
+}
+
+kda_status_t scan_step_impl(const char* fn, const void* x, const void* dt, const float* A,
+                            const void* B, const void* C, int dtype, const float* D, const void* z,
+                            const float* dt_bias, float* h, void* y, const int32_t* n_advance,
+                            int N, int T, int channels, int states, int groups, int64_t x_stride,
+                            int64_t dt_stride, int64_t B_stride, int64_t C_stride,
+                            int64_t z_stride, int64_t y_stride, kda_stream_t stream,
+                            unsigned flags, bool multi) {
+  kda_status_t st = scan_shape(fn, dtype, channels, states, groups, flags);
+  if (st != KDA_OK) return st;
+  if (N < 0 || T < 1 || T > KDA_MULTI_STEP_MAX_T)
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: N=%d T=%d", fn, N, T);
+  if ((int64_t)N * T > INT32_MAX - 65536)
+    return fail(KDA_ERR_INVALID_ARG, "%s: N*T too large", fn);
+  if (N == 0) return KDA_OK;
+  if (!h) return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
+  const kda::ScanArgs a{x,        dt,        B,        C,        z,        A,
+                        D,        dt_bias,   nullptr,  nullptr,  y,        nullptr,
+                        T,        (int64_t)N * T, x_stride, dt_stride, B_stride, C_stride,
+                        z_stride, y_stride,  N,        channels, groups,
+                        (flags & KDA_SCAN_SOFTPLUS) != 0};
+  if ((st = scan_tensors(fn, dtype, states, a, h, !multi)) != KDA_OK) return st;
+  if ((st = check_device()) != KDA_OK) return st;
+  cudaError_t e = kda::launch_scan_step(a, dtype == KDA_BF16, states, h, n_advance, multi,
+                                        reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_causal_conv_fwd(const void* x, int dtype, const float* weight, const float* bias,
+                                 const void* state, const int32_t* cu_seqlens, int n_seqs, int B,
+                                 int64_t T, int C, int W, int64_t x_stride, void* y,
+                                 int64_t y_stride, void* final_state, kda_stream_t stream,
+                                 unsigned flags) {
+  const char* fn = "kda_causal_conv_fwd";
+  int N;
+  int64_t NT;
+  kda_status_t st = conv_shape(fn, dtype, C, W, flags);
+  if (st == KDA_OK) st = packed_counts(fn, cu_seqlens, n_seqs, B, T, &N, &NT);
+  if (st != KDA_OK) return st;
+  if (!weight || (NT > 0 && (!x || !y)))
+    return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
+  const void* ptrs[] = {weight, bias, state, final_state};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p))
+      return fail(KDA_ERR_MISALIGNED, "%s: pointers must be 16-byte aligned", fn);
+  if (NT > 0) {
+    const Rows rows[] = {{x, x_stride, C, "x"}, {y, y_stride, C, "y"}};
+    if ((st = check_rows(fn, dtype, rows)) != KDA_OK) return st;
+  } else if (!final_state) {
+    return KDA_OK;
+  }
+  if ((st = check_device()) != KDA_OK) return st;
+  cudaError_t e = kda::launch_conv(x, dtype == KDA_BF16, weight, bias, state, cu_seqlens, T, y,
+                                   final_state, NT, N, C, W, x_stride, y_stride,
+                                   (flags & KDA_CONV_SILU) != 0, kda::device_error_flag(),
+                                   reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return KDA_OK;
+}
+
+kda_status_t kda_causal_conv_step(const void* x, int dtype, const float* weight, const float* bias,
+                                  void* state, void* y, int N, int C, int W, int64_t x_stride,
+                                  int64_t y_stride, kda_stream_t stream, unsigned flags) {
+  return conv_step_impl("kda_causal_conv_step", x, dtype, weight, bias, state, y, nullptr, N, 1, C,
+                        W, x_stride, y_stride, stream, flags, false);
+}
+
+kda_status_t kda_causal_conv_multi_step(const void* x, int dtype, const float* weight,
+                                        const float* bias, void* state, void* y,
+                                        const int32_t* n_advance, int N, int T, int C, int W,
+                                        int64_t x_stride, int64_t y_stride, kda_stream_t stream,
+                                        unsigned flags) {
+  return conv_step_impl("kda_causal_conv_multi_step", x, dtype, weight, bias, state, y, n_advance,
+                        N, T, C, W, x_stride, y_stride, stream, flags, true);
+}
+
+kda_status_t kda_selective_scan_fwd(const void* x, const void* dt, const float* A, const void* B,
+                                    const void* C, int dtype, const float* D, const void* z,
+                                    const float* dt_bias, const float* h0,
+                                    const int32_t* cu_seqlens, int n_seqs, int batch, int64_t T,
+                                    int channels, int states, int groups, int64_t x_stride,
+                                    int64_t dt_stride, int64_t B_stride, int64_t C_stride,
+                                    int64_t z_stride, void* y, int64_t y_stride, float* hT,
+                                    kda_stream_t stream, unsigned flags) {
+  const char* fn = "kda_selective_scan_fwd";
+  int N;
+  int64_t NT;
+  kda_status_t st = scan_shape(fn, dtype, channels, states, groups, flags);
+  if (st == KDA_OK) st = packed_counts(fn, cu_seqlens, n_seqs, batch, T, &N, &NT);
+  if (st != KDA_OK) return st;
+  if (NT == 0 && !hT) return KDA_OK;
+  const kda::ScanArgs a{x,        dt,       B,         C,        z,        A,        D,  dt_bias,
+                        h0,       cu_seqlens, y,       hT,       T,        NT,       x_stride,
+                        dt_stride, B_stride, C_stride, z_stride, y_stride, N,        channels,
+                        groups,   (flags & KDA_SCAN_SOFTPLUS) != 0};
+  if (NT > 0) {
+    if ((st = scan_tensors(fn, dtype, states, a, nullptr, true)) != KDA_OK) return st;
+  } else {
+    const void* ptrs[] = {A, D, dt_bias, h0, hT};
+    if (!A) return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
+    for (const void* p : ptrs)
+      if (p && !aligned16(p))
+        return fail(KDA_ERR_MISALIGNED, "%s: pointers must be 16-byte aligned", fn);
+  }
+  if ((st = check_device()) != KDA_OK) return st;
+  cudaError_t e = kda::launch_scan(a, dtype == KDA_BF16, states, kda::device_error_flag(),
+                                   reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return KDA_OK;
+}
+
+kda_status_t kda_selective_step(const void* x, const void* dt, const float* A, const void* B,
+                                const void* C, int dtype, const float* D, const void* z,
+                                const float* dt_bias, float* h, void* y, int N, int channels,
+                                int states, int groups, int64_t x_stride, int64_t dt_stride,
+                                int64_t B_stride, int64_t C_stride, int64_t z_stride,
+                                int64_t y_stride, kda_stream_t stream, unsigned flags) {
+  return scan_step_impl("kda_selective_step", x, dt, A, B, C, dtype, D, z, dt_bias, h, y, nullptr,
+                        N, 1, channels, states, groups, x_stride, dt_stride, B_stride, C_stride,
+                        z_stride, y_stride, stream, flags, false);
+}
+
+kda_status_t kda_selective_multi_step(const void* x, const void* dt, const float* A, const void* B,
+                                      const void* C, int dtype, const float* D, const void* z,
+                                      const float* dt_bias, float* h, void* y,
+                                      const int32_t* n_advance, int N, int T, int channels,
+                                      int states, int groups, int64_t x_stride, int64_t dt_stride,
+                                      int64_t B_stride, int64_t C_stride, int64_t z_stride,
+                                      int64_t y_stride, kda_stream_t stream, unsigned flags) {
+  return scan_step_impl("kda_selective_multi_step", x, dt, A, B, C, dtype, D, z, dt_bias, h, y,
+                        n_advance, N, T, channels, states, groups, x_stride, dt_stride, B_stride,
+                        C_stride, z_stride, y_stride, stream, flags, true);
+}
+
+kda_status_t kda_verify_draft(const int32_t* draft_tokens, const void* draft_probs,
+                              const void* target_probs, int dtype, const float* accept_uniforms,
+                              const float* sample_uniforms, int32_t* tokens, int32_t* n_advance,
+                              int N, int T, int vocab, kda_stream_t stream) {
+  const char* fn = "kda_verify_draft";
+  if (dtype != KDA_F32 && dtype != KDA_BF16)
+    return fail(KDA_ERR_UNSUPPORTED_DTYPE, "%s: dtype %d", fn, dtype);
+  if (N < 0 || N > (1 << 24) || T < 0 || T >= KDA_MULTI_STEP_MAX_T || vocab < 1 ||
+      vocab > (1 << 30))
+    return fail(KDA_ERR_UNSUPPORTED_SHAPE, "%s: N=%d T=%d vocab=%d", fn, N, T, vocab);
+  if (N == 0) return KDA_OK;
+  if (!target_probs || !sample_uniforms || !tokens || !n_advance ||
+      (T > 0 && (!draft_tokens || !draft_probs || !accept_uniforms)))
+    return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
+  if (!aligned16(target_probs) || (draft_probs && !aligned16(draft_probs)))
+    return fail(KDA_ERR_MISALIGNED, "%s: probabilities must be 16-byte aligned", fn);
+  const void* words[] = {draft_tokens, accept_uniforms, sample_uniforms, tokens, n_advance};
+  for (const void* p : words)
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)
+      return fail(KDA_ERR_MISALIGNED, "%s: pointers must be 4-byte aligned", fn);
+  kda_status_t st = check_device();
+  if (st != KDA_OK) return st;
+  cudaError_t e = kda::launch_verify(draft_tokens, draft_probs, target_probs, dtype == KDA_BF16,
+                                     accept_uniforms, sample_uniforms, tokens, n_advance, N, T,
+                                     vocab, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  return KDA_OK;
+}
+
+}  // extern "C"

@@ -245,4 +245,38 @@ cudaError_t launch_linear_tc(const void* q, const void* k, const void* v, const 
                              int64_t T_per_seq, void* o, float* hT, int64_t n_tokens, int n_seqs,
                              int H, int Hk, int seg_chunks, void* ws, int* err, cudaStream_t s);
 
+// Short causal depthwise convolution: strides in elements between tokens; w [C][W], b [C] or
+// null, state and last [N][W-1][C] or null (last may be state).
+cudaError_t launch_conv(const void* x, int bf16, const float* w, const float* b, const void* state,
+                        const int32_t* cu, int64_t T_per_seq, void* y, void* last, int64_t n_tokens,
+                        int n_seqs, int C, int W, int64_t sx, int64_t sy, int act, int* err,
+                        cudaStream_t s);
+// T new tokens of N sequences; y may be null.
+cudaError_t launch_conv_step(const void* x, int bf16, const float* w, const float* b, void* state,
+                             void* y, const int32_t* n_advance, int N, int T, int C, int W,
+                             int64_t sx, int64_t sy, int act, cudaStream_t s);
+
+// Selective state space scan.  Strides are elements between tokens.
+struct ScanArgs {
+  const void *x, *dt, *B, *Cm, *z;  // [tokens][C], [tokens][C], [tokens][G][S] twice, [tokens][C]
+  const float *A, *D, *bias;        // [C][S], [C], [C]; z, D and bias may be null
+  const float* h0;                  // [N][C][S] or null
+  const int32_t* cu;                // [N+1], or null: T tokens a sequence
+  void* y;
+  float* hT;                        // [N][C][S] or null
+  int64_t T, NT;
+  int64_t sx, sdt, sB, sC, sz, sy;
+  int N, C, G, softplus;
+};
+cudaError_t launch_scan(const ScanArgs& a, int bf16, int S, int* err, cudaStream_t s);
+// a.T new tokens of a.N sequences, the states [N][C][S] advanced by n_advance[n] of them (null:
+// all); a.y may be null.
+cudaError_t launch_scan_step(const ScanArgs& a, int bf16, int S, float* state,
+                             const int32_t* n_advance, bool multi, cudaStream_t s);
+
+// Verification of T <= 15 drafted tokens of N sequences against V probabilities a place.
+cudaError_t launch_verify(const int32_t* draft, const void* q, const void* p, int bf16,
+                          const float* u_accept, const float* u_sample, int32_t* tokens,
+                          int32_t* n_advance, int N, int T, int V, cudaStream_t s);
+
 }  // namespace kda

@@ -494,6 +494,131 @@ kda_status_t kda_linear_recurrent_multi_step(const void* q, const void* k, const
                                              int H, int Hk, int dk, int dv, kda_stream_t stream,
                                              unsigned flags);
 
+/* Flag of the causal convolution: SiLU behind it. */
+enum { KDA_CONV_SILU = 1u };
+
+/*
+ * kda_causal_conv_fwd -- the short causal depthwise convolution in front of a recurrent layer
+ * (the k = 4 convolution and Swish on q, k and v: "Kimi K3: architecture, training and
+ * inference systems", section 3.2), over whole packed sequences:
+ *     y_t[c] = act(bias[c] + sum_{j < W} weight[c][j] x_{t-W+1+j}[c])
+ *   x, y     [NT] rows of C channels of `dtype`, token t at t * x_stride (y_stride) elements:
+ *            slices of a packed projection need no copy.  Strides are at least C and multiples
+ *            of 16 bytes; C is a multiple of 8.  y must not overlap an input.
+ *   weight   fp32 [C][W], W = 2, 3 or 4, the last tap on the token itself; bias fp32 [C] or NULL.
+ *   state    [N][W-1][C] of `dtype`: the inputs before each sequence, oldest first (NULL: zeros).
+ *   final_state  like state, written (NULL to skip): the last W-1 inputs, those of `state` among
+ *            them where a sequence is shorter; it may be `state`.  It continues as the state of
+ *            the calls below.
+ *   cu_seqlens, n_seqs, B, T  as kda_chunk_fwd.  Offsets that do not run from 0 to NT without
+ *            decreasing are reported by kda_get_device_error; y and final_state are then
+ *            unspecified, nothing outside them is written.
+ *   flags    KDA_CONV_SILU: act is x Sigmoid(x), else the identity.
+ * Sums are fp32, rounded once to `dtype`.  No workspace.
+ */
+kda_status_t kda_causal_conv_fwd(const void* x, int dtype, const float* weight, const float* bias,
+                                 const void* state, const int32_t* cu_seqlens, int n_seqs, int B,
+                                 int64_t T, int C, int W, int64_t x_stride, void* y,
+                                 int64_t y_stride, void* final_state, kda_stream_t stream,
+                                 unsigned flags);
+
+/*
+ * kda_causal_conv_step -- one new token of N sequences: x, y [N] rows, state [N][W-1][C] read and
+ * overwritten in place.  N == 0 is a no-op.
+ *
+ * kda_causal_conv_multi_step -- T (1..KDA_MULTI_STEP_MAX_T) tokens a sequence, row n * T + t:
+ * outputs of all T (y may be NULL), the state as it is behind the first n_advance[n] tokens
+ * (device int32 [N], clamped to [0, T]; NULL = all T; 0 leaves it unchanged).
+ */
+kda_status_t kda_causal_conv_step(const void* x, int dtype, const float* weight, const float* bias,
+                                  void* state, void* y, int N, int C, int W, int64_t x_stride,
+                                  int64_t y_stride, kda_stream_t stream, unsigned flags);
+kda_status_t kda_causal_conv_multi_step(const void* x, int dtype, const float* weight,
+                                        const float* bias, void* state, void* y,
+                                        const int32_t* n_advance, int N, int T, int C, int W,
+                                        int64_t x_stride, int64_t y_stride, kda_stream_t stream,
+                                        unsigned flags);
+
+/* Flag of the selective scan: delta = softplus(dt + dt_bias), else dt + dt_bias. */
+enum { KDA_SCAN_SOFTPLUS = 1u };
+
+/*
+ * kda_selective_scan_fwd -- prompt pass of the selective state space scan, the recurrence of a
+ * layer with a decay for each channel and state and with an input-dependent step:
+ *     delta_t[c] = softplus(dt_t[c] + dt_bias[c])
+ *     h_t[c][s]  = exp(delta_t[c] A[c][s]) h_{t-1}[c][s] + delta_t[c] x_t[c] B_t[g][s]
+ *     y_t[c]     = (sum_s C_t[g][s] h_t[c][s] + D[c] x_t[c]) * z_t[c] Sigmoid(z_t[c])
+ * with g = c / (channels / groups) the group of channel c.
+ *   x, dt, z, y  [NT] rows of `channels` elements of `dtype`; z may be NULL (no gate).
+ *   B, C     [NT] rows of groups x states elements of `dtype`; states 8, 16 or 32.
+ *            Tokens of all of these are their own stride apart (at least a row, a multiple of 16
+ *            bytes).  channels / groups is a multiple of 8.  y must not overlap an input.
+ *   A        fp32 [channels][states], finite, <= 0 for decays; D, dt_bias fp32 [channels] or NULL
+ *            (zeros).
+ *   h0, hT   fp32 [N][channels][states], optional; hT may be h0.  hT continues as the h of the
+ *            calls below.
+ *   cu_seqlens, n_seqs, batch, T  as kda_chunk_fwd's cu_seqlens, n_seqs, B, T; malformed offsets
+ *            as kda_causal_conv_fwd.
+ * Decays, states and sums are fp32, y is rounded once to `dtype`.  A sequence of length 0 gets
+ * hT = h0 (or zeros).  No workspace.
+ */
+kda_status_t kda_selective_scan_fwd(const void* x, const void* dt, const float* A, const void* B,
+                                    const void* C, int dtype, const float* D, const void* z,
+                                    const float* dt_bias, const float* h0,
+                                    const int32_t* cu_seqlens, int n_seqs, int batch, int64_t T,
+                                    int channels, int states, int groups, int64_t x_stride,
+                                    int64_t dt_stride, int64_t B_stride, int64_t C_stride,
+                                    int64_t z_stride, void* y, int64_t y_stride, float* hT,
+                                    kda_stream_t stream, unsigned flags);
+
+/*
+ * kda_selective_step -- one token of the scan above for N sequences, the states h fp32
+ * [N][channels][states] updated in place.  N == 0 is a no-op.
+ *
+ * kda_selective_multi_step -- T (1..KDA_MULTI_STEP_MAX_T) tokens a sequence, row n * T + t;
+ * n_advance and y (may be NULL) as kda_causal_conv_multi_step.
+ */
+kda_status_t kda_selective_step(const void* x, const void* dt, const float* A, const void* B,
+                                const void* C, int dtype, const float* D, const void* z,
+                                const float* dt_bias, float* h, void* y, int N, int channels,
+                                int states, int groups, int64_t x_stride, int64_t dt_stride,
+                                int64_t B_stride, int64_t C_stride, int64_t z_stride,
+                                int64_t y_stride, kda_stream_t stream, unsigned flags);
+kda_status_t kda_selective_multi_step(const void* x, const void* dt, const float* A, const void* B,
+                                      const void* C, int dtype, const float* D, const void* z,
+                                      const float* dt_bias, float* h, void* y,
+                                      const int32_t* n_advance, int N, int T, int channels,
+                                      int states, int groups, int64_t x_stride, int64_t dt_stride,
+                                      int64_t B_stride, int64_t C_stride, int64_t z_stride,
+                                      int64_t y_stride, kda_stream_t stream, unsigned flags);
+
+/*
+ * kda_verify_draft -- decides how many drafted tokens every sequence keeps, the n_advance of the
+ * multi-step calls (the accept / reject step between speculative verify and replay: "Kimi K3:
+ * architecture, training and inference systems", section 13.2).  Token i of a draft, drawn from
+ * q_i, is accepted while accept_uniforms_i q_i(d_i) < p_i(d_i) (the products exact); behind the k
+ * accepted ones a token is drawn from max(p_k - q_k, 0) if d_k was rejected, from p_k if
+ * the draft had ended there: the first index whose running sum exceeds sample_uniforms times
+ * the sum.  Tokens so obtained are distributed as if drawn from p one by one.
+ *   draft_tokens  int32 [N][T], T in 0..KDA_MULTI_STEP_MAX_T - 1; an entry outside
+ *            [0, vocab) ends that sequence's draft (shorter drafts are padded with -1).
+ *   draft_probs, target_probs  [N][T][vocab] and [N][T+1][vocab] of `dtype` (p_T follows the
+ *            whole draft); they need not add up to 1 exactly.  What is not above 0 (NaN too)
+ *            weighs nothing, what is above 1 weighs 1.
+ *   accept_uniforms, sample_uniforms  fp32 [N][T] and [N], in [0, 1); the latter to 24 bits.
+ *   tokens   int32 [N][T+1], written: the accepted ones, the drawn one, -1 behind it.
+ *   n_advance  int32 [N], written: k + 1, the tokens valid in `tokens` and the number of inputs
+ *            (the last token before the draft and the k accepted) that states advance by.
+ * Where nothing is left of max(p_k - q_k, 0) the token is drawn from p_k, where p_k is 0
+ * everywhere it is 0.  Weights are whole numbers of 2^-56 (the difference rounded to fp32
+ * before), so that sums are exact and results do not depend on the order of additions; sums
+ * stop at 256.  N == 0 is a no-op.
+ */
+kda_status_t kda_verify_draft(const int32_t* draft_tokens, const void* draft_probs,
+                              const void* target_probs, int dtype, const float* accept_uniforms,
+                              const float* sample_uniforms, int32_t* tokens, int32_t* n_advance,
+                              int N, int T, int vocab, kda_stream_t stream);
+
 /* Message for the last non-OK status returned on this thread (never NULL). */
 const char* kda_last_error_string(void);
 

@@ -31,6 +31,8 @@ Functions and the passages they follow:
 * :func:`output_gate` -- the head-wise RMSNorm of the KDA output times the
   full-rank Sigmoid gate ("Kimi K3 technical report review", section 3.3, Eq. 6;
   the same systems page, section 3.3), without the W_o / W_g projections.
+* :func:`causal_conv`, :func:`selective_scan`, :func:`verify_draft` -- the short causal
+  convolution, the selective state space scan and the verification of drafted tokens.
 
 Pins: ``tests/test_oracle.py`` checks these against closed forms, special
 cases and invariants the pages fix (see that file's docstring).
@@ -331,3 +333,106 @@ def norm_rope(x, positions, inv_freq, weight=None, eps=1e-6, freq_axis=None, int
     z = (y[..., lo] + 1j * y[..., hi]) * turn
     out[..., lo], out[..., hi] = z.real, z.imag
     return out
+
+
+def _silu(x):
+    with np.errstate(over="ignore"):
+        return x / (1.0 + np.exp(-x))
+
+
+def _softplus(x):
+    return np.maximum(x, 0.0) + np.log1p(np.exp(-np.abs(x)))
+
+
+def causal_conv(x, weight, bias=None, state=None, cu_seqlens=None, silu=True, n_advance=None):
+    """Short causal depthwise convolution, y_t = act(bias + sum_j w[:, j] x_{t-W+1+j}); the inputs
+    before a sequence are state[n] [W-1, C] or zeros.  Returns (y, final state), the latter behind
+    the first n_advance[n] tokens of a sequence (None: all)."""
+    x, w = _f64(x), _f64(weight)
+    W, C = w.shape[1], x.shape[-1]
+    cu = [0, x.shape[0]] if cu_seqlens is None else [int(c) for c in cu_seqlens]
+    N = len(cu) - 1
+    old = np.zeros((N, W - 1, C)) if state is None else _f64(state)
+    y, last = np.zeros_like(x), np.zeros((N, W - 1, C))
+    for n in range(N):
+        rows = np.concatenate([old[n], x[cu[n]:cu[n + 1]]])
+        size = cu[n + 1] - cu[n]
+        for t in range(size):
+            y[cu[n] + t] = np.einsum("wc,cw->c", rows[t:t + W], w)
+        adv = size if n_advance is None else min(max(int(n_advance[n]), 0), size)
+        last[n] = rows[adv:adv + W - 1]
+    if bias is not None:
+        y = y + _f64(bias)
+    return (_silu(y) if silu else y), last
+
+
+def selective_scan(x, dt, A, B, C, h0=None, cu_seqlens=None, D=None, z=None, dt_bias=None,
+                   softplus=True, n_advance=None):
+    """h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t, y_t = (C_t . h_t + D x_t) SiLU(z_t) token by
+    token: x, dt, z [NT, channels], A [channels, S], B, C [NT, G, S], h0 [N, channels, S].
+    Returns (y, hT), the latter behind the first n_advance[n] tokens (None: all)."""
+    x, dt, A, B, C = _f64(x), _f64(dt), _f64(A), _f64(B), _f64(C)
+    nt, ch = x.shape
+    per = ch // B.shape[1]
+    delta = dt + (0.0 if dt_bias is None else _f64(dt_bias))
+    if softplus:
+        delta = _softplus(delta)
+    cu = [0, nt] if cu_seqlens is None else [int(c) for c in cu_seqlens]
+    N = len(cu) - 1
+    y, hT = np.zeros_like(x), np.zeros((N,) + A.shape)
+    for n in range(N):
+        h = np.zeros_like(A) if h0 is None else _f64(h0)[n].copy()
+        adv = cu[n + 1] - cu[n] if n_advance is None else int(n_advance[n])
+        hT[n] = h
+        for t in range(cu[n], cu[n + 1]):
+            b, c = np.repeat(B[t], per, axis=0), np.repeat(C[t], per, axis=0)
+            h = np.exp(delta[t][:, None] * A) * h + (delta[t] * x[t])[:, None] * b
+            y[t] = (c * h).sum(axis=1)
+            if t - cu[n] < adv:
+                hT[n] = h
+    if D is not None:
+        y = y + _f64(D) * x
+    if z is not None:
+        y = y * _silu(_f64(z))
+    return y, hT
+
+
+def verify_draft(draft, q, p, u_accept, u_sample):
+    """Accepted drafted tokens and the token behind them, in exact fractions: draft [N][T], q
+    [N][T][V], p [N][T+1][V].  Returns (tokens [N][T+1], n_advance [N])."""
+    from fractions import Fraction
+
+    p, q = _f64(p), _f64(q)
+    N, T1, V = p.shape
+    tokens, count = np.full((N, T1), -1, dtype=np.int64), np.zeros(N, dtype=np.int64)
+
+    def whole(w):
+        return [int(min(max(float(v), 0.0), 1.0) * 2.0 ** 56) if v > 0 else 0 for v in w]
+
+    for n in range(N):
+        k, rejected = 0, False
+        while k < T1 - 1 and 0 <= int(draft[n][k]) < V:
+            d = int(draft[n][k])
+            a, b = float(q[n, k, d]), float(p[n, k, d])
+            u = float(u_accept[n][k])
+            good = np.isfinite(a) and np.isfinite(b)
+            if not (Fraction(u) * Fraction(a) < Fraction(b) if good else u * a < b):
+                rejected = True
+                break
+            k += 1
+        w = p[n, k].astype(np.float32)
+        with np.errstate(invalid="ignore"):
+            rest = whole(w - q[n, k].astype(np.float32)) if rejected else whole(w)
+        if sum(rest) == 0:
+            rest = whole(w)
+        limit = sum(rest) * int(float(u_sample[n]) * 2 ** 24) >> 24
+        run, new = 0, 0
+        for v, r in enumerate(rest):
+            run += r
+            if run > limit:
+                new = v
+                break
+        tokens[n, :k] = draft[n][:k]
+        tokens[n, k] = new
+        count[n] = k + 1
+    return tokens, count
