@@ -34,4 +34,25 @@ __device__ __forceinline__ float softplus(float v) {
   return fmaf(2.f * r, p, fmaxf(v, 0.f));
 }
 
+// The same of two values at once (packed products: half the instructions).
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 silu2(float2 x) {
+  const float2 u = __fmul2_rn(both(-kLog2e), x);
+  const float2 q = __fadd2_rn(both(1.f), make_float2(ex2(u.x), ex2(u.y)));
+  return make_float2(__fdividef(x.x, q.x), __fdividef(x.y, q.y));
+}
+__device__ __forceinline__ float2 softplus2(float2 v) {
+  const float2 e = make_float2(ex2(-kLog2e * fabsf(v.x)), ex2(-kLog2e * fabsf(v.y)));
+  const float2 q = __fadd2_rn(both(2.f), e);
+  const float2 r = make_float2(__fdividef(e.x, q.x), __fdividef(e.y, q.y));
+  const float2 r2 = __fmul2_rn(r, r);
+  float2 p = __ffma2_rn(r2, both(1.f / 13), both(1.f / 11));
+  p = __ffma2_rn(r2, p, both(1.f / 9));
+  p = __ffma2_rn(r2, p, both(1.f / 7));
+  p = __ffma2_rn(r2, p, both(1.f / 5));
+  p = __ffma2_rn(r2, p, both(1.f / 3));
+  p = __ffma2_rn(r2, p, both(1.f));
+  return __ffma2_rn(__fadd2_rn(r, r), p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+
 }  // namespace kda
