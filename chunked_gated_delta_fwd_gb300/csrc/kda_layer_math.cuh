@@ -14,9 +14,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 1 / x to about 2^-23 of itself, 0 for an infinite x (a division that minds results and divisors
+// below 2^-126, which do not occur here, takes several times the instructions).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // x Sigmoid(x) = x / (1 + e^-x)
 __device__ __forceinline__ float silu(float x) {
-  return __fdividef(x, 1.f + ex2(-kLog2e * x));
+  return x * rcp(1.f + ex2(-kLog2e * x));
 }
 
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v|, small results to their own last bits:
@@ -24,7 +32,7 @@ __device__ __forceinline__ float silu(float x) {
 // whose rest is below 2^-26 of it.  (log of the rounded 1 + e keeps three digits at v = -9.)
 __device__ __forceinline__ float softplus(float v) {
   const float e = ex2(-kLog2e * fabsf(v));
-  const float r = __fdividef(e, 2.f + e), r2 = r * r;
+  const float r = e * rcp(2.f + e), r2 = r * r;
   float p = fmaf(r2, 1.f / 13, 1.f / 11);
   p = fmaf(r2, p, 1.f / 9);
   p = fmaf(r2, p, 1.f / 7);
@@ -39,12 +47,12 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 silu2(float2 x) {
   const float2 u = __fmul2_rn(both(-kLog2e), x);
   const float2 q = __fadd2_rn(both(1.f), make_float2(ex2(u.x), ex2(u.y)));
-  return make_float2(__fdividef(x.x, q.x), __fdividef(x.y, q.y));
+  return __fmul2_rn(x, make_float2(rcp(q.x), rcp(q.y)));
 }
 __device__ __forceinline__ float2 softplus2(float2 v) {
   const float2 e = make_float2(ex2(-kLog2e * fabsf(v.x)), ex2(-kLog2e * fabsf(v.y)));
   const float2 q = __fadd2_rn(both(2.f), e);
-  const float2 r = make_float2(__fdividef(e.x, q.x), __fdividef(e.y, q.y));
+  const float2 r = __fmul2_rn(e, make_float2(rcp(q.x), rcp(q.y)));
   const float2 r2 = __fmul2_rn(r, r);
   float2 p = __ffma2_rn(r2, both(1.f / 13), both(1.f / 11));
   p = __ffma2_rn(r2, p, both(1.f / 9));

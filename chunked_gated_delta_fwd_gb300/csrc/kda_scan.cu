@@ -19,14 +19,9 @@
 namespace kda {
 namespace {
 
-constexpr int kScanWarps = 4;
+constexpr int kScanWarps = 12;
 constexpr int kTok = 8;  // tokens of a tile
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* src, bool valid) {
-  const int bytes = valid ? 16 : 0;  // (0: zeros are written)
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -38,22 +33,113 @@ __device__ __forceinline__ void hand(int id) {
   asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
 }
 
+// Shared memory of a warp.  Rows of a tile are looked after by four lanes each (kVec channels a
+// lane); states belong to lanes by channel and eighth, lane = channel + kCh * eighth.
 template <typename T, int kS>
-struct ScanWarp {  // shared memory of a warp
-  static constexpr int kLn = kS / 8, kCh = 32 / kLn;
-  static constexpr int kPitch = kCh * (int)sizeof(T) + 16;  // (rows of lanes that read together
-                                                            // lie in different banks)
-  __align__(16) char raw[3][kTok][kPitch];  // x, dt, z as they lie in memory
-  __align__(16) char bc[2][kTok][kS * sizeof(T)];
-  __align__(16) float2 step[kTok][kCh];     // delta, delta x
-  __align__(16) float BC[2][kTok][kS];
+struct ScanWarp {
+  static constexpr int kLn = kS / 8, kCh = 32 / kLn, kVec = kCh / 4;
+  static constexpr int kX = kVec * (int)sizeof(T) / 4, kB = kS * (int)sizeof(T) / 8;  // words a lane
+  __align__(16) uint32_t x[32][kX], dt[32][kX], z[32][kX], bc[32][kB];  // a tile as it comes
+  __align__(16) float delta[2][kTok][kCh];  // of this tile and the next
+  __align__(16) float dx[2][kTok][kCh];     // delta x
+  __align__(16) float BC[2][2][kTok][kS];
+  __align__(16) float part[kLn][(kTok + 1) * kCh];  // sums over a lane's states (a row to spare:
+                                                    // other banks for every eighth)
   __align__(16) float4 state[2][32];        // what the warp hands on
 };
 
+// kN consecutive elements of T as they lie in memory.
+template <typename T, int kN>
+struct Raw {
+  static constexpr int kWords = kN * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  // By way of the lane's own piece of shared memory: nothing of a tile in flight sits in registers
+  // (whose few scoreboards the code in between needs).
+  static __device__ __forceinline__ void copy(uint32_t* to, const char* p, bool valid) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (kWords < 4) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(p),
+                   "n"(4 * kWords), "r"(valid ? 4 * kWords : 0)
+                   : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + 4 * i),
+                     "l"(p + 4 * i), "r"(valid ? 16 : 0)
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ void take(const uint32_t* from) {
+    if constexpr (kWords == 1) {
+      w[0] = *from;
+    } else if constexpr (kWords == 2) {
+      const uint2 u = *reinterpret_cast<const uint2*>(from);
+      w[0] = u.x; w[1] = u.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(from + i);
+        w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ float2 pair(int i) const {  // elements 2 i and 2 i + 1
+    if constexpr (sizeof(T) == 2)
+      return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else
+      return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  __device__ __forceinline__ void set_pair(int i, float2 v) {
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      w[2 * i] = __float_as_uint(v.x);
+      w[2 * i + 1] = __float_as_uint(v.y);
+    }
+  }
+  __device__ __forceinline__ void store(char* p) const {
+    if constexpr (kWords == 1) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else if constexpr (kWords == 2) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+  }
+};
+// kN floats (2, 4 or 8) in shared memory.
+template <int kN>
+__device__ __forceinline__ void put(float* p, const float2* v) {
+  if constexpr (kN == 2) {
+    *reinterpret_cast<float2*>(p) = v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] =
+          make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+  }
+}
+template <int kN>
+__device__ __forceinline__ void get(const float* p, float2* v) {
+  if constexpr (kN == 2) {
+    v[0] = *reinterpret_cast<const float2*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i) {
+      const float4 u = reinterpret_cast<const float4*>(p)[i];
+      v[2 * i] = make_float2(u.x, u.y);
+      v[2 * i + 1] = make_float2(u.z, u.w);
+    }
+  }
+}
+
 template <typename T, int kS>
-__global__ void __launch_bounds__(32 * kScanWarps, 16 / kScanWarps) scan_kernel(const ScanArgs a, int* err) {
+__global__ void __launch_bounds__(32 * kScanWarps, 1) scan_kernel(const ScanArgs a, int* err) {
   using W = ScanWarp<T, kS>;
-  constexpr int kLn = W::kLn, kCh = W::kCh, kMine = kTok / kLn;
+  constexpr int kLn = W::kLn, kCh = W::kCh, kVec = W::kVec, kBc = kS / 2;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   W& w = reinterpret_cast<W*>(smem)[warp];
@@ -72,7 +158,6 @@ __global__ void __launch_bounds__(32 * kScanWarps, 16 / kScanWarps) scan_kernel(
   const int width = min(kCh, per_group - first);  // channels there are (a multiple of 8)
   const bool on = cl < width;
   const int c0 = g * per_group + first, c = c0 + (on ? cl : 0);
-  const float bias = a.bias ? __ldg(a.bias + c) : 0.f, skip = a.D ? __ldg(a.D + c) : 0.f;
   float2 A[4];
   {
     float v[8];
@@ -81,46 +166,6 @@ __global__ void __launch_bounds__(32 * kScanWarps, 16 / kScanWarps) scan_kernel(
     for (int i = 0; i < 4; ++i) A[i] = make_float2(kLog2e * v[2 * i], kLog2e * v[2 * i + 1]);
   }
   const int64_t at = ((int64_t)n * a.C + c) * kS + 8 * sub;
-
-  // Copies of a tile: rows of x, dt and z by 16-byte pieces, then those of B and C.  A lane copies
-  // the same pieces of every tile of its warp.
-  constexpr int kRow = kCh * (int)sizeof(T) / 16, kBc = kS * (int)sizeof(T) / 16;
-  constexpr int kX = kTok * kRow, kB = kTok * kBc;
-  constexpr uint32_t kNone = ~0u;
-  constexpr int kXs = (3 * kX + 31) / 32, kBs = (2 * kB + 31) / 32;
-  const char* src[kXs + kBs];
-  int64_t step[kXs + kBs];
-  uint32_t to[kXs + kBs];  // (kNone: no piece)
-  int row[kXs + kBs];      // (kTok: a piece behind the last channel)
-#pragma unroll
-  for (int k = 0; k < kXs + kBs; ++k) {
-    const bool isx = k < kXs;
-    const int p = 32 * (isx ? k : k - kXs) + lane;
-    const int of = isx ? kX : kB, per = isx ? kRow : kBc;
-    const int which = p / of, col = p % per;
-    row[k] = p % of / per;
-    const void* base = isx ? (which == 0 ? a.x : which == 1 ? a.dt : a.z) : which == 0 ? a.B : a.Cm;
-    const int64_t stride = isx ? (which == 0 ? a.sx : which == 1 ? a.sdt : a.sz)
-                               : which == 0 ? a.sB : a.sC;
-    to[k] = p >= (isx ? 3 : 2) * of || !base ? kNone
-            : (uint32_t)__cvta_generic_to_shared(isx ? &w.raw[which % 3][row[k]][16 * col]
-                                                     : &w.bc[which % 2][row[k]][16 * col]);
-    if (to[k] == kNone) base = a.x;
-    const bool in = !isx || col * 16 / (int)sizeof(T) < width;
-    src[k] = static_cast<const char*>(base) +
-             ((t0 + (int64_t)warp * kTok + row[k]) * stride + (isx ? c0 : g * kS)) * (int)sizeof(T) +
-             (in ? 16 * col : 0);
-    step[k] = stride * kTok * kScanWarps * (int)sizeof(T);
-    if (!in) row[k] = kTok;
-  }
-  // `left`: tokens of the sequence from the tile's first on
-  auto fetch = [&](int left) {
-#pragma unroll
-    for (int k = 0; k < kXs + kBs; ++k) {
-      if (to[k] != kNone) copy16(to[k], row[k] < left ? src[k] : static_cast<const char*>(a.x), row[k] < left && row[k] < kTok);
-      src[k] += step[k];
-    }
-  };
 
   const int len = (int)(t1 - t0), tiles = (len + kTok - 1) / kTok;
   if (tiles == 0) {
@@ -132,52 +177,103 @@ __global__ void __launch_bounds__(32 * kScanWarps, 16 / kScanWarps) scan_kernel(
     }
     return;
   }
-  if (warp < tiles) fetch(len - warp * kTok);
-  T* y = static_cast<T*>(a.y) + (t0 + warp * kTok + kMine * sub) * a.sy + c;
-  for (int tile = warp; tile < tiles; tile += kScanWarps, y += kScanWarps * kTok * a.sy) {
-    const int left = len - tile * kTok - kMine * sub;  // tokens from the lane's own ones on
-    wait_copies();
-    __syncwarp();
-    // steps, each by one lane; B and C to fp32
-    float2 x[kMine / 2], z[kMine / 2];
+  if (warp >= tiles) return;
+  // The lane's part of a tile's rows: kVec channels of token `row`, and kS / 2 values of B or C.
+  const int row = lane / 4, ch = kVec * (lane % 4);
+  const bool has = ch < width;
+  const int mine = c0 + (has ? ch : 0);
+  const int64_t first_row = t0 + warp * kTok + row;
+  const char* xp = static_cast<const char*>(a.x) + (first_row * a.sx + mine) * (int)sizeof(T);
+  const char* dp = static_cast<const char*>(a.dt) + (first_row * a.sdt + mine) * (int)sizeof(T);
+  const char* zp = a.z ? static_cast<const char*>(a.z) + (first_row * a.sz + mine) * (int)sizeof(T) : nullptr;
+  char* yp = static_cast<char*>(a.y) + (first_row * a.sy + mine) * (int)sizeof(T);
+  const int brow = (lane & 15) / 2, bcol = kBc * (lane & 1);
+  const int64_t sb = lane < 16 ? a.sB : a.sC;
+  const char* bp = static_cast<const char*>(lane < 16 ? a.B : a.Cm) +
+                   ((t0 + warp * kTok + brow) * sb + g * kS + bcol) * (int)sizeof(T);
+  constexpr int64_t kHop = (int64_t)kScanWarps * kTok * sizeof(T);
+  float2 bias[kVec / 2], skip[kVec / 2];
 #pragma unroll
-    for (int j = 0; j < kMine / 2; ++j) {
-      const int t = kMine * sub + 2 * j;
-      auto two = [&](int which) {
-        return make_float2(to_f32(reinterpret_cast<const T*>(w.raw[which][t])[cl]),
-                           to_f32(reinterpret_cast<const T*>(w.raw[which][t + 1])[cl]));
-      };
-      x[j] = two(0);
-      if (a.z) z[j] = two(2);
-      float2 d = __fadd2_rn(two(1), both(bias));
-      if (a.softplus) d = softplus2(d);
-      if (2 * j >= left) d.x = 0.f;  // behind the end: the state stays
-      if (2 * j + 1 >= left) d.y = 0.f;
-      const float2 dx = __fmul2_rn(d, x[j]);
-      w.step[t][cl] = make_float2(d.x, dx.x);
-      w.step[t + 1][cl] = make_float2(d.y, dx.y);
-    }
+  for (int j = 0; j < kVec / 2; ++j) {
+    bias[j] = a.bias ? *reinterpret_cast<const float2*>(a.bias + mine + 2 * j) : both(0.f);
+    skip[j] = a.D ? *reinterpret_cast<const float2*>(a.D + mine + 2 * j) : both(0.f);
+  }
+  const char* safe = static_cast<const char*>(a.x);  // (nothing is read from it)
+  Raw<T, kVec> x, z;  // of the tile at hand
+  Raw<T, kBc> rb;
+  auto fetch = [&](int left) {  // `left`: tokens of the sequence from the tile's first on
+    const bool ok = has && row < left;
+    Raw<T, kVec>::copy(w.x[lane], ok ? xp : safe, ok);
+    Raw<T, kVec>::copy(w.dt[lane], ok ? dp : safe, ok);
+    if (zp) Raw<T, kVec>::copy(w.z[lane], ok ? zp : safe, ok);
+    Raw<T, kBc>::copy(w.bc[lane], brow < left ? bp : safe, brow < left);
+    xp += kHop * a.sx;
+    dp += kHop * a.sdt;
+    zp += zp ? kHop * a.sz : 0;
+    bp += kHop * sb;
+  };
+  // Steps of the fetched tile, and its B and C as fp32: in registers, then in shared memory.
+  float2 fd[kVec / 2], fx[kVec / 2];
+  auto front = [&](int left) {
+    Raw<T, kVec> rd;
+    x.take(w.x[lane]);
+    z.take(w.z[lane]);  // (whatever lies there, without a gate)
+    rd.take(w.dt[lane]);
+    rb.take(w.bc[lane]);
 #pragma unroll
-    for (int k = 0; k < (2 * kTok * kS / 8 + 31) / 32; ++k) {
-      const int p = 8 * (32 * k + lane);
-      if (p < 2 * kTok * kS) {
-        float v[8];
-        load8(reinterpret_cast<const T*>(w.bc) + p, v);
-        store8(&w.BC[0][0][0] + p, v);
-      }
+    for (int j = 0; j < kVec / 2; ++j) {
+      fd[j] = __fadd2_rn(rd.pair(j), bias[j]);
+      const float2 sp = softplus2(fd[j]);
+      if (a.softplus) fd[j] = sp;
+      if (row >= left) fd[j] = both(0.f);  // behind the end: the state stays
+      fx[j] = __fmul2_rn(fd[j], x.pair(j));
     }
-    __syncwarp();
-    if (tile + kScanWarps < tiles) fetch(len - (tile + kScanWarps) * kTok);
+  };
+  auto lay = [&](int buf) {
+    put<kVec>(&w.delta[buf][row][ch], fd);
+    put<kVec>(&w.dx[buf][row][ch], fx);
+    float2 v[kBc / 2];
+#pragma unroll
+    for (int j = 0; j < kBc / 2; ++j) v[j] = rb.pair(j);
+    put<kBc>(&w.BC[buf][lane / 16][brow][bcol], v);
+  };
+  fetch(len - warp * kTok);
+  wait_copies();
+  front(len - warp * kTok);
+  lay(0);
+  __syncwarp();
+  if (warp + kScanWarps < tiles) fetch(len - (warp + kScanWarps) * kTok);
+  int buf = 0;
+  for (int tile = warp; tile < tiles; tile += kScanWarps) {
+    const int left = len - tile * kTok;  // tokens from the tile's first on
 
-    float2 e[kTok][4];  // the decays, then the states
+    // what the tile's tokens do to a state that comes in: h -> all h + own, y = acc + share . h
+    float2 own[4], all[4], share[kTok][4], acc[kTok];
+    float time = 0.f;
 #pragma unroll
     for (int t = 0; t < kTok; ++t) {
-      const float d = w.step[t][cl].x;
+      const float d = w.delta[buf][t][cl], dx = w.dx[buf][t][cl];
+      float2 bs[4], cs[4];
+      get<8>(&w.BC[buf][0][t][8 * sub], bs);
+      get<8>(&w.BC[buf][1][t][8 * sub], cs);
+      time += d;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 u = __fmul2_rn(A[i], make_float2(d, d));
-        e[t][i] = make_float2(ex2(u.x), ex2(u.y));
+        const float2 u = __fmul2_rn(A[i], both(d));
+        const float2 e = make_float2(ex2(u.x), ex2(u.y));
+        const float2 add = __fmul2_rn(both(dx), bs[i]);
+        own[i] = t == 0 ? add : __ffma2_rn(e, own[i], add);
+        all[i] = t == 0 ? e : __fmul2_rn(e, all[i]);
+        acc[t] = i == 0 ? __fmul2_rn(cs[i], own[i]) : __ffma2_rn(cs[i], own[i], acc[t]);
+        share[t][i] = __fmul2_rn(cs[i], all[i]);
       }
+    }
+    // (the state itself decays by one exponential a tile: their errors, of about 2^-26 and one
+    // sign, add up over as many tokens as a slow decay remembers)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = __fmul2_rn(A[i], both(time));
+      all[i] = make_float2(ex2(u.x), ex2(u.y));
     }
     float2 h[4];
     if (tile == 0) {
@@ -191,53 +287,51 @@ __global__ void __launch_bounds__(32 * kScanWarps, 16 / kScanWarps) scan_kernel(
       h[2] = make_float2(hi.x, hi.y); h[3] = make_float2(hi.z, hi.w);
     }
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      const float dx = w.step[t][cl].y;
-      const float4 lo = *reinterpret_cast<const float4*>(&w.BC[0][t][8 * sub]);
-      const float4 hi = *reinterpret_cast<const float4*>(&w.BC[0][t][8 * sub + 4]);
-      const float2 d2 = make_float2(dx, dx);
-      e[t][0] = h[0] = __ffma2_rn(e[t][0], h[0], __fmul2_rn(d2, make_float2(lo.x, lo.y)));
-      e[t][1] = h[1] = __ffma2_rn(e[t][1], h[1], __fmul2_rn(d2, make_float2(lo.z, lo.w)));
-      e[t][2] = h[2] = __ffma2_rn(e[t][2], h[2], __fmul2_rn(d2, make_float2(hi.x, hi.y)));
-      e[t][3] = h[3] = __ffma2_rn(e[t][3], h[3], __fmul2_rn(d2, make_float2(hi.z, hi.w)));
-    }
+    for (int i = 0; i < 4; ++i) own[i] = __ffma2_rn(all[i], h[i], own[i]);
     if (tile + 1 < tiles) {
-      w.state[0][lane] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-      w.state[1][lane] = make_float4(h[2].x, h[2].y, h[3].x, h[3].y);
+      w.state[0][lane] = make_float4(own[0].x, own[0].y, own[1].x, own[1].y);
+      w.state[1][lane] = make_float4(own[2].x, own[2].y, own[3].x, own[3].y);
       hand(1 + warp);
     } else if (a.hT && on) {
-      const float v[8] = {h[0].x, h[0].y, h[1].x, h[1].y, h[2].x, h[2].y, h[3].x, h[3].y};
+      const float v[8] = {own[0].x, own[0].y, own[1].x, own[1].y, own[2].x, own[2].y, own[3].x, own[3].y};
       store8(a.hT + at, v);
     }
-    float acc[kTok];
+    // this tile's outputs, and the next one's front between them (of zeros, behind the last)
+    float2 gate[kVec / 2], old[kVec / 2];
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      const float4 lo = *reinterpret_cast<const float4*>(&w.BC[1][t][8 * sub]);
-      const float4 hi = *reinterpret_cast<const float4*>(&w.BC[1][t][8 * sub + 4]);
-      float2 s = __fmul2_rn(e[t][0], make_float2(lo.x, lo.y));
-      s = __ffma2_rn(e[t][1], make_float2(lo.z, lo.w), s);
-      s = __ffma2_rn(e[t][2], make_float2(hi.x, hi.y), s);
-      s = __ffma2_rn(e[t][3], make_float2(hi.z, hi.w), s);
-      acc[t] = s.x + s.y;
+    for (int j = 0; j < kVec / 2; ++j) {
+      old[j] = __fmul2_rn(skip[j], x.pair(j));
+      gate[j] = silu2(z.pair(j));
+      if (!a.z) gate[j] = both(1.f);
     }
-    // halving exchange inside a channel's lanes: lane sub ends with tokens kMine sub ..
+    wait_copies();
+    front(left - kScanWarps * kTok);
 #pragma unroll
-    for (int m = kLn / 2, keep = kTok / 2; m > 0; m /= 2, keep /= 2) {
-      const bool upper = (sub & m) != 0;
+    for (int t = 0; t < kTok; ++t)
 #pragma unroll
-      for (int j = 0; j < keep; ++j) {
-        const float other = __shfl_xor_sync(0xffffffffu, upper ? acc[j] : acc[j + keep], m * kCh);
-        acc[j] = (upper ? acc[j + keep] : acc[j]) + other;
-      }
+      for (int i = 0; i < 4; ++i) acc[t] = __ffma2_rn(share[t][i], h[i], acc[t]);
+    buf ^= 1;
+#pragma unroll
+    for (int t = 0; t < kTok; ++t) w.part[sub][t * kCh + cl] = acc[t].x + acc[t].y;
+    lay(buf);
+    __syncwarp();
+    if (tile + 2 * kScanWarps < tiles) fetch(len - (tile + 2 * kScanWarps) * kTok);
+    float2 v[kVec / 2];
+    get<kVec>(&w.part[0][row * kCh + ch], v);
+#pragma unroll
+    for (int m = 1; m < kLn; ++m) {
+      float2 u[kVec / 2];
+      get<kVec>(&w.part[m][row * kCh + ch], u);
+#pragma unroll
+      for (int j = 0; j < kVec / 2; ++j) v[j] = __fadd2_rn(v[j], u[j]);
     }
+    Raw<T, kVec> out;
 #pragma unroll
-    for (int j = 0; j < kMine / 2; ++j) {
-      float2 v = __ffma2_rn(both(skip), x[j], make_float2(acc[2 * j], acc[2 * j + 1]));
-      if (a.z) v = __fmul2_rn(v, silu2(z[j]));
-      if (on && 2 * j < left) y[2 * j * a.sy] = from_f32<T>(v.x);
-      if (on && 2 * j + 1 < left) y[(2 * j + 1) * a.sy] = from_f32<T>(v.y);
-    }
-    __syncwarp();  // step and BC may be written again
+    for (int j = 0; j < kVec / 2; ++j)
+      out.set_pair(j, __fmul2_rn(__fadd2_rn(v[j], old[j]), gate[j]));
+    if (has && row < left) out.store(yp);
+    yp += kHop * a.sy;
+    __syncwarp();  // the sums have been read
   }
 }
 
