@@ -4,7 +4,10 @@
 //     h <- exp(delta_t A) h + delta_t x_t B_t,   y_t = (C_t . h + D x_t) SiLU(z_t)
 //
 // Bound by HBM: 8 bytes a state and call.  A lane holds four states of a channel (16-byte
-// accesses, a warp's are contiguous); S / 4 lanes share a channel.
+// accesses, a warp's are contiguous) of S / 4 sequences at once, and S / 4 lanes share a channel:
+// each of them looks after one of the sequences (its step, its gate, its output, once a token
+// and channel), and the others get the step by a shuffle.  B and C of the sequences' tokens sit in
+// shared memory.
 #include "kda_internal.cuh"
 #include "kda_scan.cuh"
 
@@ -13,51 +16,99 @@ namespace {
 
 constexpr int kStepThreads = 128;
 
-template <typename T, int kS>
+template <typename T, int kS, bool kMulti>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
     const ScanArgs a, float* __restrict__ state, const int32_t* __restrict__ n_advance) {
-  constexpr int kLn = kS / 4;
-  const int64_t id = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
-  const int64_t ch = id / kLn;  // n * C + c
-  const int sub = (int)(id % kLn);
-  const bool on = ch < (int64_t)a.N * a.C;
-  const int64_t n = on ? ch / a.C : 0;
-  const int c = on ? (int)(ch - n * a.C) : 0;
-  const int Tn = (int)a.T;
-  int adv = Tn;
-  if (n_advance) {
-    adv = __ldg(n_advance + n);
-    adv = adv < 0 ? 0 : (adv > Tn ? Tn : adv);
+  constexpr int kLn = kS / 4, kSlots = kLn, kT = kMulti ? 16 : 1;
+  constexpr unsigned kAll = 0xffffffffu;
+  __shared__ __align__(16) float BC[2][kSlots][kT][kS];
+  const int Tn = kMulti ? (int)a.T : 1;
+  const int per_group = a.C / a.G;
+  const int blocks = (per_group * kLn + kStepThreads - 1) / kStepThreads;  // of a group
+  const int64_t bunch = blockIdx.x / ((int64_t)blocks * a.G);
+  const int block = (int)(blockIdx.x - bunch * blocks * a.G), g = block / blocks;
+  const int id = (block - g * blocks) * kStepThreads + threadIdx.x;
+  const bool on = id < per_group * kLn;
+  const int c = g * per_group + (on ? id / kLn : 0), sub = id % kLn;
+  const int64_t n0 = bunch * kSlots;
+  const int there = (int)min((int64_t)kSlots, a.N - n0);  // sequences
+  const bool mine = on && sub < there;
+  const int64_t n = n0 + (sub < there ? sub : 0);  // the sequence the lane looks after
+
+  float4* at = reinterpret_cast<float4*>(state) + (n0 * a.C + c) * kLn + sub;
+  const int64_t hop = (int64_t)a.C * kLn;
+  float h[kSlots][4];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (on && i < there) {
+      const float4 v = __ldcs(at + i * hop);
+      h[i][0] = v.x; h[i][1] = v.y; h[i][2] = v.z; h[i][3] = v.w;
+    } else {
+      h[i][0] = h[i][1] = h[i][2] = h[i][3] = 0.f;
+    }
+  int64_t row = n * Tn;
+  T rx, rd, rz;
+  auto fetch = [&](int64_t r) {
+    rx = static_cast<const T*>(a.x)[r * a.sx + c];
+    rd = static_cast<const T*>(a.dt)[r * a.sdt + c];
+    if (a.z) rz = static_cast<const T*>(a.z)[r * a.sz + c];
+  };
+  fetch(row);
+  for (int e = threadIdx.x; e < 2 * there * Tn * kLn; e += kStepThreads) {
+    const int q = e % kLn, which = e / kLn % 2, t = e / (2 * kLn) % Tn, i = e / (2 * kLn) / Tn;
+    const int64_t r = (n0 + i) * Tn + t;
+    const T* src = which ? static_cast<const T*>(a.Cm) + r * a.sC : static_cast<const T*>(a.B) + r * a.sB;
+    float v[4];
+    load4(src + g * kS + 4 * q, v);
+    store4(&BC[which][i][t][4 * q], v);
   }
-  const int g = c / (a.C / a.G);
-  float4* at = reinterpret_cast<float4*>(state) + (n * a.C + c) * kLn + sub;
-  float h[4], A[4];
-  load4(reinterpret_cast<const float*>(at), h);
+  float A[4];
   load4(a.A + (int64_t)c * kS + 4 * sub, A);
 #pragma unroll
   for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
   const float bias = a.bias ? __ldg(a.bias + c) : 0.f, skip = a.D ? __ldg(a.D + c) : 0.f;
+  int adv = Tn;
+  if (kMulti && n_advance) {
+    adv = __ldg(n_advance + n);
+    adv = adv < 0 ? 0 : (adv > Tn ? Tn : adv);
+  }
+  __syncthreads();
+#pragma unroll 1
   for (int t = 0; t < Tn; ++t) {
-    const int64_t row = n * Tn + t;
-    const float xv = to_f32(static_cast<const T*>(a.x)[row * a.sx + c]);
-    float d = to_f32(static_cast<const T*>(a.dt)[row * a.sdt + c]) + bias;
+    const float x = to_f32(rx), z = a.z ? to_f32(rz) : 0.f;
+    float d = to_f32(rd) + bias;
+    if (kMulti && t + 1 < Tn) fetch(row + t + 1);
     if (a.softplus) d = softplus(d);
-    float b[4], cc[4];
-    load4(static_cast<const T*>(a.B) + row * a.sB + g * kS + 4 * sub, b);
-    load4(static_cast<const T*>(a.Cm) + row * a.sC + g * kS + 4 * sub, cc);
-    float acc = 0.f;
+    const float dx = d * x;
+    float acc[kSlots];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = fmaf(ex2(d * A[i]), h[i], d * xv * b[i]);
-      acc = fmaf(cc[i], h[i], acc);
+    for (int i = 0; i < kSlots; ++i) {
+      const float di = __shfl_sync(kAll, d, i, kLn), dxi = __shfl_sync(kAll, dx, i, kLn);
+      const float4 b = *reinterpret_cast<const float4*>(&BC[0][i][t][4 * sub]);
+      const float4 k = *reinterpret_cast<const float4*>(&BC[1][i][t][4 * sub]);
+      h[i][0] = fmaf(ex2(di * A[0]), h[i][0], dxi * b.x);
+      h[i][1] = fmaf(ex2(di * A[1]), h[i][1], dxi * b.y);
+      h[i][2] = fmaf(ex2(di * A[2]), h[i][2], dxi * b.z);
+      h[i][3] = fmaf(ex2(di * A[3]), h[i][3], dxi * b.w);
+      acc[i] = fmaf(k.x, h[i][0], fmaf(k.y, h[i][1], fmaf(k.z, h[i][2], k.w * h[i][3])));
+      const bool keep = kMulti ? t + 1 == __shfl_sync(kAll, adv, i, kLn) : true;
+      if (on && i < there && keep)
+        __stcs(at + i * hop, make_float4(h[i][0], h[i][1], h[i][2], h[i][3]));
     }
-    if (on && t + 1 == adv) *at = make_float4(h[0], h[1], h[2], h[3]);
     if (!a.y) continue;
+    // halving exchange inside a channel's lanes: lane sub ends with sequence sub
 #pragma unroll
-    for (int m = 1; m < kLn; m *= 2) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-    acc = fmaf(skip, xv, acc);
-    if (a.z) acc *= silu(to_f32(static_cast<const T*>(a.z)[row * a.sz + c]));
-    if (on && sub == 0) static_cast<T*>(a.y)[row * a.sy + c] = from_f32<T>(acc);
+    for (int m = kLn / 2; m > 0; m /= 2) {
+      const bool upper = (sub & m) != 0;
+#pragma unroll
+      for (int j = 0; j < m; ++j) {
+        const float other = __shfl_xor_sync(kAll, upper ? acc[j] : acc[j + m], m);
+        acc[j] = (upper ? acc[j + m] : acc[j]) + other;
+      }
+    }
+    float y = fmaf(skip, x, acc[0]);
+    if (a.z) y *= silu(z);
+    if (mine) static_cast<T*>(a.y)[(row + t) * a.sy + c] = from_f32<T>(y);
   }
 }
 
@@ -65,15 +116,17 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
 
 cudaError_t launch_scan_step(const ScanArgs& a, int bf16, int S, float* state,
                              const int32_t* n_advance, bool multi, cudaStream_t s) {
-  const int64_t blocks = ((int64_t)a.N * a.C * (S / 4) + kStepThreads - 1) / kStepThreads;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int lanes = S / 4;
+  const int64_t blocks = (int64_t)a.G * (((int64_t)a.C / a.G * lanes + kStepThreads - 1) / kStepThreads);
+  const int64_t grid = blocks * (((int64_t)a.N + lanes - 1) / lanes);
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   ProfScope prof_scope(multi ? "kda_scan_multi_step" : "kda_scan_step", s);
   with_states(S, [&](auto k) {
     constexpr int kS = decltype(k)::value;
-    if (bf16)
-      scan_step_kernel<__nv_bfloat16, kS><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, state, n_advance);
-    else
-      scan_step_kernel<float, kS><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, state, n_advance);
+    using H = __nv_bfloat16;
+    const auto fn = multi ? (bf16 ? scan_step_kernel<H, kS, true> : scan_step_kernel<float, kS, true>)
+                          : (bf16 ? scan_step_kernel<H, kS, false> : scan_step_kernel<float, kS, false>);
+    fn<<<(unsigned)grid, kStepThreads, 0, s>>>(a, state, n_advance);
   });
   return cudaGetLastError();
 }
