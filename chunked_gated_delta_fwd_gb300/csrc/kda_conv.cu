@@ -3,9 +3,10 @@
 //     y_t[c] = act(bias[c] + sum_{j < W} w[c][j] x_{t-W+1+j}[c]),   W = 2 .. 4,
 // act the identity or SiLU; what lies before a sequence comes from its kept inputs (or is 0).
 //
-// Bound by HBM: x is read and y written once.  A lane holds 16 bytes of channels of a row and
+// Bound by HBM: x is read and y written once.  A lane holds four channels and
 // walks a run of tokens with the last W - 1 inputs in registers, so a run reads W - 1 rows more
-// than it has (from L2: its neighbour reads them as well).  Sums are fp32, rounded once.
+// than it has (from L2: its neighbour reads them as well).  Eight rows are on their way while eight
+// are worked on; products are packed pairs.  Sums are fp32, rounded once.
 #include <algorithm>
 #include <type_traits>
 
@@ -16,71 +17,67 @@ namespace kda {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kGroup = 4;  // rows of a lane in flight
+constexpr int kGroup = 8;      // rows of a lane in flight (prompts)
+constexpr int kStepGroup = 4;  // (new tokens)
 
-// 16 bytes of channels: their count, and as fp32.
-template <typename T> struct Vec { static constexpr int n = 16 / (int)sizeof(T); };
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Four channels of a row: as they lie in memory, and as pairs of fp32.
+template <typename T> struct Words;
+template <> struct Words<__nv_bfloat16> { using type = uint2; };
+template <> struct Words<float> { using type = uint4; };
+template <typename T> using Row = typename Words<T>::type;
+constexpr int kVec = 4, kPairs = 2;
+__device__ __forceinline__ void unpack(const uint2& u, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+  f[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
-  f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-  f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+__device__ __forceinline__ void unpack(const uint4& u, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void pack(const float2 (&f)[2], uint2& u) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0].x, f[0].y), b = __floats2bfloat162_rn(f[1].x, f[1].y);
+  u = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                    __float_as_uint(f[3]));
+__device__ __forceinline__ void pack(const float2 (&f)[2], uint4& u) {
+  u = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                 __float_as_uint(f[1].y));
 }
 
-// The taps of a lane's channels, and one output row from the window's rows old .. new.
+// The taps of a lane's channels, and one output row from a window of rows, the oldest first.
 template <typename T, int kW>
 struct Taps {
-  static constexpr int n = Vec<T>::n;
-  float w[n][kW], b[n];
-  __device__ __forceinline__ void load(const float* weight, const float* bias, int c) {
-    float raw[n * kW];
+  float2 w[kW][kPairs], b[kPairs];
+  __device__ __forceinline__ void load(const float* weight, const float* bias, int cv) {
+    float raw[kVec * kW];
 #pragma unroll
-    for (int i = 0; i < n * kW / 4; ++i) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(weight + (int64_t)c * kW) + i);
+    for (int i = 0; i < kW; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(weight) + (int64_t)cv * kW + i);
       raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
     }
+    const float4 v = bias ? __ldg(reinterpret_cast<const float4*>(bias) + cv)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    b[0] = make_float2(v.x, v.y);
+    b[1] = make_float2(v.z, v.w);
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < kPairs; ++i)
 #pragma unroll
-      for (int j = 0; j < kW; ++j) w[i][j] = raw[i * kW + j];
-      b[i] = bias ? __ldg(bias + c + i) : 0.f;
-    }
+      for (int j = 0; j < kW; ++j) w[j][i] = make_float2(raw[2 * i * kW + j], raw[(2 * i + 1) * kW + j]);
   }
-  __device__ __forceinline__ uint4 row(const uint4* window, bool act) const {
-    float y[n];
+  __device__ __forceinline__ Row<T> row(const float2 (*window)[kPairs], bool act) const {
+    float2 y[kPairs];
 #pragma unroll
-    for (int i = 0; i < n; ++i) y[i] = b[i];
+    for (int i = 0; i < kPairs; ++i) {
+      y[i] = b[i];
 #pragma unroll
-    for (int j = 0; j < kW; ++j) {
-      float f[n];
-      unpack(window[j], f);
-#pragma unroll
-      for (int i = 0; i < n; ++i) y[i] = fmaf(w[i][j], f[i], y[i]);
+      for (int j = 0; j < kW; ++j) y[i] = __ffma2_rn(w[j][i], window[j][i], y[i]);
     }
     if (act) {
 #pragma unroll
-      for (int i = 0; i < n; ++i) y[i] = silu(y[i]);
+      for (int i = 0; i < kPairs; ++i) y[i] = silu2(y[i]);
     }
-    return pack(y);
+    Row<T> u;
+    pack(y, u);
+    return u;
   }
 };
 
@@ -136,129 +133,165 @@ __device__ __forceinline__ int64_t run_begin(const ConvArgs& a, int64_t t, Span&
 template <typename T>
 __device__ void conv_ends(const ConvArgs& a, int K, int* err) {
   bool bad = false;
-  const int lanes = a.C / Vec<T>::n;
+  const int lanes = a.C / kVec;
   for (int n = blockIdx.x; n < a.N; n += a.ends) {
     const int64_t b = a.cu ? __ldg(a.cu + n) : 0, e = a.cu ? __ldg(a.cu + n + 1) : 0;
     bad |= b < 0 || e < b || e > a.NT || (n == 0 && b != 0) || (n == a.N - 1 && e != a.NT);
     if (!a.last || b != e) continue;
     const int64_t at = (int64_t)n * K * lanes;
     for (int i = threadIdx.x; i < K * lanes; i += blockDim.x)
-      reinterpret_cast<uint4*>(a.last)[at + i] =
-          a.state ? reinterpret_cast<const uint4*>(a.state)[at + i] : make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<Row<T>*>(a.last)[at + i] =
+          a.state ? reinterpret_cast<const Row<T>*>(a.state)[at + i] : Row<T>{};
   }
   if (bad && threadIdx.x == 0 && err) atomicExch(err, kDevErrBadSeqlens);
 }
 
 template <typename T, int kW>
 __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, int* err) {
-  constexpr int kV = Vec<T>::n, K = kW - 1;
+  constexpr int K = kW - 1;
+  constexpr int kPiece = (int)sizeof(Row<T>);
   if ((int)blockIdx.x < a.ends) {
     conv_ends<T>(a, K, err);
     return;
   }
-  const int lanes = a.C / kV;
+  const int lanes = a.C / kVec;
   const int64_t id = (int64_t)(blockIdx.x - a.ends) * kConvThreads + threadIdx.x;
   const int64_t tile = id / lanes;
-  if (tile >= a.runs) return;
   const int cv = (int)(id - tile * lanes);
+  if (tile >= a.runs) return;
   Span sp, after;
   int64_t t = run_begin<kW>(a, tile * a.run, sp);
   const int64_t stop = run_begin<kW>(a, min((tile + 1) * a.run, a.NT), after);
   if (t >= stop) return;
   Taps<T, kW> taps;
-  taps.load(a.w, a.b, cv * kV);
-  const char* x = a.x + 16 * (int64_t)cv;
-  char* y = a.y + 16 * (int64_t)cv;
+  taps.load(a.w, a.b, cv);
+  const char* x = a.x + kPiece * (int64_t)cv;
+  char* y = a.y + kPiece * (int64_t)cv;
   const int64_t kept = (int64_t)a.C * sizeof(T);  // bytes of a kept row
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 win[K + kGroup];
+  const Row<T> zero{};
+  float2 win[K + kGroup][kPairs];
+  Row<T> ahead[kGroup];
+  auto fetch = [&](int64_t from, int64_t end) {
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      if (from + i < end) ahead[i] = *reinterpret_cast<const Row<T>*>(x + (from + i) * a.sx);
+  };
   while (t < stop) {  // sequence by sequence
     const int64_t end = min(sp.end, stop);
+    fetch(t, end);
+    Row<T> old[K];
     if (t == sp.begin) {
-      const int64_t at = (int64_t)sp.n * K * kept + 16 * (int64_t)cv;
+      const int64_t at = (int64_t)sp.n * K * kept + kPiece * (int64_t)cv;
 #pragma unroll
       for (int r = 0; r < K; ++r)
-        win[r] = a.state ? *reinterpret_cast<const uint4*>(a.state + at + r * kept) : zero;
+        old[r] = a.state ? *reinterpret_cast<const Row<T>*>(a.state + at + r * kept) : zero;
       if (a.last) {
         const int64_t len = sp.end - sp.begin;
-        uint4 out[K];
+        Row<T> out[K];
 #pragma unroll
         for (int r = 0; r < K; ++r) {
           if (len + r >= K) {
-            out[r] = *reinterpret_cast<const uint4*>(x + (sp.end - K + r) * a.sx);
+            out[r] = *reinterpret_cast<const Row<T>*>(x + (sp.end - K + r) * a.sx);
           } else {
             out[r] = zero;
 #pragma unroll
             for (int m = 0; m < K; ++m)
-              if (m == len + r) out[r] = win[m];
+              if (m == len + r) out[r] = old[m];
           }
         }
 #pragma unroll
-        for (int r = 0; r < K; ++r) *reinterpret_cast<uint4*>(a.last + at + r * kept) = out[r];
+        for (int r = 0; r < K; ++r) *reinterpret_cast<Row<T>*>(a.last + at + r * kept) = out[r];
       }
     } else {
 #pragma unroll
       for (int r = 0; r < K; ++r)  // (all of them, where the offsets are sound)
-        win[r] = t - K + r >= sp.begin ? *reinterpret_cast<const uint4*>(x + (t - K + r) * a.sx) : zero;
+        old[r] = t - K + r >= sp.begin ? *reinterpret_cast<const Row<T>*>(x + (t - K + r) * a.sx) : zero;
     }
-    while (t < end) {
-      const int64_t left = end - t;
-      const int m = left < kGroup ? (int)left : kGroup;
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i)
-        if (i < m) win[K + i] = *reinterpret_cast<const uint4*>(x + (t + i) * a.sx);
+    for (int r = 0; r < K; ++r) unpack(old[r], win[r]);
+    for (;;) {
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i)
-        if (i < m) *reinterpret_cast<uint4*>(y + (t + i) * a.sy) = taps.row(win + i, a.act);
-      t += m;
-      if (t < end) {  // a whole group
+      for (int i = 0; i < kGroup; ++i) unpack(ahead[i], win[K + i]);
+      fetch(t + kGroup, end);
+      if (end - t >= kGroup) {
 #pragma unroll
-        for (int r = 0; r < K; ++r) win[r] = win[kGroup + r];
+        for (int i = 0; i < kGroup; ++i)
+          *reinterpret_cast<Row<T>*>(y + (t + i) * a.sy) = taps.row(win + i, a.act);
+        t += kGroup;
+        if (t == end) break;
+#pragma unroll
+        for (int r = 0; r < K; ++r)
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) win[r][j] = win[kGroup + r][j];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kGroup - 1; ++i)
+          if (t + i < end) *reinterpret_cast<Row<T>*>(y + (t + i) * a.sy) = taps.row(win + i, a.act);
+        t = end;
+        break;
       }
     }
     if (t < stop) sp = span_of(a, t);
   }
 }
 
-// T new tokens of N sequences; the kept inputs end as they are behind the first n_advance.
-template <typename T, int kW>
+// T new tokens of N sequences (kOne: one); the kept inputs end as they are behind the first
+// n_advance.  Several sequences a lane, to read the taps once, are slower (512 sequences x 12288
+// channels: 39 us with two or four).
+template <typename T, int kW, bool kOne>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(
-    const ConvArgs a, char* __restrict__ state, const int32_t* __restrict__ n_advance, int Tn) {
-  constexpr int kV = Vec<T>::n, K = kW - 1;
-  const int lanes = a.C / kV;
+    const ConvArgs a, char* __restrict__ state, const int32_t* __restrict__ n_advance, int T_) {
+  constexpr int K = kW - 1, kG = kOne ? 1 : kStepGroup;
+  constexpr int kPiece = (int)sizeof(Row<T>);
+  const int lanes = a.C / kVec, Tn = kOne ? 1 : T_;
   const int64_t id = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
   const int64_t n = id / lanes;
   if (n >= a.N) return;
   const int cv = (int)(id - n * lanes);
+  const int64_t kept = (int64_t)a.C * sizeof(T);
+  char* st = state + n * K * kept + kPiece * (int64_t)cv;
+  const char* x = a.x + n * Tn * a.sx + kPiece * (int64_t)cv;
+  char* y = a.y ? a.y + n * Tn * a.sy + kPiece * (int64_t)cv : nullptr;
+  Row<T> win[K + kG];
+#pragma unroll
+  for (int r = 0; r < K; ++r) win[r] = *reinterpret_cast<const Row<T>*>(st + r * kept);
+#pragma unroll
+  for (int i = 0; i < kG; ++i)
+    if (i < Tn) win[K + i] = *reinterpret_cast<const Row<T>*>(x + i * a.sx);
   int adv = Tn;
-  if (n_advance) {
+  if (!kOne && n_advance) {
     adv = __ldg(n_advance + n);
     adv = adv < 0 ? 0 : (adv > Tn ? Tn : adv);
   }
-  const char* x = a.x + n * Tn * a.sx + 16 * (int64_t)cv;
-  char* y = a.y ? a.y + n * Tn * a.sy + 16 * (int64_t)cv : nullptr;
-  const int64_t kept = (int64_t)a.C * sizeof(T), at = n * K * kept + 16 * (int64_t)cv;
-  uint4 win[K + kGroup];
-#pragma unroll
-  for (int r = 0; r < K; ++r) win[r] = *reinterpret_cast<const uint4*>(state + at + r * kept);
   Taps<T, kW> taps;
-  if (y) taps.load(a.w, a.b, cv * kV);
-  for (int t = 0; t < Tn; t += kGroup) {
+  if (y) taps.load(a.w, a.b, cv);
+  for (int t = 0; t < Tn; t += kG) {
+    Row<T> ahead[kG];
+    if (!kOne) {
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i)
-      if (t + i < Tn) win[K + i] = *reinterpret_cast<const uint4*>(x + (t + i) * a.sx);
+      for (int i = 0; i < kG; ++i)
+        if (t + kG + i < Tn) ahead[i] = *reinterpret_cast<const Row<T>*>(x + (t + kG + i) * a.sx);
+    }
+    float2 f[K + kG][kPairs];
+    if (y) {
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) {
-      if (t + i >= Tn) continue;
-      if (y) *reinterpret_cast<uint4*>(y + (t + i) * a.sy) = taps.row(win + i, a.act);
-      if (t + i + 1 == adv) {
-#pragma unroll
-        for (int r = 0; r < K; ++r)
-          *reinterpret_cast<uint4*>(state + at + r * kept) = win[i + 1 + r];
-      }
+      for (int i = 0; i < K + kG; ++i) unpack(win[i], f[i]);
     }
 #pragma unroll
-    for (int r = 0; r < K; ++r) win[r] = win[kGroup + r];
+    for (int i = 0; i < kG; ++i) {
+      if (t + i >= Tn) continue;
+      if (y) *reinterpret_cast<Row<T>*>(y + (t + i) * a.sy) = taps.row(f + i, a.act);
+      if (t + i + 1 == adv) {
+#pragma unroll
+        for (int r = 0; r < K; ++r) *reinterpret_cast<Row<T>*>(st + r * kept) = win[i + 1 + r];
+      }
+    }
+    if (!kOne) {
+#pragma unroll
+      for (int r = 0; r < K; ++r) win[r] = win[kG + r];
+#pragma unroll
+      for (int i = 0; i < kG; ++i) win[K + i] = ahead[i];
+    }
   }
 }
 
@@ -271,8 +304,12 @@ void with_width(int W, F f) {
 
 template <typename T>
 cudaError_t launch_conv_t(ConvArgs a, int W, int* err, cudaStream_t s) {
-  const int lanes = a.C / Vec<T>::n;
-  a.run = 16;
+  const int lanes = a.C / kVec;
+  // Runs as long as they leave some 500 lanes an SM, up to 64 tokens: a lane finds its sequence, its
+  // taps and its first rows once a run (8192 tokens x 12288 channels: 96, 83, 81 us in runs of 16, 32
+  // and 64).
+  a.run = 64;
+  while (a.run > kGroup && a.NT * lanes / a.run < 152 * 512) a.run /= 2;
   a.runs = (a.NT + a.run - 1) / a.run;
   const int64_t blocks = (a.runs * lanes + kConvThreads - 1) / kConvThreads;
   // (without offsets there is something to see to only if no sequence has tokens)
@@ -304,17 +341,17 @@ cudaError_t launch_conv_step(const void* x, int bf16, const float* w, const floa
   const int e = bf16 ? 2 : 4;
   ConvArgs a{static_cast<const char*>(x), static_cast<char*>(y), w, b, nullptr, nullptr, nullptr, T,
              (int64_t)N * T, sx * e, sy * e, 0, N, C, 0, act, 0};
-  const int64_t blocks = ((int64_t)N * (C * e / 16) + kConvThreads - 1) / kConvThreads;
+  const int64_t lanes = C / kVec;
+  const int64_t blocks = (N * lanes + kConvThreads - 1) / kConvThreads;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   ProfScope prof_scope("kda_conv_step", s);
+  const bool one = T == 1 && !n_advance && y;
   with_width(W, [&](auto w_) {
     constexpr int kW = decltype(w_)::value;
-    if (bf16)
-      conv_step_kernel<__nv_bfloat16, kW><<<(unsigned)blocks, kConvThreads, 0, s>>>(
-          a, static_cast<char*>(state), n_advance, T);
-    else
-      conv_step_kernel<float, kW><<<(unsigned)blocks, kConvThreads, 0, s>>>(
-          a, static_cast<char*>(state), n_advance, T);
+    using H = __nv_bfloat16;
+    const auto fn = one ? (bf16 ? conv_step_kernel<H, kW, true> : conv_step_kernel<float, kW, true>)
+                        : (bf16 ? conv_step_kernel<H, kW, false> : conv_step_kernel<float, kW, false>);
+    fn<<<(unsigned)blocks, kConvThreads, 0, s>>>(a, static_cast<char*>(state), n_advance, T);
   });
   return cudaGetLastError();
 }
