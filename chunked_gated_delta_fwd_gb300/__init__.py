@@ -698,26 +698,27 @@ def _row_stride(t: torch.Tensor, name: str, tail: tuple, dtype=None, device=None
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     shape, k = t.shape, len(tail)
-    if len(shape) <= k or shape[len(shape) - k:] != tail:
+    dims = len(shape)
+    if dims <= k or shape[dims - k:] != tail:
         raise ValueError(f"{name} must be [..., {', '.join(map(str, tail))}], got {tuple(shape)}")
     row = tail[0] if k == 1 else tail[0] * tail[1]
     if t.is_contiguous():
         return row
     stride = t.stride()
     inner = 1
-    for size, s in zip(reversed(shape[-k:]), reversed(stride[-k:])):
-        if size > 1 and s != inner:
+    for i in range(dims - 1, dims - 1 - k, -1):
+        if stride[i] != inner and shape[i] > 1:
             raise ValueError(f"{name}: the elements of a token must be contiguous")
-        inner *= size
+        inner *= shape[i]
     step = expect = None
-    for size, s in zip(reversed(shape[:-k]), reversed(stride[:-k])):
-        if size == 1:
+    for i in range(dims - 1 - k, -1, -1):
+        if shape[i] == 1:
             continue
         if step is None:
-            step = s
-        elif s != expect:
+            step = stride[i]
+        elif stride[i] != expect:
             raise ValueError(f"{name}: the tokens must be one stride apart")
-        expect = s * size
+        expect = stride[i] * shape[i]
     return row if step is None else step
 
 
@@ -752,7 +753,7 @@ def _conv_inputs(x, weight, bias):
 def _rows_out(out, x, C):
     """``out`` (or a new contiguous tensor) of x's shape, and its token stride."""
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device), C
+        return torch.empty_like(x, memory_format=torch.contiguous_format), C
     s = _row_stride(out, "out", (C,), x.dtype, x.device)
     if out.shape != x.shape:
         raise ValueError(f"out must be {tuple(x.shape)}, got {tuple(out.shape)}")
@@ -831,30 +832,31 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias):
     inputs."""
     if not isinstance(x, torch.Tensor) or x.dim() < 2:
         raise ValueError("x must be a tensor [..., channels]")
-    n, dev, dtype, lead = x.shape[-1], x.device, x.dtype, x.shape[:-1]
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    n, lead = shape[-1], shape[:-1]
     _need(A, "A", torch.float32, dev)
     if A.dim() != 2 or A.shape[0] != n:
         raise ValueError(f"A must be [{n}, states], got {tuple(A.shape)}")
     S = A.shape[1]
     G = B.shape[-2] if isinstance(B, torch.Tensor) and B.dim() > 2 else 1
-    sx = _row_stride(x, "x", (n,))
-    strides = [sx]
-    for name, t, tail in (("dt", dt, (n,)), ("B", B, (G, S)), ("C", C, (G, S))):
-        strides.append(_row_stride(t, name, tail, dtype, dev))
-        if t.shape[:len(t.shape) - len(tail)] != lead:
-            raise ValueError(f"{name} must be {tuple(lead) + tail}, got {tuple(t.shape)}")
-    sz = n
-    if z is not None:
-        sz = _row_stride(z, "z", (n,), dtype, dev)
-        if z.shape != x.shape:
-            raise ValueError(f"z must be {tuple(x.shape)}, got {tuple(z.shape)}")
-    strides.append(sz)
+    row, bc, whole = (n,), (G, S), lead + (n,)
+    sx = _row_stride(x, "x", row)
+    sdt = _row_stride(dt, "dt", row, dtype, dev)
+    sB = _row_stride(B, "B", bc, dtype, dev)
+    sC = _row_stride(C, "C", bc, dtype, dev)
+    sz = _row_stride(z, "z", row, dtype, dev) if z is not None else n
+    for name, t in (("dt", dt), ("z", z)):
+        if t is not None and t.shape != whole:
+            raise ValueError(f"{name} must be {tuple(whole)}, got {tuple(t.shape)}")
+    for name, t in (("B", B), ("C", C)):
+        if t.shape != lead + bc:
+            raise ValueError(f"{name} must be {tuple(lead + bc)}, got {tuple(t.shape)}")
     for name, t in (("D", D), ("dt_bias", dt_bias)):
         if t is not None:
             _need(t, name, torch.float32, dev)
-            if t.shape != (n,):
+            if t.shape != row:
                 raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-    return n, S, G, _dtype_code(x), strides
+    return n, S, G, _dtype_code(x), (sx, sdt, sB, sC, sz)
 
 
 def selective_scan_fwd(x, dt, A, B, C, h0=None, cu_seqlens=None, *, D=None, z=None, dt_bias=None,

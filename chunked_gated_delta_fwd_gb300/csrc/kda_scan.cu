@@ -10,7 +10,7 @@
 // a warp that gets the state runs its 8 tokens, hands it on, and forms its outputs behind that.
 // A lane holds 8 states of one channel (S / 8 lanes share a channel), the decays of the tile in
 // registers; B, C and the steps come from shared memory.
-#include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kda_internal.cuh"
@@ -335,6 +335,23 @@ __global__ void __launch_bounds__(32 * kScanWarps, 1) scan_kernel(const ScanArgs
   }
 }
 
+template <typename T, int kS>
+cudaError_t launch_scan_t(const ScanArgs& a, unsigned units, int* err, cudaStream_t s) {
+  constexpr size_t smem = kScanWarps * sizeof(ScanWarp<T, kS>);
+  static std::atomic<uint64_t> told{0};  // devices that know how much shared memory this takes
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(told.load() & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        scan_kernel<T, kS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    told |= bit;
+  }
+  scan_kernel<T, kS><<<units, 32 * kScanWarps, smem, s>>>(a, err);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_scan(const ScanArgs& a, int bf16, int S, int* err, cudaStream_t s) {
@@ -345,17 +362,10 @@ cudaError_t launch_scan(const ScanArgs& a, int bf16, int S, int* err, cudaStream
   cudaError_t e = cudaSuccess;
   with_states(S, [&](auto k) {
     constexpr int kS = decltype(k)::value;
-    auto launch = [&](auto kernel, size_t smem) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e == cudaSuccess)
-        kernel<<<(unsigned)units, 32 * kScanWarps, smem, s>>>(a, err);
-    };
-    if (bf16)
-      launch(scan_kernel<__nv_bfloat16, kS>, kScanWarps * sizeof(ScanWarp<__nv_bfloat16, kS>));
-    else
-      launch(scan_kernel<float, kS>, kScanWarps * sizeof(ScanWarp<float, kS>));
+    e = bf16 ? launch_scan_t<__nv_bfloat16, kS>(a, (unsigned)units, err, s)
+             : launch_scan_t<float, kS>(a, (unsigned)units, err, s);
   });
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return e;
 }
 
 }  // namespace kda
