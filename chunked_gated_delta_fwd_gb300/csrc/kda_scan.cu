@@ -10,6 +10,8 @@
 // a warp that gets the state runs its 8 tokens, hands it on, and forms its outputs behind that.
 // A lane holds 8 states of one channel (S / 8 lanes share a channel), the decays of the tile in
 // registers; B, C and the steps come from shared memory.
+#include <cooperative_groups.h>
+
 #include <atomic>
 #include <type_traits>
 
@@ -19,7 +21,6 @@
 namespace kda {
 namespace {
 
-constexpr int kScanWarps = 12;
 constexpr int kTok = 8;  // tokens of a tile
 
 __device__ __forceinline__ void wait_copies() {
@@ -31,6 +32,24 @@ __device__ __forceinline__ void handed(int id) {
 }
 __device__ __forceinline__ void hand(int id) {
   asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+}
+
+// A lane's eight states, kept by lanes.
+__device__ __forceinline__ void put_state(float4 (*s)[32], int lane, const float2 (&h)[4]) {
+  s[0][lane] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+  s[1][lane] = make_float4(h[2].x, h[2].y, h[3].x, h[3].y);
+}
+__device__ __forceinline__ void get_state(const float4 (*s)[32], int lane, float2 (&h)[4]) {
+  const float4 lo = s[0][lane], hi = s[1][lane];
+  h[0] = make_float2(lo.x, lo.y); h[1] = make_float2(lo.z, lo.w);
+  h[2] = make_float2(hi.x, hi.y); h[3] = make_float2(hi.z, hi.w);
+}
+__device__ __forceinline__ void get_last(const float2 (&h)[4], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = h[i].x;
+    v[2 * i + 1] = h[i].y;
+  }
 }
 
 // Shared memory of a warp.  Rows of a tile are looked after by four lanes each (kVec channels a
@@ -136,19 +155,31 @@ __device__ __forceinline__ void get(const float* p, float2* v) {
   }
 }
 
-template <typename T, int kS>
-__global__ void __launch_bounds__(32 * kScanWarps, 1) scan_kernel(const ScanArgs a, int* err) {
+// What a segment of a sequence does to a state (kCut): h -> exp(A time) h + own.
+template <int kS>
+struct Segment {
+  float4 own[2][32];
+  float time[256 / kS];
+};
+
+// kWarps: of a ring, 12 of them an SM in one CTA or in three of 4.  kCut: the CTAs of a cluster take
+// a segment of the sequence each, two passes over it: what it does to a state, then, from the state
+// that the segments before it leave, the scan.
+template <typename T, int kS, int kWarps, bool kCut>
+__global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const ScanArgs a, int* err) {
   using W = ScanWarp<T, kS>;
   constexpr int kLn = W::kLn, kCh = W::kCh, kVec = W::kVec, kBc = kS / 2;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   W& w = reinterpret_cast<W*>(smem)[warp];
-  const int from = (warp + kScanWarps - 1) % kScanWarps;
+  const int from = (warp + kWarps - 1) % kWarps;
   const W& before = reinterpret_cast<W*>(smem)[from];
 
   const int per_group = a.C / a.G;
   const int blocks = (per_group + kCh - 1) / kCh;  // of a group
-  const int64_t unit = blockIdx.x;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();  // (of one CTA, uncut)
+  const int64_t unit = blockIdx.x / (kCut ? cluster.num_blocks() : 1);
   const int n = (int)(unit / ((int64_t)blocks * a.G));
   const int rest = (int)(unit - (int64_t)n * blocks * a.G);
   const int g = rest / blocks, first = (rest - g * blocks) * kCh;  // first channel in the group
@@ -167,17 +198,22 @@ __global__ void __launch_bounds__(32 * kScanWarps, 1) scan_kernel(const ScanArgs
   }
   const int64_t at = ((int64_t)n * a.C + c) * kS + 8 * sub;
 
+  if constexpr (kCut) {
+    const int64_t all = (t1 - t0 + kTok - 1) / kTok;
+    const int64_t part = (all + cluster.num_blocks() - 1) / cluster.num_blocks() * kTok;
+    t0 = min(t1, t0 + cluster.block_rank() * part);
+    t1 = min(t1, t0 + part);
+  }
   const int len = (int)(t1 - t0), tiles = (len + kTok - 1) / kTok;
-  if (tiles == 0) {
-    if (warp == 0 && a.hT && on) {
+  if constexpr (!kCut) {
+    if (tiles == 0 && warp == 0 && a.hT && on) {
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = a.h0 ? a.h0[at + i] : 0.f;
       store8(a.hT + at, v);
     }
-    return;
+    if (warp >= tiles) return;
   }
-  if (warp >= tiles) return;
   // The lane's part of a tile's rows: kVec channels of token `row`, and kS / 2 values of B or C.
   const int row = lane / 4, ch = kVec * (lane % 4);
   const bool has = ch < width;
@@ -191,7 +227,7 @@ __global__ void __launch_bounds__(32 * kScanWarps, 1) scan_kernel(const ScanArgs
   const int64_t sb = lane < 16 ? a.sB : a.sC;
   const char* bp = static_cast<const char*>(lane < 16 ? a.B : a.Cm) +
                    ((t0 + warp * kTok + brow) * sb + g * kS + bcol) * (int)sizeof(T);
-  constexpr int64_t kHop = (int64_t)kScanWarps * kTok * sizeof(T);
+  constexpr int64_t kHop = (int64_t)kWarps * kTok * sizeof(T);
   float2 bias[kVec / 2], skip[kVec / 2];
 #pragma unroll
   for (int j = 0; j < kVec / 2; ++j) {
@@ -237,119 +273,255 @@ __global__ void __launch_bounds__(32 * kScanWarps, 1) scan_kernel(const ScanArgs
     for (int j = 0; j < kBc / 2; ++j) v[j] = rb.pair(j);
     put<kBc>(&w.BC[buf][lane / 16][brow][bcol], v);
   };
-  fetch(len - warp * kTok);
-  wait_copies();
-  front(len - warp * kTok);
-  lay(0);
-  __syncwarp();
-  if (warp + kScanWarps < tiles) fetch(len - (warp + kScanWarps) * kTok);
-  int buf = 0;
-  for (int tile = warp; tile < tiles; tile += kScanWarps) {
-    const int left = len - tile * kTok;  // tokens from the tile's first on
-
-    // what the tile's tokens do to a state that comes in: h -> all h + own, y = acc + share . h
-    float2 own[4], all[4], share[kTok][4], acc[kTok];
-    float time = 0.f;
+  // The state that comes in from outside, and what leaves at the end (of an uncut sequence at once).
+  __shared__ Segment<kS> mine_seg;
+  __shared__ float4 enter[2][32];
+  __shared__ float times[kWarps][kCh];
+  float last[8];
+  bool ends = false;
+  auto outside = [&](float2 (&h)[4]) {
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-      const float d = w.delta[buf][t][cl], dx = w.dx[buf][t][cl];
-      float2 bs[4], cs[4];
-      get<8>(&w.BC[buf][0][t][8 * sub], bs);
-      get<8>(&w.BC[buf][1][t][8 * sub], cs);
-      time += d;
+    for (int i = 0; i < 4; ++i)
+      h[i] = a.h0 ? *reinterpret_cast<const float2*>(a.h0 + at + 2 * i) : both(0.f);
+  };
+  auto start = [&] {  // the first tile's front, the second one's copies
+    fetch(len - warp * kTok);
+    wait_copies();
+    front(len - warp * kTok);
+    lay(0);
+    __syncwarp();
+    if (warp + kWarps < tiles) fetch(len - (warp + kWarps) * kTok);
+  };
+  if constexpr (kCut) {
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    float sum = 0.f;
+    if (rank + 1 < ctas && warp < tiles) {  // (nothing follows on the last segment)
+      const char *const x0 = xp, *const d0 = dp, *const z0 = zp, *const b0 = bp;
+      zp = nullptr;
+      start();
+      int buf = 0;
+      for (int tile = warp; tile < tiles; tile += kWarps) {
+        float2 own[4], h[4];
+        float time = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = __fmul2_rn(A[i], both(d));
-        const float2 e = make_float2(ex2(u.x), ex2(u.y));
-        const float2 add = __fmul2_rn(both(dx), bs[i]);
-        own[i] = t == 0 ? add : __ffma2_rn(e, own[i], add);
-        all[i] = t == 0 ? e : __fmul2_rn(e, all[i]);
-        acc[t] = i == 0 ? __fmul2_rn(cs[i], own[i]) : __ffma2_rn(cs[i], own[i], acc[t]);
-        share[t][i] = __fmul2_rn(cs[i], all[i]);
+        for (int t = 0; t < kTok; ++t) {
+          const float d = w.delta[buf][t][cl], dx = w.dx[buf][t][cl];
+          float2 bs[4];
+          get<8>(&w.BC[buf][0][t][8 * sub], bs);
+          time += d;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 u = __fmul2_rn(A[i], both(d));
+            const float2 add = __fmul2_rn(both(dx), bs[i]);
+            own[i] = t == 0 ? add : __ffma2_rn(make_float2(ex2(u.x), ex2(u.y)), own[i], add);
+          }
+        }
+        sum += time;
+        if (tile > 0) {
+          handed(1 + from);
+          get_state(before.state, lane, h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 u = __fmul2_rn(A[i], both(time));
+            own[i] = __ffma2_rn(make_float2(ex2(u.x), ex2(u.y)), h[i], own[i]);
+          }
+        }
+        if (tile + 1 < tiles) {
+          put_state(w.state, lane, own);
+          hand(1 + warp);
+        } else {
+          put_state(mine_seg.own, lane, own);
+        }
+        wait_copies();
+        front(len - (tile + kWarps) * kTok);
+        buf ^= 1;
+        lay(buf);
+        __syncwarp();
+        if (tile + 2 * kWarps < tiles) fetch(len - (tile + 2 * kWarps) * kTok);
+      }
+      xp = x0; dp = d0; zp = z0; bp = b0;
+    }
+    if (sub == 0) times[warp][cl] = sum;
+    __syncthreads();
+    if (warp == 0 && sub == 0) {
+      float time = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) time += times[i][cl];
+      mine_seg.time[cl] = time;
+    }
+    if (warp == 0 && tiles == 0) {
+      const float2 none[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+      put_state(mine_seg.own, lane, none);
+    }
+    cluster.sync();
+    if (warp == 0) {
+      float2 h[4];
+      outside(h);
+#pragma unroll 1
+      for (int j = 0; j < rank; ++j) {
+        const Segment<kS>* seg = cluster.map_shared_rank(&mine_seg, j);
+        const float time = seg->time[cl];
+        float2 own[4];
+        get_state(seg->own, lane, own);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = __fmul2_rn(A[i], both(time));
+          h[i] = __ffma2_rn(make_float2(ex2(u.x), ex2(u.y)), h[i], own[i]);
+        }
+      }
+      put_state(enter, lane, h);
+      __syncwarp();
+      if (tiles == 0 && rank + 1 == ctas) {
+        ends = true;
+        get_last(h, last);
       }
     }
-    // (the state itself decays by one exponential a tile: their errors, of about 2^-26 and one
-    // sign, add up over as many tokens as a slow decay remembers)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 u = __fmul2_rn(A[i], both(time));
-      all[i] = make_float2(ex2(u.x), ex2(u.y));
-    }
-    float2 h[4];
-    if (tile == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        h[i] = a.h0 ? *reinterpret_cast<const float2*>(a.h0 + at + 2 * i) : make_float2(0.f, 0.f);
-    } else {
-      handed(1 + from);
-      const float4 lo = before.state[0][lane], hi = before.state[1][lane];
-      h[0] = make_float2(lo.x, lo.y); h[1] = make_float2(lo.z, lo.w);
-      h[2] = make_float2(hi.x, hi.y); h[3] = make_float2(hi.z, hi.w);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) own[i] = __ffma2_rn(all[i], h[i], own[i]);
-    if (tile + 1 < tiles) {
-      w.state[0][lane] = make_float4(own[0].x, own[0].y, own[1].x, own[1].y);
-      w.state[1][lane] = make_float4(own[2].x, own[2].y, own[3].x, own[3].y);
-      hand(1 + warp);
-    } else if (a.hT && on) {
-      const float v[8] = {own[0].x, own[0].y, own[1].x, own[1].y, own[2].x, own[2].y, own[3].x, own[3].y};
-      store8(a.hT + at, v);
-    }
-    // this tile's outputs, and the next one's front between them (of zeros, behind the last)
-    float2 gate[kVec / 2], old[kVec / 2];
-#pragma unroll
-    for (int j = 0; j < kVec / 2; ++j) {
-      old[j] = __fmul2_rn(skip[j], x.pair(j));
-      gate[j] = silu2(z.pair(j));
-      if (!a.z) gate[j] = both(1.f);
-    }
-    wait_copies();
-    front(left - kScanWarps * kTok);
-#pragma unroll
-    for (int t = 0; t < kTok; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t] = __ffma2_rn(share[t][i], h[i], acc[t]);
-    buf ^= 1;
-#pragma unroll
-    for (int t = 0; t < kTok; ++t) w.part[sub][t * kCh + cl] = acc[t].x + acc[t].y;
-    lay(buf);
     __syncwarp();
-    if (tile + 2 * kScanWarps < tiles) fetch(len - (tile + 2 * kScanWarps) * kTok);
-    float2 v[kVec / 2];
-    get<kVec>(&w.part[0][row * kCh + ch], v);
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // outside and segments are read
+  }
+  if (!kCut || warp < tiles) {
+    start();
+    int buf = 0;
+    for (int tile = warp; tile < tiles; tile += kWarps) {
+      const int left = len - tile * kTok;  // tokens from the tile's first on
+      // what the tile's tokens do to a state that comes in: h -> all h + own, y = acc + share . h
+      float2 own[4], all[4], share[kTok][4], acc[kTok];
+      float time = 0.f;
 #pragma unroll
-    for (int m = 1; m < kLn; ++m) {
-      float2 u[kVec / 2];
-      get<kVec>(&w.part[m][row * kCh + ch], u);
+      for (int t = 0; t < kTok; ++t) {
+        const float d = w.delta[buf][t][cl], dx = w.dx[buf][t][cl];
+        float2 bs[4], cs[4];
+        get<8>(&w.BC[buf][0][t][8 * sub], bs);
+        get<8>(&w.BC[buf][1][t][8 * sub], cs);
+        time += d;
 #pragma unroll
-      for (int j = 0; j < kVec / 2; ++j) v[j] = __fadd2_rn(v[j], u[j]);
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = __fmul2_rn(A[i], both(d));
+          const float2 e = make_float2(ex2(u.x), ex2(u.y));
+          const float2 add = __fmul2_rn(both(dx), bs[i]);
+          own[i] = t == 0 ? add : __ffma2_rn(e, own[i], add);
+          all[i] = t == 0 ? e : __fmul2_rn(e, all[i]);
+          acc[t] = i == 0 ? __fmul2_rn(cs[i], own[i]) : __ffma2_rn(cs[i], own[i], acc[t]);
+          share[t][i] = __fmul2_rn(cs[i], all[i]);
+        }
+      }
+      // (the state itself decays by one exponential a tile: their errors, of about 2^-26 and one
+      // sign, add up over as many tokens as a slow decay remembers)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = __fmul2_rn(A[i], both(time));
+        all[i] = make_float2(ex2(u.x), ex2(u.y));
+      }
+      float2 h[4];
+      if (tile > 0) {
+        handed(1 + from);
+        get_state(before.state, lane, h);
+      } else if constexpr (kCut) {
+        get_state(enter, lane, h);
+      } else {
+        outside(h);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own[i] = __ffma2_rn(all[i], h[i], own[i]);
+      if (tile + 1 < tiles) {
+        put_state(w.state, lane, own);
+        hand(1 + warp);
+      } else {
+        get_last(own, last);
+        if constexpr (kCut)
+          ends = cluster.block_rank() + 1 == cluster.num_blocks();
+        else if (a.hT && on)
+          store8(a.hT + at, last);
+      }
+      // this tile's outputs, and the next one's front between them (of zeros, behind the last)
+      float2 gate[kVec / 2], old[kVec / 2];
+#pragma unroll
+      for (int j = 0; j < kVec / 2; ++j) {
+        old[j] = __fmul2_rn(skip[j], x.pair(j));
+        gate[j] = silu2(z.pair(j));
+        if (!a.z) gate[j] = both(1.f);
+      }
+      wait_copies();
+      front(left - kWarps * kTok);
+#pragma unroll
+      for (int t = 0; t < kTok; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t] = __ffma2_rn(share[t][i], h[i], acc[t]);
+      buf ^= 1;
+#pragma unroll
+      for (int t = 0; t < kTok; ++t) w.part[sub][t * kCh + cl] = acc[t].x + acc[t].y;
+      lay(buf);
+      __syncwarp();
+      if (tile + 2 * kWarps < tiles) fetch(len - (tile + 2 * kWarps) * kTok);
+      float2 v[kVec / 2];
+      get<kVec>(&w.part[0][row * kCh + ch], v);
+#pragma unroll
+      for (int m = 1; m < kLn; ++m) {
+        float2 u[kVec / 2];
+        get<kVec>(&w.part[m][row * kCh + ch], u);
+#pragma unroll
+        for (int j = 0; j < kVec / 2; ++j) v[j] = __fadd2_rn(v[j], u[j]);
+      }
+      Raw<T, kVec> out;
+#pragma unroll
+      for (int j = 0; j < kVec / 2; ++j)
+        out.set_pair(j, __fmul2_rn(__fadd2_rn(v[j], old[j]), gate[j]));
+      if (has && row < left) out.store(yp);
+      yp += kHop * a.sy;
+      __syncwarp();  // the sums have been read
     }
-    Raw<T, kVec> out;
-#pragma unroll
-    for (int j = 0; j < kVec / 2; ++j)
-      out.set_pair(j, __fmul2_rn(__fadd2_rn(v[j], old[j]), gate[j]));
-    if (has && row < left) out.store(yp);
-    yp += kHop * a.sy;
-    __syncwarp();  // the sums have been read
+  }
+  if constexpr (kCut) {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (ends && a.hT && on) store8(a.hT + at, last);  // (hT may be h0)
   }
 }
 
-template <typename T, int kS>
-cudaError_t launch_scan_t(const ScanArgs& a, unsigned units, int* err, cudaStream_t s) {
-  constexpr size_t smem = kScanWarps * sizeof(ScanWarp<T, kS>);
+template <typename T, int kS, int kWarps, bool kCut>
+cudaError_t launch_scan_t(const ScanArgs& a, unsigned units, int ctas, int* err, cudaStream_t s) {
+  constexpr size_t smem = kWarps * sizeof(ScanWarp<T, kS>);
+  const auto kernel = scan_kernel<T, kS, kWarps, kCut>;
   static std::atomic<uint64_t> told{0};  // devices that know how much shared memory this takes
   int dev = 0;
   cudaGetDevice(&dev);
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!(told.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        scan_kernel<T, kS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     told |= bit;
   }
-  scan_kernel<T, kS><<<units, 32 * kScanWarps, smem, s>>>(a, err);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(units * (unsigned)ctas);
+  c.blockDim = dim3(32 * kWarps);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  c.attrs = &at;
+  c.numAttrs = kCut ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, a, err);
+}
+
+int sm_count() {
+  int sms = 152, dev = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+// Whether three rings of 4 warps an SM are expected to end before one of 12.  A ring of 12 takes
+// 117 ns a tile, one of 4 takes 200 alone, 265 beside another and 330 beside two (S = 16; the ratios
+// are about the same for 8 and 32), and a CTA some 3 us to begin and end, which others cover where
+// there are any.  (512 units of 1024 tiles: 460 against 530 us; 4096 of 64: 279 against 220.)
+bool short_rings(int64_t units, int64_t tiles, int sms) {
+  const double t = (double)tiles, one = t * 0.117 + 3;
+  const int64_t rounds = units / (3 * sms), rest = units - rounds * 3 * sms;
+  const double last = rest == 0 ? 0 : (rest > 2 * sms ? 0.33 : rest > sms ? 0.265 : 0.2) * t + 3;
+  return rounds * (t * 0.33 + 1) + last < (double)((units + sms - 1) / sms) * one;
 }
 
 }  // namespace
@@ -359,11 +531,25 @@ cudaError_t launch_scan(const ScanArgs& a, int bf16, int S, int* err, cudaStream
   const int64_t units = (int64_t)a.N * a.G * ((a.C / a.G + ch - 1) / ch);
   if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
   ProfScope prof_scope("kda_scan", s);
+  const int64_t tiles = (a.NT / a.N + kTok - 1) / kTok;  // of a sequence, on average
+  const int sms = sm_count();
+  // Few units of long sequences: a cluster each, its CTAs a segment each.  The pass that finds
+  // what a segment does to a state costs half a scan, so two segments gain little (8192 tokens x
+  // 1024 channels 122 -> 110 us; 1024 tokens lose), four halve the time (x 512 channels 121 -> 62 us,
+  // 2048 tokens 38 -> 26).
+  int cut = 1;
+  while (cut < 8 && units * cut * 2 <= sms && tiles >= 128 * cut) cut *= 2;
+  if (cut == 2 && tiles < 512) cut = 1;
+  const bool four = cut == 1 && short_rings(units, tiles, sms);
   cudaError_t e = cudaSuccess;
   with_states(S, [&](auto k) {
     constexpr int kS = decltype(k)::value;
-    e = bf16 ? launch_scan_t<__nv_bfloat16, kS>(a, (unsigned)units, err, s)
-             : launch_scan_t<float, kS>(a, (unsigned)units, err, s);
+    using H = __nv_bfloat16;
+    const auto fn =
+        cut > 1 ? (bf16 ? launch_scan_t<H, kS, 12, true> : launch_scan_t<float, kS, 12, true>)
+        : four  ? (bf16 ? launch_scan_t<H, kS, 4, false> : launch_scan_t<float, kS, 4, false>)
+                : (bf16 ? launch_scan_t<H, kS, 12, false> : launch_scan_t<float, kS, 12, false>);
+    e = fn(a, (unsigned)units, cut, err, s);
   });
   return e;
 }

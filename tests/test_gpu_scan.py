@@ -187,6 +187,24 @@ def test_long_prompts_continue_from_their_states(kda, dtype):
         check(torch.cat([ya, yb]), hb, d)
 
 
+@pytest.mark.parametrize("dtype", DT, ids=IDS)
+@pytest.mark.parametrize("S", [8, 16, 32])
+@pytest.mark.parametrize("lens", [[4097], [5000, 0, 1, 4100], [2600, 2048, 33, 3500], [9000]])
+def test_few_channels_of_long_sequences(kda, dtype, S, lens):
+    """Few enough (sequence, channels) for sequences to be cut, among them some shorter than a
+    segment; in place, and twice the same bits."""
+    d = make(lens, 24, S, 1, dtype, seed=sum(lens) + S, strong=0.05)
+    y, hT = scan(kda, d)
+    check(y, hT, d)
+    g = on_gpu(d)
+    h = g["h0"].clone()
+    y2, _ = kda.selective_scan_fwd(g["x"], g["dt"], g["A"], g["B"], g["C"], h, g["cu"], D=g["D"],
+                                   z=g["z"], dt_bias=g["bias"], final_state_out=h)
+    assert torch.equal(y, y2) and torch.equal(h, hT)
+    y3, none = scan(kda, d, output_final_state=False)
+    assert none is None and torch.equal(y3, y)
+
+
 def test_results_do_not_depend_on_the_batch(kda):
     """A sequence alone, among others and twice: the same bits."""
     lens = [130, 0, 64, 777, 9]
