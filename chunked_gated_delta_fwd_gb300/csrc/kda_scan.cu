@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
     for (int tile = warp; tile < tiles; tile += kWarps) {
       const int left = len - tile * kTok;  // tokens from the tile's first on
       // what the tile's tokens do to a state that comes in: h -> all h + own, y = acc + share . h
-      float2 own[4], all[4], share[kTok][4], acc[kTok];
-      float time = 0.f;
+      float2 own[4], all[4], share[kTok][4];
+      float acc[kTok], time = 0.f;
 #pragma unroll
       for (int t = 0; t < kTok; ++t) {
         const float d = w.delta[buf][t][cl], dx = w.dx[buf][t][cl];
@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
         get<8>(&w.BC[buf][0][t][8 * sub], bs);
         get<8>(&w.BC[buf][1][t][8 * sub], cs);
         time += d;
+        float2 y2;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 u = __fmul2_rn(A[i], both(d));
@@ -401,9 +402,10 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
           const float2 add = __fmul2_rn(both(dx), bs[i]);
           own[i] = t == 0 ? add : __ffma2_rn(e, own[i], add);
           all[i] = t == 0 ? e : __fmul2_rn(e, all[i]);
-          acc[t] = i == 0 ? __fmul2_rn(cs[i], own[i]) : __ffma2_rn(cs[i], own[i], acc[t]);
+          y2 = i == 0 ? __fmul2_rn(cs[i], own[i]) : __ffma2_rn(cs[i], own[i], y2);
           share[t][i] = __fmul2_rn(cs[i], all[i]);
         }
+        acc[t] = y2.x + y2.y;
       }
       // (the state itself decays by one exponential a tile: their errors, of about 2^-26 and one
       // sign, add up over as many tokens as a slow decay remembers)
@@ -444,12 +446,15 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
       wait_copies();
       front(left - kWarps * kTok);
 #pragma unroll
-      for (int t = 0; t < kTok; ++t)
+      for (int t = 0; t < kTok; ++t) {
+        float2 y2 = __fmul2_rn(share[t][0], h[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t] = __ffma2_rn(share[t][i], h[i], acc[t]);
+        for (int i = 1; i < 4; ++i) y2 = __ffma2_rn(share[t][i], h[i], y2);
+        acc[t] += y2.x + y2.y;
+      }
       buf ^= 1;
 #pragma unroll
-      for (int t = 0; t < kTok; ++t) w.part[sub][t * kCh + cl] = acc[t].x + acc[t].y;
+      for (int t = 0; t < kTok; ++t) w.part[sub][t * kCh + cl] = acc[t];
       lay(buf);
       __syncwarp();
       if (tile + 2 * kWarps < tiles) fetch(len - (tile + 2 * kWarps) * kTok);
