@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
     const ScanArgs a, float* __restrict__ state, const int32_t* __restrict__ n_advance) {
   constexpr int kLn = kS / 4, kSlots = kLn, kT = kMulti ? 16 : 1;
   constexpr unsigned kAll = 0xffffffffu;
-  __shared__ __align__(16) float BC[2][kSlots][kT][kS];
+  __shared__ __align__(16) float BC[2][kSlots * kT][kS];  // rows as in memory: Tn a sequence
   const int Tn = kMulti ? (int)a.T : 1;
   const int per_group = a.C / a.G;
   const int blocks = (per_group * kLn + kStepThreads - 1) / kStepThreads;  // of a group
@@ -46,21 +46,24 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
     } else {
       h[i][0] = h[i][1] = h[i][2] = h[i][3] = 0.f;
     }
-  int64_t row = n * Tn;
+  const T* xp = static_cast<const T*>(a.x) + n * Tn * a.sx + c;
+  const T* dp = static_cast<const T*>(a.dt) + n * Tn * a.sdt + c;
+  const T* zp = a.z ? static_cast<const T*>(a.z) + n * Tn * a.sz + c : nullptr;
+  T* yp = a.y ? static_cast<T*>(a.y) + n * Tn * a.sy + c : nullptr;
   T rx, rd, rz;
-  auto fetch = [&](int64_t r) {
-    rx = static_cast<const T*>(a.x)[r * a.sx + c];
-    rd = static_cast<const T*>(a.dt)[r * a.sdt + c];
-    if (a.z) rz = static_cast<const T*>(a.z)[r * a.sz + c];
+  auto fetch = [&] {
+    rx = *xp;
+    rd = *dp;
+    if (zp) rz = *zp;
   };
-  fetch(row);
+  fetch();
   for (int e = threadIdx.x; e < 2 * there * Tn * kLn; e += kStepThreads) {
-    const int q = e % kLn, which = e / kLn % 2, t = e / (2 * kLn) % Tn, i = e / (2 * kLn) / Tn;
-    const int64_t r = (n0 + i) * Tn + t;
-    const T* src = which ? static_cast<const T*>(a.Cm) + r * a.sC : static_cast<const T*>(a.B) + r * a.sB;
+    const int q = 4 * (e % kLn), which = e / kLn % 2, r = e / (2 * kLn);
+    const T* src = which ? static_cast<const T*>(a.Cm) + (n0 * Tn + r) * a.sC
+                         : static_cast<const T*>(a.B) + (n0 * Tn + r) * a.sB;
     float v[4];
-    load4(src + g * kS + 4 * q, v);
-    store4(&BC[which][i][t][4 * q], v);
+    load4(src + g * kS + q, v);
+    store4(&BC[which][r][q], v);
   }
   float A[4];
   load4(a.A + (int64_t)c * kS + 4 * sub, A);
@@ -72,30 +75,40 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
     adv = __ldg(n_advance + n);
     adv = adv < 0 ? 0 : (adv > Tn ? Tn : adv);
   }
+  int stop[kSlots];  // the tokens behind which the states are stored (0: none)
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int upto = kMulti ? __shfl_sync(kAll, adv, i, kLn) : 1;
+    stop[i] = on && i < there ? upto : 0;
+  }
   __syncthreads();
 #pragma unroll 1
   for (int t = 0; t < Tn; ++t) {
-    const float x = to_f32(rx), z = a.z ? to_f32(rz) : 0.f;
+    const float x = to_f32(rx), z = zp ? to_f32(rz) : 0.f;
     float d = to_f32(rd) + bias;
-    if (kMulti && t + 1 < Tn) fetch(row + t + 1);
+    if (kMulti && t + 1 < Tn) {
+      xp += a.sx;
+      dp += a.sdt;
+      zp += zp ? a.sz : 0;
+      fetch();
+    }
     if (a.softplus) d = softplus(d);
     const float dx = d * x;
     float acc[kSlots];
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       const float di = __shfl_sync(kAll, d, i, kLn), dxi = __shfl_sync(kAll, dx, i, kLn);
-      const float4 b = *reinterpret_cast<const float4*>(&BC[0][i][t][4 * sub]);
-      const float4 k = *reinterpret_cast<const float4*>(&BC[1][i][t][4 * sub]);
+      const float4 b = *reinterpret_cast<const float4*>(&BC[0][i * Tn + t][4 * sub]);
+      const float4 k = *reinterpret_cast<const float4*>(&BC[1][i * Tn + t][4 * sub]);
       h[i][0] = fmaf(ex2(di * A[0]), h[i][0], dxi * b.x);
       h[i][1] = fmaf(ex2(di * A[1]), h[i][1], dxi * b.y);
       h[i][2] = fmaf(ex2(di * A[2]), h[i][2], dxi * b.z);
       h[i][3] = fmaf(ex2(di * A[3]), h[i][3], dxi * b.w);
       acc[i] = fmaf(k.x, h[i][0], fmaf(k.y, h[i][1], fmaf(k.z, h[i][2], k.w * h[i][3])));
-      const bool keep = kMulti ? t + 1 == __shfl_sync(kAll, adv, i, kLn) : true;
-      if (on && i < there && keep)
+      if (t + 1 == stop[i])
         __stcs(at + i * hop, make_float4(h[i][0], h[i][1], h[i][2], h[i][3]));
     }
-    if (!a.y) continue;
+    if (!yp) continue;
     // halving exchange inside a channel's lanes: lane sub ends with sequence sub
 #pragma unroll
     for (int m = kLn / 2; m > 0; m /= 2) {
@@ -107,8 +120,9 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
       }
     }
     float y = fmaf(skip, x, acc[0]);
-    if (a.z) y *= silu(z);
-    if (mine) static_cast<T*>(a.y)[(row + t) * a.sy + c] = from_f32<T>(y);
+    if (zp) y *= silu(z);
+    if (mine) *yp = from_f32<T>(y);
+    yp += a.sy;
   }
 }
 
