@@ -6,7 +6,10 @@
 // Bound by HBM: x is read and y written once.  A lane holds four channels and
 // walks a run of tokens with the last W - 1 inputs in registers, so a run reads W - 1 rows more
 // than it has (from L2: its neighbour reads them as well).  Eight rows are on their way while eight
-// are worked on; products are packed pairs.  Sums are fp32, rounded once.
+// are worked on; products are packed pairs.  Sums are fp32, rounded once.  8192 tokens x 12288
+// channels, W = 4 with SiLU: bf16 81 us (5.0 TB/s; unpacking, products and the two special functions a
+// channel of SiLU take a third of the schedulers' turns each), fp32 127 to 132 us (6.1 TB/s); 512
+// single tokens of as many channels 24 us (4.2 TB/s), one 3.5 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -63,7 +66,8 @@ struct Taps {
 #pragma unroll
       for (int j = 0; j < kW; ++j) w[j][i] = make_float2(raw[2 * i * kW + j], raw[(2 * i + 1) * kW + j]);
   }
-  __device__ __forceinline__ Row<T> row(const float2 (*window)[kPairs], bool act) const {
+  template <bool kAct>
+  __device__ __forceinline__ Row<T> row(const float2 (*window)[kPairs]) const {
     float2 y[kPairs];
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
@@ -71,7 +75,7 @@ struct Taps {
 #pragma unroll
       for (int j = 0; j < kW; ++j) y[i] = __ffma2_rn(w[j][i], window[j][i], y[i]);
     }
-    if (act) {
+    if constexpr (kAct) {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) y[i] = silu2(y[i]);
     }
@@ -91,7 +95,7 @@ struct ConvArgs {
   int64_t T_per_seq, NT;
   int64_t sx, sy;       // bytes between tokens
   int64_t runs;
-  int N, C, run, act;
+  int N, C, run;
   int ends;  // blocks that look after the sequences as a whole
 };
 
@@ -146,7 +150,7 @@ __device__ void conv_ends(const ConvArgs& a, int K, int* err) {
   if (bad && threadIdx.x == 0 && err) atomicExch(err, kDevErrBadSeqlens);
 }
 
-template <typename T, int kW>
+template <typename T, int kW, bool kAct>
 __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, int* err) {
   constexpr int K = kW - 1;
   constexpr int kPiece = (int)sizeof(Row<T>);
@@ -171,14 +175,23 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
   const Row<T> zero{};
   float2 win[K + kGroup][kPairs];
   Row<T> ahead[kGroup];
-  auto fetch = [&](int64_t from, int64_t end) {
+  const char* xr = nullptr;  // the row that is fetched next
+  auto fetch = [&](int left) {
+    if (left >= kGroup) {
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i)
-      if (from + i < end) ahead[i] = *reinterpret_cast<const Row<T>*>(x + (from + i) * a.sx);
+      for (int i = 0; i < kGroup; ++i, xr += a.sx) ahead[i] = *reinterpret_cast<const Row<T>*>(xr);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kGroup - 1; ++i, xr += a.sx)
+        if (i < left) ahead[i] = *reinterpret_cast<const Row<T>*>(xr);
+    }
   };
   while (t < stop) {  // sequence by sequence
     const int64_t end = min(sp.end, stop);
-    fetch(t, end);
+    int left = (int)(end - t);  // (a run's tokens at most, and W - 2)
+    xr = x + t * a.sx;
+    char* yr = y + t * a.sy;
+    fetch(left);
     Row<T> old[K];
     if (t == sp.begin) {
       const int64_t at = (int64_t)sp.n * K * kept + kPiece * (int64_t)cv;
@@ -209,28 +222,23 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
     }
 #pragma unroll
     for (int r = 0; r < K; ++r) unpack(old[r], win[r]);
-    for (;;) {
+    for (;; left -= kGroup) {
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) unpack(ahead[i], win[K + i]);
-      fetch(t + kGroup, end);
-      if (end - t >= kGroup) {
+      fetch(left - kGroup);
+      if (left < kGroup) break;
 #pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-          *reinterpret_cast<Row<T>*>(y + (t + i) * a.sy) = taps.row(win + i, a.act);
-        t += kGroup;
-        if (t == end) break;
+      for (int i = 0; i < kGroup; ++i, yr += a.sy)
+        *reinterpret_cast<Row<T>*>(yr) = taps.template row<kAct>(win + i);
 #pragma unroll
-        for (int r = 0; r < K; ++r)
+      for (int r = 0; r < K; ++r)
 #pragma unroll
-          for (int j = 0; j < kPairs; ++j) win[r][j] = win[kGroup + r][j];
-      } else {
-#pragma unroll
-        for (int i = 0; i < kGroup - 1; ++i)
-          if (t + i < end) *reinterpret_cast<Row<T>*>(y + (t + i) * a.sy) = taps.row(win + i, a.act);
-        t = end;
-        break;
-      }
+        for (int j = 0; j < kPairs; ++j) win[r][j] = win[kGroup + r][j];
     }
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i, yr += a.sy)
+      if (i < left) *reinterpret_cast<Row<T>*>(yr) = taps.template row<kAct>(win + i);
+    t = end;
     if (t < stop) sp = span_of(a, t);
   }
 }
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
 // T new tokens of N sequences (kOne: one); the kept inputs end as they are behind the first
 // n_advance.  Several sequences a lane, to read the taps once, are slower (512 sequences x 12288
 // channels: 39 us with two or four).
-template <typename T, int kW, bool kOne>
+template <typename T, int kW, bool kAct, bool kOne>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(
     const ConvArgs a, char* __restrict__ state, const int32_t* __restrict__ n_advance, int T_) {
   constexpr int K = kW - 1, kG = kOne ? 1 : kStepGroup;
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(
 #pragma unroll
     for (int i = 0; i < kG; ++i) {
       if (t + i >= Tn) continue;
-      if (y) *reinterpret_cast<Row<T>*>(y + (t + i) * a.sy) = taps.row(f + i, a.act);
+      if (y) *reinterpret_cast<Row<T>*>(y + (t + i) * a.sy) = taps.template row<kAct>(f + i);
       if (t + i + 1 == adv) {
 #pragma unroll
         for (int r = 0; r < K; ++r) *reinterpret_cast<Row<T>*>(st + r * kept) = win[i + 1 + r];
@@ -303,7 +311,7 @@ void with_width(int W, F f) {
 }
 
 template <typename T>
-cudaError_t launch_conv_t(ConvArgs a, int W, int* err, cudaStream_t s) {
+cudaError_t launch_conv_t(ConvArgs a, int W, int act, int* err, cudaStream_t s) {
   const int lanes = a.C / kVec;
   // Runs as long as they leave some 500 lanes an SM, up to 64 tokens: a lane finds its sequence, its
   // taps and its first rows once a run (8192 tokens x 12288 channels: 96, 83, 81 us in runs of 16, 32
@@ -317,7 +325,9 @@ cudaError_t launch_conv_t(ConvArgs a, int W, int* err, cudaStream_t s) {
   if (blocks + a.ends > INT32_MAX) return cudaErrorInvalidConfiguration;
   ProfScope prof_scope("kda_conv", s);
   with_width(W, [&](auto w) {
-    conv_kernel<T, decltype(w)::value><<<(unsigned)(blocks + a.ends), kConvThreads, 0, s>>>(a, err);
+    constexpr int kW = decltype(w)::value;
+    const auto fn = act ? conv_kernel<T, kW, true> : conv_kernel<T, kW, false>;
+    fn<<<(unsigned)(blocks + a.ends), kConvThreads, 0, s>>>(a, err);
   });
   return cudaGetLastError();
 }
@@ -331,8 +341,9 @@ cudaError_t launch_conv(const void* x, int bf16, const float* w, const float* b,
   const int e = bf16 ? 2 : 4;
   ConvArgs a{static_cast<const char*>(x), static_cast<char*>(y), w, b,
              static_cast<const char*>(state), static_cast<char*>(last), cu, T_per_seq, n_tokens,
-             sx * e, sy * e, 0, n_seqs, C, 0, act, 0};
-  return bf16 ? launch_conv_t<__nv_bfloat16>(a, W, err, s) : launch_conv_t<float>(a, W, err, s);
+             sx * e, sy * e, 0, n_seqs, C, 0, 0};
+  return bf16 ? launch_conv_t<__nv_bfloat16>(a, W, act, err, s)
+              : launch_conv_t<float>(a, W, act, err, s);
 }
 
 cudaError_t launch_conv_step(const void* x, int bf16, const float* w, const float* b, void* state,
@@ -340,7 +351,7 @@ cudaError_t launch_conv_step(const void* x, int bf16, const float* w, const floa
                              int64_t sx, int64_t sy, int act, cudaStream_t s) {
   const int e = bf16 ? 2 : 4;
   ConvArgs a{static_cast<const char*>(x), static_cast<char*>(y), w, b, nullptr, nullptr, nullptr, T,
-             (int64_t)N * T, sx * e, sy * e, 0, N, C, 0, act, 0};
+             (int64_t)N * T, sx * e, sy * e, 0, N, C, 0, 0};
   const int64_t lanes = C / kVec;
   const int64_t blocks = (N * lanes + kConvThreads - 1) / kConvThreads;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -348,9 +359,14 @@ cudaError_t launch_conv_step(const void* x, int bf16, const float* w, const floa
   const bool one = T == 1 && !n_advance && y;
   with_width(W, [&](auto w_) {
     constexpr int kW = decltype(w_)::value;
-    using H = __nv_bfloat16;
-    const auto fn = one ? (bf16 ? conv_step_kernel<H, kW, true> : conv_step_kernel<float, kW, true>)
-                        : (bf16 ? conv_step_kernel<H, kW, false> : conv_step_kernel<float, kW, false>);
+    auto pick = [&](auto act_, auto one_) {
+      constexpr bool kAct = decltype(act_)::value, kOne = decltype(one_)::value;
+      return bf16 ? conv_step_kernel<__nv_bfloat16, kW, kAct, kOne>
+                  : conv_step_kernel<float, kW, kAct, kOne>;
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    const auto fn = act ? (one ? pick(yes, yes) : pick(yes, no)) : (one ? pick(no, yes) : pick(no, no));
     fn<<<(unsigned)blocks, kConvThreads, 0, s>>>(a, static_cast<char*>(state), n_advance, T);
   });
   return cudaGetLastError();
