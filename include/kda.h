@@ -560,7 +560,11 @@ enum { KDA_SCAN_SOFTPLUS = 1u };
  *   cu_seqlens, n_seqs, batch, T  as kda_chunk_fwd's cu_seqlens, n_seqs, B, T; malformed offsets
  *            as kda_causal_conv_fwd.
  * Decays, states and sums are fp32, y is rounded once to `dtype`.  A sequence of length 0 gets
- * hT = h0 (or zeros).  No workspace.
+ * hT = h0 (or zeros).  No workspace.  Where there are few (sequence, channels) and sequences are
+ * long on average, each is cut into 4 or 8 segments that run at once (two where it is very long);
+ * the result equals the uncut one up to rounding and does not change from call to call.  Which form
+ * runs depends on the numbers of sequences, tokens and channels, not on the lengths or values.  A
+ * non-finite x, dt or z reaches outputs and states of its own channel and sequence only.
  */
 kda_status_t kda_selective_scan_fwd(const void* x, const void* dt, const float* A, const void* B,
                                     const void* C, int dtype, const float* D, const void* z,
