@@ -685,18 +685,16 @@ def linear_recurrent_multi_step(q, k, v, g, S, n_advance=None, *, scale: float =
     return o
 
 
-def _row_stride(t: torch.Tensor, name: str, tail: tuple, dtype=None, device=None) -> int:
+def _row_stride(t: torch.Tensor, name: str, tail: tuple, dtype, device) -> int:
     """Elements between the tokens of a [..., *tail] tensor whose tokens are contiguous in
     themselves and one stride apart (a slice of a packed projection has more elements a token
     than its own); ``t`` is checked on the way."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     shape, k = t.shape, len(tail)
     dims = len(shape)
     if dims <= k or shape[dims - k:] != tail:
@@ -722,6 +720,18 @@ def _row_stride(t: torch.Tensor, name: str, tail: tuple, dtype=None, device=None
     return row if step is None else step
 
 
+def _tokens(x, name):
+    """(shape, dtype, device, dtype code) of a call's first tensor, tokens of channels."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, dtype = x.shape, x.dtype
+    if len(shape) < 2:
+        raise ValueError(f"{name} must be [..., channels], got {tuple(shape)}")
+    return shape, dtype, x.device, _dtype_code(x)
+
+
 def _packed(lead, cu_seqlens, dev, name):
     """(N, B, T) of a prompt call whose tokens have the leading dimensions ``lead``."""
     if cu_seqlens is not None:
@@ -735,19 +745,19 @@ def _packed(lead, cu_seqlens, dev, name):
 
 
 def _conv_inputs(x, weight, bias):
-    """(row stride, C, W, dtype code) of a convolution's checked inputs."""
-    if not isinstance(x, torch.Tensor) or x.dim() < 2:
-        raise ValueError("x must be a tensor [..., C]")
-    C, dev = x.shape[-1], x.device
-    sx = _row_stride(x, "x", (C,))
+    """(row stride, shape, dtype, device, C, W, dtype code) of a convolution's checked inputs."""
+    shape, dtype, dev, code = _tokens(x, "x")
+    C = shape[-1]
+    sx = _row_stride(x, "x", (C,), dtype, dev)
     _need(weight, "weight", torch.float32, dev)
-    if weight.dim() != 2 or weight.shape[0] != C:
-        raise ValueError(f"weight must be [{C}, W], got {tuple(weight.shape)}")
+    ws = weight.shape
+    if len(ws) != 2 or ws[0] != C:
+        raise ValueError(f"weight must be [{C}, W], got {tuple(ws)}")
     if bias is not None:
         _need(bias, "bias", torch.float32, dev)
         if bias.shape != (C,):
             raise ValueError(f"bias must be [{C}], got {tuple(bias.shape)}")
-    return sx, C, weight.shape[1], _dtype_code(x)
+    return sx, shape, dtype, dev, C, ws[1], code
 
 
 def _rows_out(out, x, C):
@@ -773,13 +783,12 @@ def causal_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, silu: 
     Returns ``(y, final_state)``; final_state (None if not asked) is the state of
     :func:`causal_conv_step`.
     """
-    sx, C, W, dt = _conv_inputs(x, weight, bias)
-    dev = x.device
-    N, B, T = _packed(x.shape[:-1], cu_seqlens, dev, "x")
-    shape = (N, W - 1, C)
+    sx, shape, dtype, dev, C, W, dt = _conv_inputs(x, weight, bias)
+    N, B, T = _packed(shape[:-1], cu_seqlens, dev, "x")
+    kept = (N, W - 1, C)
     if state is not None:
-        _like(state, "state", shape, x.dtype, dev)
-    last = _like(final_state_out, "final_state_out", shape, x.dtype, dev) \
+        _like(state, "state", kept, dtype, dev)
+    last = _like(final_state_out, "final_state_out", kept, dtype, dev) \
         if output_final_state else None
     y, sy = _rows_out(out, x, C)
     _call(lib.kda_causal_conv_fwd, dev, x.data_ptr(), dt, weight.data_ptr(), _addr(bias),
@@ -791,11 +800,11 @@ def causal_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, *, silu: 
 def causal_conv_step(x, weight, state, bias=None, *, silu: bool = True, out=None):
     """One new token of :func:`causal_conv_fwd` for N sequences: x [N, C], state [N, W-1, C]
     updated in place.  Returns y [N, C]."""
-    sx, C, W, dt = _conv_inputs(x, weight, bias)
-    if x.dim() != 2:
-        raise ValueError(f"x must be [N, C], got {tuple(x.shape)}")
-    N, dev = x.shape[0], x.device
-    _like(state, "state", (N, W - 1, C), x.dtype, dev, given=True)
+    sx, shape, dtype, dev, C, W, dt = _conv_inputs(x, weight, bias)
+    if len(shape) != 2:
+        raise ValueError(f"x must be [N, C], got {tuple(shape)}")
+    N = shape[0]
+    _like(state, "state", (N, W - 1, C), dtype, dev, given=True)
     y, sy = _rows_out(out, x, C)
     _call(lib.kda_causal_conv_step, dev, x.data_ptr(), dt, weight.data_ptr(), _addr(bias),
           state.data_ptr(), y.data_ptr(), N, C, W, sx, sy, tail=(1 if silu else 0,))
@@ -815,11 +824,11 @@ def causal_conv_multi_step(x, weight, state, n_advance=None, bias=None, *, silu:
     """T <= 16 new tokens a sequence: x [N, T, C], state [N, W-1, C] left as it is behind the
     first n_advance[n] tokens (int32 [N] on the device; None = all T).  Returns y [N, T, C] (of
     all T tokens), or None when return_outputs is False."""
-    sx, C, W, dt = _conv_inputs(x, weight, bias)
-    if x.dim() != 3:
-        raise ValueError(f"x must be [N, T, C], got {tuple(x.shape)}")
-    N, T, dev = x.shape[0], x.shape[1], x.device
-    _like(state, "state", (N, W - 1, C), x.dtype, dev, given=True)
+    sx, shape, dtype, dev, C, W, dt = _conv_inputs(x, weight, bias)
+    if len(shape) != 3:
+        raise ValueError(f"x must be [N, T, C], got {tuple(shape)}")
+    N, T, _ = shape
+    _like(state, "state", (N, W - 1, C), dtype, dev, given=True)
     adv = _advance(n_advance, N, dev)
     y, sy = _rows_out(out, x, C) if return_outputs else (None, C)
     _call(lib.kda_causal_conv_multi_step, dev, x.data_ptr(), dt, weight.data_ptr(), _addr(bias),
@@ -828,35 +837,42 @@ def causal_conv_multi_step(x, weight, state, n_advance=None, bias=None, *, silu:
 
 
 def _scan_inputs(x, dt, A, B, C, D, z, dt_bias):
-    """(channels, states, groups, dtype code, strides of x, dt, B, C, z) of a scan's checked
-    inputs."""
-    if not isinstance(x, torch.Tensor) or x.dim() < 2:
-        raise ValueError("x must be a tensor [..., channels]")
-    shape, dev, dtype = x.shape, x.device, x.dtype
+    """(shape of x, device, channels, states, groups, dtype code, strides of x, dt, B, C, z) of a
+    scan's checked inputs."""
+    shape, dtype, dev, code = _tokens(x, "x")
     n, lead = shape[-1], shape[:-1]
     _need(A, "A", torch.float32, dev)
-    if A.dim() != 2 or A.shape[0] != n:
-        raise ValueError(f"A must be [{n}, states], got {tuple(A.shape)}")
-    S = A.shape[1]
+    As = A.shape
+    if len(As) != 2 or As[0] != n:
+        raise ValueError(f"A must be [{n}, states], got {tuple(As)}")
+    S = As[1]
     G = B.shape[-2] if isinstance(B, torch.Tensor) and B.dim() > 2 else 1
-    row, bc, whole = (n,), (G, S), lead + (n,)
-    sx = _row_stride(x, "x", row)
+    row, bc = (n,), (G, S)
+    sx = _row_stride(x, "x", row, dtype, dev)
     sdt = _row_stride(dt, "dt", row, dtype, dev)
     sB = _row_stride(B, "B", bc, dtype, dev)
     sC = _row_stride(C, "C", bc, dtype, dev)
-    sz = _row_stride(z, "z", row, dtype, dev) if z is not None else n
-    for name, t in (("dt", dt), ("z", z)):
-        if t is not None and t.shape != whole:
-            raise ValueError(f"{name} must be {tuple(whole)}, got {tuple(t.shape)}")
-    for name, t in (("B", B), ("C", C)):
-        if t.shape != lead + bc:
-            raise ValueError(f"{name} must be {tuple(lead + bc)}, got {tuple(t.shape)}")
-    for name, t in (("D", D), ("dt_bias", dt_bias)):
-        if t is not None:
-            _need(t, name, torch.float32, dev)
-            if t.shape != row:
-                raise ValueError(f"{name} must be [{n}], got {tuple(t.shape)}")
-    return n, S, G, _dtype_code(x), (sx, sdt, sB, sC, sz)
+    if dt.shape != shape:
+        raise ValueError(f"dt must be {tuple(shape)}, got {tuple(dt.shape)}")
+    whole = B.shape
+    if whole != lead + bc:
+        raise ValueError(f"B must be {tuple(lead + bc)}, got {tuple(whole)}")
+    if C.shape != whole:
+        raise ValueError(f"C must be {tuple(whole)}, got {tuple(C.shape)}")
+    sz = n
+    if z is not None:
+        sz = _row_stride(z, "z", row, dtype, dev)
+        if z.shape != shape:
+            raise ValueError(f"z must be {tuple(shape)}, got {tuple(z.shape)}")
+    if D is not None:
+        _need(D, "D", torch.float32, dev)
+        if D.shape != row:
+            raise ValueError(f"D must be [{n}], got {tuple(D.shape)}")
+    if dt_bias is not None:
+        _need(dt_bias, "dt_bias", torch.float32, dev)
+        if dt_bias.shape != row:
+            raise ValueError(f"dt_bias must be [{n}], got {tuple(dt_bias.shape)}")
+    return shape, dev, n, S, G, code, sx, sdt, sB, sC, sz
 
 
 def selective_scan_fwd(x, dt, A, B, C, h0=None, cu_seqlens=None, *, D=None, z=None, dt_bias=None,
@@ -873,9 +889,8 @@ def selective_scan_fwd(x, dt, A, B, C, h0=None, cu_seqlens=None, *, D=None, z=No
     [N, channels, states] or None.  ``out`` must not overlap an input; ``final_state_out`` may be
     h0.  Returns ``(y, hT)``; hT (None if not asked) is the h of :func:`selective_step`.
     """
-    n, S, G, code, (sx, sdt, sB, sC, sz) = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
-    dev = x.device
-    N, batch, T = _packed(x.shape[:-1], cu_seqlens, dev, "x")
+    shape, dev, n, S, G, code, sx, sdt, sB, sC, sz = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
+    N, batch, T = _packed(shape[:-1], cu_seqlens, dev, "x")
     if h0 is not None:
         _like(h0, "h0", (N, n, S), torch.float32, dev)
     hT = _like(final_state_out, "final_state_out", (N, n, S), torch.float32, dev) \
@@ -892,10 +907,10 @@ def selective_step(x, dt, A, B, C, h, *, D=None, z=None, dt_bias=None, softplus:
                    out=None):
     """One new token of :func:`selective_scan_fwd` for N sequences: x, dt, z [N, channels], B, C
     [N, groups, states], h fp32 [N, channels, states] updated in place.  Returns y [N, channels]."""
-    n, S, G, code, (sx, sdt, sB, sC, sz) = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
-    if x.dim() != 2:
-        raise ValueError(f"x must be [N, channels], got {tuple(x.shape)}")
-    N, dev = x.shape[0], x.device
+    shape, dev, n, S, G, code, sx, sdt, sB, sC, sz = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
+    if len(shape) != 2:
+        raise ValueError(f"x must be [N, channels], got {tuple(shape)}")
+    N = shape[0]
     _like(h, "h", (N, n, S), torch.float32, dev, given=True)
     y, sy = _rows_out(out, x, n)
     _call(lib.kda_selective_step, dev, x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
@@ -910,10 +925,10 @@ def selective_multi_step(x, dt, A, B, C, h, n_advance=None, *, D=None, z=None, d
     [N, channels, states] advanced in place by n_advance[n] tokens (int32 [N] on the device;
     None = all T).  Returns y [N, T, channels] (of all T tokens), or None when return_outputs is
     False."""
-    n, S, G, code, (sx, sdt, sB, sC, sz) = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
-    if x.dim() != 3:
-        raise ValueError(f"x must be [N, T, channels], got {tuple(x.shape)}")
-    N, T, dev = x.shape[0], x.shape[1], x.device
+    shape, dev, n, S, G, code, sx, sdt, sB, sC, sz = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
+    if len(shape) != 3:
+        raise ValueError(f"x must be [N, T, channels], got {tuple(shape)}")
+    N, T, _ = shape
     _like(h, "h", (N, n, S), torch.float32, dev, given=True)
     adv = _advance(n_advance, N, dev)
     y, sy = _rows_out(out, x, n) if return_outputs else (None, n)

@@ -205,6 +205,42 @@ def test_few_channels_of_long_sequences(kda, dtype, S, lens):
     assert none is None and torch.equal(y3, y)
 
 
+def test_cut_sequences_malformed_captured_and_with_non_finite_inputs(kda):
+    d = make([4500, 4700], 40, 16, 1, torch.bfloat16, seed=21, strong=0.05)
+    g = on_gpu(d)
+    args = (g["x"], g["dt"], g["A"], g["B"], g["C"], g["h0"])
+    more = dict(D=g["D"], z=g["z"], dt_bias=g["bias"])
+    y0, h0 = kda.selective_scan_fwd(*args, g["cu"], **more)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y1, h1 = kda.selective_scan_fwd(*args, g["cu"], **more)
+        y2, h2 = kda.selective_scan_fwd(*args[:5], h1, g["cu"], **more)
+    graph.replay()
+    y3, h3 = kda.selective_scan_fwd(*args[:5], h0, g["cu"], **more)
+    assert torch.equal(y0, y1) and torch.equal(h0, h1)
+    assert torch.equal(y2, y3) and torch.equal(h2, h3)
+    for cu in ([0, 9000, 4000], [7, 4500, 9200], [0, -5, 9200], [0, 2 ** 31 - 1, 9200]):
+        buf = torch.full((9200 + 64, 40), 7.0, dtype=torch.bfloat16, device="cuda")
+        kept = torch.full((4, 40, 16), 7.0, device="cuda")
+        kda.selective_scan_fwd(*args, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                               out=buf[32:-32], final_state_out=kept[1:3], **more)
+        with pytest.raises(kda.KdaError):
+            kda.get_device_error()
+        assert torch.all(buf[:32] == 7) and torch.all(buf[-32:] == 7)
+        assert torch.all(kept[0] == 7) and torch.all(kept[3] == 7)
+    bad = dict(d)
+    bad["xz"] = d["xz"].clone()
+    bad["xz"][1000, 5] = float("nan")
+    bad["xz"][6000, 7] = float("inf")
+    y4, h4 = scan(kda, bad)
+    same = torch.ones(9200, 40, dtype=torch.bool)
+    same[1000:4500, 5] = same[6000:, 7] = False
+    assert torch.equal(y4.cpu()[same], y0.cpu()[same]) and torch.isnan(h4[0, 5]).all()
+    keep = torch.ones(2, 40, dtype=torch.bool)
+    keep[0, 5] = keep[1, 7] = False
+    assert torch.equal(h4.cpu()[keep], h0.cpu()[keep])
+
+
 def test_results_do_not_depend_on_the_batch(kda):
     """A sequence alone, among others and twice: the same bits."""
     lens = [130, 0, 64, 777, 9]
