@@ -163,14 +163,20 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
   const int64_t tile = id / lanes;
   const int cv = (int)(id - tile * lanes);
   if (tile >= a.runs) return;
-  Span sp, after;
-  int64_t t = run_begin<kW>(a, tile * a.run, sp);
-  const int64_t stop = run_begin<kW>(a, min((tile + 1) * a.run, a.NT), after);
-  if (t >= stop) return;
-  Taps<T, kW> taps;
-  taps.load(a.w, a.b, cv);
   const char* x = a.x + kPiece * (int64_t)cv;
   char* y = a.y + kPiece * (int64_t)cv;
+  // The first rows and the taps are on their way while the run's sequence is looked up.
+  const int64_t guess = tile * a.run;
+#pragma unroll
+  for (int i = -K; i < kGroup; ++i)
+    if (guess + i >= 0 && guess + i < a.NT)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (guess + i) * a.sx));
+  Taps<T, kW> taps;
+  taps.load(a.w, a.b, cv);
+  Span sp, after;
+  int64_t t = run_begin<kW>(a, guess, sp);
+  const int64_t stop = run_begin<kW>(a, min(guess + a.run, a.NT), after);
+  if (t >= stop) return;
   const int64_t kept = (int64_t)a.C * sizeof(T);  // bytes of a kept row
   const Row<T> zero{};
   float2 win[K + kGroup][kPairs];
