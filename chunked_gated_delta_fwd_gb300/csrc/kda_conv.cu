@@ -6,10 +6,10 @@
 // Bound by HBM: x is read and y written once.  A lane holds four channels and
 // walks a run of tokens with the last W - 1 inputs in registers, so a run reads W - 1 rows more
 // than it has (from L2: its neighbour reads them as well).  Eight rows are on their way while eight
-// are worked on; products are packed pairs.  Sums are fp32, rounded once.  8192 tokens x 12288
-// channels, W = 4 with SiLU: bf16 81 us (5.0 TB/s; unpacking, products and the two special functions a
-// channel of SiLU take a third of the schedulers' turns each), fp32 127 to 132 us (6.1 TB/s); 512
-// single tokens of as many channels 24 us (4.2 TB/s), one 3.5 us.
+// are worked on, and the eight behind them on theirs to L2 (79 -> 70 us in the first case below);
+// products are packed pairs.  Sums are fp32, rounded once.  8192 tokens x 12288
+// channels, W = 4 with SiLU: bf16 67 us (6.0 TB/s), fp32 123 us (6.5 TB/s); 512 single tokens of as many
+// channels 21 us (4.8 TB/s), one 3.5 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -169,8 +169,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
   const int64_t guess = tile * a.run;
 #pragma unroll
   for (int i = -K; i < kGroup; ++i)
-    if (guess + i >= 0 && guess + i < a.NT)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (guess + i) * a.sx));
+    if (guess + i >= 0 && guess + i < a.NT) prefetch(x + (guess + i) * a.sx);
   Taps<T, kW> taps;
   taps.load(a.w, a.b, cv);
   Span sp, after;
@@ -186,6 +185,11 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
     if (left >= kGroup) {
 #pragma unroll
       for (int i = 0; i < kGroup; ++i, xr += a.sx) ahead[i] = *reinterpret_cast<const Row<T>*>(xr);
+      if (left >= 2 * kGroup) {
+        const char* p = xr;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i, p += a.sx) prefetch(p);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < kGroup - 1; ++i, xr += a.sx)
