@@ -85,6 +85,11 @@ struct Taps {
   }
 };
 
+// id / lanes, in 32 bits where they do.
+__device__ __forceinline__ int64_t quotient(int64_t id, int lanes) {
+  return (id >> 32) != 0 ? id / lanes : (int64_t)((uint32_t)id / (uint32_t)lanes);
+}
+
 struct ConvArgs {
   const char* x;
   char* y;
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
   }
   const int lanes = a.C / kVec;
   const int64_t id = (int64_t)(blockIdx.x - a.ends) * kConvThreads + threadIdx.x;
-  const int64_t tile = id / lanes;
+  const int64_t tile = quotient(id, lanes);
   const int cv = (int)(id - tile * lanes);
   if (tile >= a.runs) return;
   const char* x = a.x + kPiece * (int64_t)cv;
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(
   constexpr int kPiece = (int)sizeof(Row<T>);
   const int lanes = a.C / kVec, Tn = kOne ? 1 : T_;
   const int64_t id = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-  const int64_t n = id / lanes;
+  const int64_t n = quotient(id, lanes);
   if (n >= a.N) return;
   const int cv = (int)(id - n * lanes);
   const int64_t kept = (int64_t)a.C * sizeof(T);

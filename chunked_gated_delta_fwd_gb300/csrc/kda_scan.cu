@@ -191,9 +191,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
   const int blocks = (per_group + kCh - 1) / kCh;  // of a group
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();  // (of one CTA, uncut)
-  const int64_t unit = blockIdx.x / (kCut ? cluster.num_blocks() : 1);
-  const int n = (int)(unit / ((int64_t)blocks * a.G));
-  const int rest = (int)(unit - (int64_t)n * blocks * a.G);
+  const int unit = (int)blockIdx.x / (kCut ? (int)cluster.num_blocks() : 1);
+  const int n = unit / (blocks * a.G), rest = unit - n * (blocks * a.G);
   const int g = rest / blocks, first = (rest - g * blocks) * kCh;  // first channel in the group
   int64_t t0, t1;
   if (!seq_range(a, n, t0, t1) && threadIdx.x == 0 && err) atomicExch(err, kDevErrBadSeqlens);

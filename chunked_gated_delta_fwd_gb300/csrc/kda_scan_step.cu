@@ -27,12 +27,13 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
   const int Tn = kMulti ? (int)a.T : 1;
   const int per_group = a.C / a.G;
   const int blocks = (per_group * kLn + kStepThreads - 1) / kStepThreads;  // of a group
-  const int64_t bunch = blockIdx.x / ((int64_t)blocks * a.G);
-  const int block = (int)(blockIdx.x - bunch * blocks * a.G), g = block / blocks;
+  const int row_blocks = blocks * a.G;  // (the grid is a multiple of it)
+  const int bunch = (int)blockIdx.x / row_blocks;
+  const int block = (int)blockIdx.x - bunch * row_blocks, g = block / blocks;
   const int id = (block - g * blocks) * kStepThreads + threadIdx.x;
   const bool on = id < per_group * kLn;
   const int c = g * per_group + (on ? id / kLn : 0), sub = id % kLn;
-  const int64_t n0 = bunch * kSlots;
+  const int64_t n0 = (int64_t)bunch * kSlots;
   const int there = (int)min((int64_t)kSlots, a.N - n0);  // sequences
   const bool mine = on && sub < there;
   const int64_t n = n0 + (sub < there ? sub : 0);  // the sequence the lane looks after
