@@ -700,9 +700,11 @@ def _row_stride(t: torch.Tensor, name: str, tail: tuple, dtype, device) -> int:
     if dims <= k or shape[dims - k:] != tail:
         raise ValueError(f"{name} must be [..., {', '.join(map(str, tail))}], got {tuple(shape)}")
     row = tail[0] if k == 1 else tail[0] * tail[1]
+    stride = t.stride()
+    if dims == k + 1 and stride[-1] == 1 and (k == 1 or tail[0] == 1 or stride[1] == tail[1]):
+        return row if shape[0] == 1 else stride[0]  # (one leading dimension, most calls)
     if t.is_contiguous():
         return row
-    stride = t.stride()
     inner = 1
     for i in range(dims - 1, dims - 1 - k, -1):
         if stride[i] != inner and shape[i] > 1:
