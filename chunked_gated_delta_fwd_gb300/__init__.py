@@ -889,7 +889,8 @@ def selective_scan_fwd(x, dt, A, B, C, h0=None, cu_seqlens=None, *, D=None, z=No
     neighbours), bf16 or fp32; their tokens may be slices of packed projections.  A fp32
     [channels, states], D and dt_bias fp32 [channels] or None, z None for no gate.  h0 fp32
     [N, channels, states] or None.  ``out`` must not overlap an input; ``final_state_out`` may be
-    h0.  Returns ``(y, hT)``; hT (None if not asked) is the h of :func:`selective_step`.
+    h0.  Long sequences of few channels are cut into segments that run at once (the same result up
+    to rounding).  Returns ``(y, hT)``; hT (None if not asked) is the h of :func:`selective_step`.
     """
     shape, dev, n, S, G, code, sx, sdt, sB, sC, sz = _scan_inputs(x, dt, A, B, C, D, z, dt_bias)
     N, batch, T = _packed(shape[:-1], cu_seqlens, dev, "x")

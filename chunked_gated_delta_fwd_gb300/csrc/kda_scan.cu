@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
   const int64_t first_row = t0 + warp * kTok + row;
   const char* xp = static_cast<const char*>(a.x) + (first_row * a.sx + mine) * (int)sizeof(T);
   const char* dp = static_cast<const char*>(a.dt) + (first_row * a.sdt + mine) * (int)sizeof(T);
-  const char* zp = a.z ? static_cast<const char*>(a.z) + (first_row * a.sz + mine) * (int)sizeof(T) : nullptr;
+  const char* zp =
+      a.z ? static_cast<const char*>(a.z) + (first_row * a.sz + mine) * (int)sizeof(T) : nullptr;
   char* yp = static_cast<char*>(a.y) + (first_row * a.sy + mine) * (int)sizeof(T);
   const int brow = (lane & 15) / 2, bcol = kBc * (lane & 1);
   const int64_t sb = lane < 16 ? a.sB : a.sC;
@@ -364,6 +365,7 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
       const float2 none[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
       put_state(mine_seg.own, lane, none);
     }
+    __syncwarp();
     cluster.sync();
     if (warp == 0) {
       float2 h[4];

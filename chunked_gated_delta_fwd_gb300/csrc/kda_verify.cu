@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(
     __syncthreads();
     upto = warp_inclusive(lane < kVerifyWarps ? piece[lane] : 0, lane);  // over the CTA's pieces
     if (threadIdx.x == 31) cta_total = upto;
+    __syncwarp();
     cluster.sync();
     const uint64_t y = lane < ctas ? *cluster.map_shared_rank(&cta_total, lane) : 0;
     const uint64_t to_cta = warp_inclusive(y, lane);

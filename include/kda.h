@@ -553,8 +553,9 @@ enum { KDA_SCAN_SOFTPLUS = 1u };
  *   B, C     [NT] rows of groups x states elements of `dtype`; states 8, 16 or 32.
  *            Tokens of all of these are their own stride apart (at least a row, a multiple of 16
  *            bytes).  channels / groups is a multiple of 8.  y must not overlap an input.
- *   A        fp32 [channels][states], finite, <= 0 for decays; D, dt_bias fp32 [channels] or NULL
- *            (zeros).
+ *   A        fp32 [channels][states], finite; with delta >= 0, A <= 0 for decays.  (Growth is
+ *            computed as well; where the growth of some 8 tokens, or of a segment below, passes fp32's
+ *            range by itself, results are not finite.)  D, dt_bias fp32 [channels] or NULL (zeros).
  *   h0, hT   fp32 [N][channels][states], optional; hT may be h0.  hT continues as the h of the
  *            calls below.
  *   cu_seqlens, n_seqs, batch, T  as kda_chunk_fwd's cu_seqlens, n_seqs, B, T; malformed offsets

@@ -280,6 +280,23 @@ def test_non_finite_inputs_stay_in_their_channel_and_sequence(kda):
     keep = torch.ones(2, 48, dtype=torch.bool)
     keep[0, 5] = keep[1, 7] = False
     assert torch.equal(hT.cpu()[keep], hT2.cpu()[keep])
+    bad = dict(d, dt=d["dt"].clone())  # steps that are not numbers, or endless
+    bad["dt"][13, 3], bad["dt"][37, 4] = float("nan"), float("inf")
+    y3, hT3 = scan(kda, bad)
+    same = torch.ones(60, 48, dtype=torch.bool)
+    same[13:30, 3] = same[37:, 4] = False
+    assert torch.equal(y.cpu()[same], y3.cpu()[same]) and torch.isnan(y3[13:30, 3]).all()
+    keep = torch.ones(2, 48, dtype=torch.bool)
+    keep[0, 3] = keep[1, 4] = False
+    assert torch.equal(hT.cpu()[keep], hT3.cpu()[keep])
+
+
+def test_growing_states(kda):
+    """A above 0: the same bounds hold, the weights of old terms above 1."""
+    d = make([90, 33], 24, 16, 1, torch.float32, seed=22)
+    d["A"] = d["A"].abs() * 0.05
+    y, hT = scan(kda, d)
+    check(y, hT, d)
 
 
 def test_malformed_offsets_are_reported_and_stay_inside(kda):
