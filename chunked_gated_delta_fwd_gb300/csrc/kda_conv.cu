@@ -8,8 +8,8 @@
 // than it has (from L2: its neighbour reads them as well).  Eight rows are on their way while eight
 // are worked on, and the eight behind them on theirs to L2 (79 -> 70 us in the first case below);
 // products are packed pairs.  Sums are fp32, rounded once.  8192 tokens x 12288
-// channels, W = 4 with SiLU: bf16 67 us (6.0 TB/s), fp32 123 us (6.5 TB/s); 512 single tokens of as many
-// channels 21 us (4.8 TB/s), one 3.5 us.
+// channels, W = 4 with SiLU: bf16 65 us (6.2 TB/s), fp32 123 us (6.5 TB/s); 512 single tokens of as many
+// channels 21 us (4.8 TB/s), one 4.4 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -16,11 +16,11 @@
 // Bound by what the schedulers can issue: a state, token and channel takes 7 fp32 operations (4 in
 // the plain recurrence) and one exponential, a token and channel some 45 instructions for its step,
 // its gate and its copies, and packed operations, two at once, take two turns of the lanes that
-// integer instructions use too.  8192 tokens x 8192 channels of 16 states, bf16: 457 us, 117 ns a tile
-// and SM, 66% of the issue slots and 64% of the products' pipe (of the exponentials' 39%, HBM 15%);
-// 65536 x 2048: 893 us; fp32 8192 x 4096: 234 us.  The bare recurrence (4 operations, handed on behind
-// them) takes the same 456 us in the first case and 2.1 times as long for 2048 channels; scalar
-// instead of packed operations 557 us; products of the copied inputs in registers instead of shared
+// integer instructions use too.  8192 tokens x 8192 channels of 16 states, bf16: 452 to 460 us, 117 ns
+// a tile and SM, 66% of the issue slots and 64% of the products' pipe (39% of the exponentials', 15% of
+// HBM); 65536 x 2048: 889 us; fp32 8192 x 4096: 235 us.  The bare recurrence (4 operations, handed on
+// behind them) takes the same 456 us in the first case and 2.1 times as long with 2048 channels;
+// scalar instead of packed operations 557 us; inputs that wait in registers instead of shared
 // memory 680 us (a load in flight holds one of the few scoreboards that the code between needs).
 #include <cooperative_groups.h>
 

@@ -7,9 +7,9 @@
 // accesses, a warp's are contiguous) of S / 4 sequences at once, and S / 4 lanes share a channel:
 // each of them looks after one of the sequences (its step, its gate, its output, once a token
 // and channel), and the others get the step by a shuffle.  B and C of the sequences' tokens sit in
-// shared memory.  512 sequences x 8192 channels of 16 states, one token: 92 to 97 us, 6.0 TB/s (195 us
-// with one sequence a lane, whose four lanes each formed the step); 5 tokens of 96 x 4096: 29.5 us,
-// where the tokens (3.1 us each) bound it, by what the schedulers can issue.
+// shared memory.  512 sequences x 8192 channels of 16 states, one token: 90 us, 6.3 TB/s (195 us with
+// one sequence a lane, whose four lanes each formed the step); 5 tokens of 96 x 4096: 24 to 26 us, where
+// the tokens (3.1 us each) bound it, by what the schedulers can issue (71% of their slots).
 #include "kda_internal.cuh"
 #include "kda_scan.cuh"
 

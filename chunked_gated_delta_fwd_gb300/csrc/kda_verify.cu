@@ -15,7 +15,8 @@
 //
 // Bound by HBM for large batches (one row of p, one of q where a token was rejected) and by its
 // chain of loads for small ones: drafted token -> its probabilities -> rows -> search.  128 rows of
-// 163840: fp32 31 us (4.8 TB/s of the rows it needs), bf16 21 us; one row of 32000: 6 us, of 163840: 8.
+// 163840: fp32 31 to 35 us (4.3 to 4.8 TB/s of the rows it needs), bf16 21 us; one row of 32000: 6 us,
+// of 163840: 8.
 #include <cooperative_groups.h>
 
 #include "kda_internal.cuh"
