@@ -15,8 +15,9 @@
 //
 // Bound by HBM for large batches (one row of p, one of q where a token was rejected) and by its
 // chain of loads for small ones: drafted token -> its probabilities -> rows -> search.  128 rows of
-// 163840: fp32 31 to 35 us (4.3 to 4.8 TB/s of the rows it needs), bf16 21 us; one row of 32000: 6 us,
-// of 163840: 8.
+// 163840: fp32 31 to 35 us (4.3 to 4.8 TB/s of the rows it needs), bf16 21 us; of 163841, whose rows
+// begin anywhere, token by token: 35 and 32 us (42 and 40 with 4 loads in flight); one row of 32000:
+// 6 us, of 163840: 8.
 #include <cooperative_groups.h>
 
 #include "kda_internal.cuh"
@@ -117,7 +118,9 @@ __device__ __forceinline__ uint64_t exclusive(uint64_t upto, int i) {
 template <typename T, bool kVec, bool kQ>
 __device__ __forceinline__ uint64_t lane_sum(const T* p, const T* q, int64_t begin, int64_t end,
                                              int lane) {
-  constexpr int kN = kVec ? 16 / (int)sizeof(T) : 1, kAhead = kN == 8 ? 2 : 4;  // pieces of a lane in flight
+  constexpr int kN = kVec ? 16 / (int)sizeof(T) : 1;
+  // Loads of a lane in flight: 16 tokens; 8 of fp32 one by one (whose registers are as many).
+  constexpr int kAhead = kVec || sizeof(T) == 2 ? 16 / kN : 8;
   uint64_t sum = 0;
   for (int64_t v0 = begin; v0 < end; v0 += 32 * kN * kAhead) {
     float x[kAhead][kN], y[kAhead][kN];
