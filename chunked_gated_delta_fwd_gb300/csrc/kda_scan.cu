@@ -16,12 +16,13 @@
 // Bound by what the schedulers can issue: a state, token and channel takes 7 fp32 operations (4 in
 // the plain recurrence) and one exponential, a token and channel some 45 instructions for its step,
 // its gate and its copies, and packed operations, two at once, take two turns of the lanes that
-// integer instructions use too.  8192 tokens x 8192 channels of 16 states, bf16: 452 to 460 us, 117 ns
-// a tile and SM, 66% of the issue slots and 64% of the products' pipe (39% of the exponentials', 15% of
-// HBM); 65536 x 2048: 889 us; fp32 8192 x 4096: 235 us.  The bare recurrence (4 operations, handed on
-// behind them) takes the same 456 us in the first case and 2.1 times as long with 2048 channels;
-// scalar instead of packed operations 557 us; inputs that wait in registers instead of shared
-// memory 680 us (a load in flight holds one of the few scoreboards that the code between needs).
+// integer instructions use too.  8192 tokens x 8192 channels of 16 states, bf16: 418 us, 117 ns a tile
+// and SM, 67% of the issue slots (38% of the exponentials', 19% of HBM); 65536 x 2048: 889 us; fp32 8192 x
+// 4096: 235 us.  In the first case with a CTA a unit (452 us, 111 ns a tile, four rounds instead of three
+// and a half): the bare recurrence (4 operations, handed on behind them) 456 us, and 2.1 times as long
+// with 2048 channels; scalar instead of packed operations 557 us; inputs that wait in registers instead
+// of shared memory 680 us (a load in flight holds one of the few scoreboards that the code between
+// needs).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -33,7 +34,19 @@
 namespace kda {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kTok = 8;  // tokens of a tile
+
+// The halves of a cluster's barrier.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 
 __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -174,14 +187,19 @@ struct Segment {
   float time[256 / kS];
 };
 
-// kWarps: of a ring, 12 of them an SM in one CTA or in three of 4.  kCut: the CTAs of a cluster take
-// a segment of the sequence each, two passes over it: what it does to a state, then, from the state
-// that the segments before it leave, the scan.
-template <typename T, int kS, int kWarps, bool kCut>
-__global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const ScanArgs a, int* err) {
+// How the work is drawn: a unit (some neighbouring channels of one sequence) a CTA; or the CTAs of a
+// cluster take a segment of its sequence each, two passes over it: what it does to a state, then, from
+// the state that the segments before it leave, the scan; or two CTAs share several units.
+enum How { kUnits, kSegments, kPairs };
+enum Piece { kWhole, kFirstHalf, kSecondHalf };  // of a unit
+
+// A unit (or what of it is this CTA's) by a ring of kWarps.
+template <typename T, int kS, int kWarps, How kHow>
+__device__ __forceinline__ void scan_unit(const ScanArgs& a, int* err, char* smem, int unit,
+                                          Piece piece) {
   using W = ScanWarp<T, kS>;
+  constexpr bool kCut = kHow == kSegments, kPair = kHow == kPairs;
   constexpr int kLn = W::kLn, kCh = W::kCh, kVec = W::kVec, kBc = kS / 2;
-  extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   W& w = reinterpret_cast<W*>(smem)[warp];
   const int from = (warp + kWarps - 1) % kWarps;
@@ -189,9 +207,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
 
   const int per_group = a.C / a.G;
   const int blocks = (per_group + kCh - 1) / kCh;  // of a group
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();  // (of one CTA, uncut)
-  const int unit = (int)blockIdx.x / (kCut ? (int)cluster.num_blocks() : 1);
+  cg::cluster_group cluster = cg::this_cluster();  // (of one CTA, a unit a CTA)
+  __shared__ float4 enter[2][32];                  // the state that comes from another CTA
   const int n = unit / (blocks * a.G), rest = unit - n * (blocks * a.G);
   const int g = rest / blocks, first = (rest - g * blocks) * kCh;  // first channel in the group
   int64_t t0, t1;
@@ -215,13 +232,25 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
     t0 = min(t1, t0 + cluster.block_rank() * part);
     t1 = min(t1, t0 + part);
   }
+  if constexpr (kPair) {
+    const int64_t middle = t0 + (t1 - t0 + kTok - 1) / kTok / 2 * kTok;
+    if (piece == kFirstHalf) t1 = middle;
+    if (piece == kSecondHalf) t0 = middle;
+  }
   const int len = (int)(t1 - t0), tiles = (len + kTok - 1) / kTok;
   if constexpr (!kCut) {
-    if (tiles == 0 && warp == 0 && a.hT && on) {
+    if (tiles == 0 && warp == 0) {  // (of halves the first one, or both)
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = a.h0 ? a.h0[at + i] : 0.f;
-      store8(a.hT + at, v);
+      if (kPair && piece == kFirstHalf) {
+        float2 h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = make_float2(v[2 * i], v[2 * i + 1]);
+        put_state(cluster.map_shared_rank(enter, 1), lane, h);
+      } else if (a.hT && on) {
+        store8(a.hT + at, v);
+      }
     }
     if (warp >= tiles) return;
   }
@@ -287,7 +316,6 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
   };
   // The state that comes in from outside, and what leaves at the end (of an uncut sequence at once).
   __shared__ Segment<kS> mine_seg;
-  __shared__ float4 enter[2][32];
   __shared__ float times[kWarps][kCh];
   float last[8];
   bool ends = false;
@@ -389,8 +417,7 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
         get_last(h, last);
       }
     }
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // outside and segments are read
+    cluster_arrive();  // outside and segments are read
   }
   if (!kCut || warp < tiles) {
     start();
@@ -433,6 +460,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
         get_state(before.state, lane, h);
       } else if constexpr (kCut) {
         get_state(enter, lane, h);
+      } else if (kPair && piece == kSecondHalf) {
+        get_state(enter, lane, h);
       } else {
         outside(h);
       }
@@ -445,6 +474,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
         get_last(own, last);
         if constexpr (kCut)
           ends = cluster.block_rank() + 1 == cluster.num_blocks();
+        else if (kPair && piece == kFirstHalf)
+          put_state(cluster.map_shared_rank(enter, 1), lane, own);
         else if (a.hT && on)
           store8(a.hT + at, last);
       }
@@ -490,16 +521,52 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const Sc
     }
   }
   if constexpr (kCut) {
-    __syncwarp();
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    cluster_wait();
     if (ends && a.hT && on) store8(a.hT + at, last);  // (hT may be h0)
   }
 }
 
-template <typename T, int kS, int kWarps, bool kCut>
+// kWarps: 12 of them an SM in one CTA or in three of 4.
+template <typename T, int kS, int kWarps, How kHow>
+__global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) scan_kernel(const ScanArgs a, int* err) {
+  extern __shared__ __align__(16) char smem[];
+  if constexpr (kHow != kPairs) {
+    const int ctas = kHow == kSegments ? (int)cg::this_cluster().num_blocks() : 1;
+    scan_unit<T, kS, kWarps, kHow>(a, err, smem, (int)blockIdx.x / ctas, kWhole);
+  } else {
+    // Every so many-th unit is a pair's (neighbours run at the same time: their rows lie beside each
+    // other), the first half of them the first CTA's and the rest the second's; the middle one of
+    // an odd number is cut: the first CTA begins with its half, the second ends with its own, for
+    // which the state has long been there.
+    constexpr int kCh = ScanWarp<T, kS>::kCh;
+    const int units = a.N * a.G * ((a.C / a.G + kCh - 1) / kCh);
+    const int pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2, rank = (int)blockIdx.x % 2;
+    const int count = units / pairs + (pair < units % pairs), pieces = (count + 1) / 2;
+    const int first = pair + pairs * (rank * (count / 2));
+    cg::this_cluster().sync();  // the other CTA is there
+    const bool odd = count % 2 != 0, gives = odd && rank == 0;
+    if (!gives) cluster_arrive();
+#pragma unroll 1
+    for (int i = 0; i < pieces; ++i) {
+      Piece piece = kWhole;
+      if (gives && i == 0) piece = kFirstHalf;
+      if (odd && rank == 1 && i + 1 == pieces) {
+        cluster_wait();  // the state is there
+        piece = kSecondHalf;
+      }
+      const int unit = first + pairs * ((rank == 0 ? i + pieces - 1 : i + 1) % pieces);
+      scan_unit<T, kS, kWarps, kHow>(a, err, smem, unit, piece);
+      __syncthreads();  // the ring is at rest
+      if (gives && i == 0) cluster_arrive();
+    }
+    if (!odd || rank == 0) cluster_wait();
+  }
+}
+
+template <typename T, int kS, int kWarps, How kHow>
 cudaError_t launch_scan_t(const ScanArgs& a, unsigned units, int ctas, int* err, cudaStream_t s) {
   constexpr size_t smem = kWarps * sizeof(ScanWarp<T, kS>);
-  const auto kernel = scan_kernel<T, kS, kWarps, kCut>;
+  const auto kernel = scan_kernel<T, kS, kWarps, kHow>;
   static std::atomic<uint64_t> told{0};  // devices that know how much shared memory this takes
   int dev = 0;
   cudaGetDevice(&dev);
@@ -520,7 +587,7 @@ cudaError_t launch_scan_t(const ScanArgs& a, unsigned units, int ctas, int* err,
   at.val.clusterDim.x = (unsigned)ctas;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   c.attrs = &at;
-  c.numAttrs = kCut ? 1 : 0;
+  c.numAttrs = kHow == kUnits ? 0 : 1;
   return cudaLaunchKernelEx(&c, kernel, a, err);
 }
 
@@ -535,11 +602,11 @@ int sm_count() {
 // 117 ns a tile, one of 4 takes 200 alone, 265 beside another and 330 beside two (S = 16; the ratios
 // are about the same for 8 and 32), and a CTA some 3 us to begin and end, which others cover where
 // there are any.  (512 units of 1024 tiles: 460 against 530 us; 4096 of 64: 279 against 220.)
-bool short_rings(int64_t units, int64_t tiles, int sms) {
+bool short_rings(int64_t units, int64_t tiles, int sms, double rounds_of_12) {
   const double t = (double)tiles, one = t * 0.117 + 3;
   const int64_t rounds = units / (3 * sms), rest = units - rounds * 3 * sms;
   const double last = rest == 0 ? 0 : (rest > 2 * sms ? 0.33 : rest > sms ? 0.265 : 0.2) * t + 3;
-  return rounds * (t * 0.33 + 1) + last < (double)((units + sms - 1) / sms) * one;
+  return rounds * (t * 0.33 + 1) + last < rounds_of_12 * one;
 }
 
 }  // namespace
@@ -558,16 +625,23 @@ cudaError_t launch_scan(const ScanArgs& a, int bf16, int S, int* err, cudaStream
   int cut = 1;
   while (cut < 8 && units * cut * 2 <= sms && tiles >= 128 * cut) cut *= 2;
   if (cut == 2 && tiles < 512) cut = 1;
-  const bool four = cut == 1 && short_rings(units, tiles, sms);
+  // Rounds of rings of 12, and those that pairs of CTAs take, which can end on half a unit (8192
+  // tokens x 8192 channels 452 -> 418 us, 4096 x 2560 119 -> 96, 2048 x 5120 97 -> 84).
+  const int64_t pairs = sms / 2, alone = (units + sms - 1) / sms;
+  const double paired = 0.5 * (double)((units + pairs - 1) / pairs);
+  const bool pair = cut == 1 && (!a.cu || a.N == 1) && units > sms && paired < alone;
+  const bool four = cut == 1 && short_rings(units, tiles, sms, pair ? paired : alone);
   cudaError_t e = cudaSuccess;
   with_states(S, [&](auto k) {
     constexpr int kS = decltype(k)::value;
     using H = __nv_bfloat16;
     const auto fn =
-        cut > 1 ? (bf16 ? launch_scan_t<H, kS, 12, true> : launch_scan_t<float, kS, 12, true>)
-        : four  ? (bf16 ? launch_scan_t<H, kS, 4, false> : launch_scan_t<float, kS, 4, false>)
-                : (bf16 ? launch_scan_t<H, kS, 12, false> : launch_scan_t<float, kS, 12, false>);
-    e = fn(a, (unsigned)units, cut, err, s);
+        cut > 1 ? (bf16 ? launch_scan_t<H, kS, 12, kSegments> : launch_scan_t<float, kS, 12, kSegments>)
+        : four  ? (bf16 ? launch_scan_t<H, kS, 4, kUnits> : launch_scan_t<float, kS, 4, kUnits>)
+        : pair  ? (bf16 ? launch_scan_t<H, kS, 12, kPairs> : launch_scan_t<float, kS, 12, kPairs>)
+                : (bf16 ? launch_scan_t<H, kS, 12, kUnits> : launch_scan_t<float, kS, 12, kUnits>);
+    const bool two = pair && !four;
+    e = fn(a, (unsigned)(two ? pairs : units), two ? 2 : cut, err, s);
   });
   return e;
 }

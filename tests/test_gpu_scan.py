@@ -241,6 +241,67 @@ def test_cut_sequences_malformed_captured_and_with_non_finite_inputs(kda):
     assert torch.equal(h4.cpu()[keep], h0.cpu()[keep])
 
 
+@pytest.mark.parametrize("dtype", DT, ids=IDS)
+@pytest.mark.parametrize("S,N,ch,G,T", [(16, 1, 2560, 1, 401), (16, 5, 512, 2, 400), (8, 1, 4872, 1, 392),
+                                        (32, 1, 1280, 1, 399), (16, 1, 4960, 1, 1600)])
+def test_more_channels_than_run_at_once(kda, dtype, S, N, ch, G, T):
+    """Channels for more than one and less than two (or more than two and less than three) rounds
+    over the SMs, whose last ones are shared by two CTAs: odd and even tiles, in place, captured,
+    and the same bits as a part of the channels alone."""
+    d = make([T] * N, ch, S, G, dtype, seed=ch + T, strong=0.05)
+    if N == 1:
+        y, hT = scan(kda, d)  # packed, one sequence
+    g = on_gpu(d)
+    v = lambda t: t.unflatten(0, (N, T))  # noqa: E731
+    h = g["h0"].clone()
+    args = (v(g["x"]), v(g["dt"]), g["A"], v(g["B"]), v(g["C"]))
+    more = dict(D=g["D"], z=v(g["z"]), dt_bias=g["bias"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y2, _ = kda.selective_scan_fwd(*args, h, final_state_out=h, **more)
+        y3, h3 = kda.selective_scan_fwd(*args, h, **more)
+    graph.replay()
+    check(y2, h, d)
+    y4, h4 = kda.selective_scan_fwd(*args, h, **more)
+    assert torch.equal(y3, y4) and torch.equal(h3, h4)
+    if N == 1:
+        assert torch.equal(y, y2[0]) and torch.equal(hT, h)
+        part = ch // 16 * 8
+        some = [t[..., :part] for t in args[:2]] + [g["A"][:part]] + list(args[3:])
+        y5, h5 = kda.selective_scan_fwd(*some, g["h0"][:, :part].contiguous(), D=g["D"][:part],
+                                        z=more["z"][..., :part], dt_bias=g["bias"][:part])
+        assert torch.equal(y5, y2[..., :part]) and torch.equal(h5, h[:, :part])
+
+
+def test_shared_channels_malformed_and_with_non_finite_inputs(kda):
+    d = make([400], 2560, 16, 1, torch.bfloat16, seed=23, strong=0.05)
+    g = on_gpu(d)
+    args = (g["x"], g["dt"], g["A"], g["B"], g["C"], g["h0"])
+    more = dict(D=g["D"], z=g["z"], dt_bias=g["bias"])
+    y0, h0 = scan(kda, d)
+    for cu in ([0, 399], [7, 400], [400, 400], [0, 7], [0, 2 ** 31 - 1], [300, -1]):
+        buf = torch.full((400 + 64, 2560), 7.0, dtype=torch.bfloat16, device="cuda")
+        kept = torch.full((3, 2560, 16), 7.0, device="cuda")
+        kda.selective_scan_fwd(*args, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                               out=buf[32:-32], final_state_out=kept[1:2], **more)
+        with pytest.raises(kda.KdaError):
+            kda.get_device_error()
+        assert torch.all(buf[:32] == 7) and torch.all(buf[-32:] == 7)
+        assert torch.all(kept[0] == 7) and torch.all(kept[2] == 7)
+        if cu in ([400, 400], [300, -1]):  # no tokens: the state as it came
+            assert torch.equal(kept[1:2], g["h0"])
+    bad = dict(d)
+    bad["xz"] = d["xz"].clone()
+    bad["xz"][100, 5::160] = float("nan")  # of one unit in ten
+    y1, h1 = scan(kda, bad)
+    same = torch.ones(400, 2560, dtype=torch.bool)
+    same[100:, 5::160] = False
+    assert torch.equal(y1.cpu()[same], y0.cpu()[same]) and torch.isnan(h1[0, 5::160]).all()
+    keep = torch.ones(2560, dtype=torch.bool)
+    keep[5::160] = False
+    assert torch.equal(h1[0].cpu()[keep], h0[0].cpu()[keep])
+
+
 def test_results_do_not_depend_on_the_batch(kda):
     """A sequence alone, among others and twice: the same bits."""
     lens = [130, 0, 64, 777, 9]
