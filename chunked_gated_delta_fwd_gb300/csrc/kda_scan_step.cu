@@ -3,13 +3,15 @@
 // n_advance, the outputs of all T written):
 //     h <- exp(delta_t A) h + delta_t x_t B_t,   y_t = (C_t . h + D x_t) SiLU(z_t)
 //
-// Bound by HBM: 8 bytes a state and call.  A lane holds four states of a channel (16-byte
-// accesses, a warp's are contiguous) of S / 4 sequences at once, and S / 4 lanes share a channel:
-// each of them looks after one of the sequences (its step, its gate, its output, once a token
+// Bound by HBM: 8 bytes a state and call.  A lane holds eight states of a channel (two 16-byte
+// accesses, S / 8 lanes side by side in each) of S / 8 sequences at once, and S / 8 lanes share a
+// channel: each of them looks after one of the sequences (its step, its gate, its output, once a token
 // and channel), and the others get the step by a shuffle.  B and C of the sequences' tokens sit in
-// shared memory.  512 sequences x 8192 channels of 16 states, one token: 90 us, 6.3 TB/s (195 us with
-// one sequence a lane, whose four lanes each formed the step); 5 tokens of 96 x 4096: 24 to 26 us, where
-// the tokens (3.1 us each) bound it, by what the schedulers can issue (71% of their slots).
+// shared memory.  512 sequences x 8192 channels of 16 states, one token: 86 to 91 us, 6.3 TB/s (195 us
+// with one sequence a lane, whose lanes each formed the step; 97 with four states a lane and four
+// sequences; 118 with sixteen and 114 with two channels of one sequence a lane, whose accesses reach
+// into more lines at once); 5 tokens of 96 x 4096: 21 to 24 us (24 to 28 with four states a lane), where
+// the tokens (2.6 us each, 3.1) bound it, by what the schedulers can issue.
 #include "kda_internal.cuh"
 #include "kda_scan.cuh"
 
@@ -21,7 +23,7 @@ constexpr int kStepThreads = 128;
 template <typename T, int kS, bool kMulti>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
     const ScanArgs a, float* __restrict__ state, const int32_t* __restrict__ n_advance) {
-  constexpr int kLn = kS / 4, kSlots = kLn, kT = kMulti ? 16 : 1;
+  constexpr int kQ = 2, kLn = kS / 4 / kQ, kSlots = kLn, kT = kMulti ? 16 : 1;
   constexpr unsigned kAll = 0xffffffffu;
   __shared__ __align__(16) float BC[2][kSlots * kT][kS];  // rows as in memory: Tn a sequence
   const int Tn = kMulti ? (int)a.T : 1;
@@ -38,16 +40,15 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
   const bool mine = on && sub < there;
   const int64_t n = n0 + (sub < there ? sub : 0);  // the sequence the lane looks after
 
-  float4* at = reinterpret_cast<float4*>(state) + (n0 * a.C + c) * kLn + sub;
-  const int64_t hop = (int64_t)a.C * kLn;
-  float h[kSlots][4];
+  float4* at = reinterpret_cast<float4*>(state) + (n0 * a.C + c) * (kS / 4) + sub;
+  const int64_t hop = (int64_t)a.C * (kS / 4);
+  float h[kSlots][kQ][4];
 #pragma unroll
   for (int i = 0; i < kSlots; ++i)
-    if (on && i < there) {
-      const float4 v = __ldcs(at + i * hop);
-      h[i][0] = v.x; h[i][1] = v.y; h[i][2] = v.z; h[i][3] = v.w;
-    } else {
-      h[i][0] = h[i][1] = h[i][2] = h[i][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kQ; ++j) {
+      const float4 v = on && i < there ? __ldcs(at + i * hop + j * kLn) : make_float4(0.f, 0.f, 0.f, 0.f);
+      h[i][j][0] = v.x; h[i][j][1] = v.y; h[i][j][2] = v.z; h[i][j][3] = v.w;
     }
   const T* xp = static_cast<const T*>(a.x) + n * Tn * a.sx + c;
   const T* dp = static_cast<const T*>(a.dt) + n * Tn * a.sdt + c;
@@ -60,18 +61,21 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
     if (zp) rz = *zp;
   };
   fetch();
-  for (int e = threadIdx.x; e < 2 * there * Tn * kLn; e += kStepThreads) {
-    const int q = 4 * (e % kLn), which = e / kLn % 2, r = e / (2 * kLn);
+  for (int e = threadIdx.x; e < 2 * there * Tn * (kS / 4); e += kStepThreads) {
+    const int q = 4 * (e % (kS / 4)), which = e / (kS / 4) % 2, r = e / (kS / 2);
     const T* src = which ? static_cast<const T*>(a.Cm) + (n0 * Tn + r) * a.sC
                          : static_cast<const T*>(a.B) + (n0 * Tn + r) * a.sB;
     float v[4];
     load4(src + g * kS + q, v);
     store4(&BC[which][r][q], v);
   }
-  float A[4];
-  load4(a.A + (int64_t)c * kS + 4 * sub, A);
+  float A[kQ][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] *= kLog2e;
+  for (int j = 0; j < kQ; ++j) {
+    load4(a.A + (int64_t)c * kS + 4 * (sub + kLn * j), A[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) A[j][i] *= kLog2e;
+  }
   const float bias = a.bias ? __ldg(a.bias + c) : 0.f, skip = a.D ? __ldg(a.D + c) : 0.f;
   int adv = Tn;
   if (kMulti && n_advance) {
@@ -101,15 +105,20 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       const float di = __shfl_sync(kAll, d, i, kLn), dxi = __shfl_sync(kAll, dx, i, kLn);
-      const float4 b = *reinterpret_cast<const float4*>(&BC[0][i * Tn + t][4 * sub]);
-      const float4 k = *reinterpret_cast<const float4*>(&BC[1][i * Tn + t][4 * sub]);
-      h[i][0] = fmaf(ex2(di * A[0]), h[i][0], dxi * b.x);
-      h[i][1] = fmaf(ex2(di * A[1]), h[i][1], dxi * b.y);
-      h[i][2] = fmaf(ex2(di * A[2]), h[i][2], dxi * b.z);
-      h[i][3] = fmaf(ex2(di * A[3]), h[i][3], dxi * b.w);
-      acc[i] = fmaf(k.x, h[i][0], fmaf(k.y, h[i][1], fmaf(k.z, h[i][2], k.w * h[i][3])));
-      if (t + 1 == stop[i])
-        __stcs(at + i * hop, make_float4(h[i][0], h[i][1], h[i][2], h[i][3]));
+      acc[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kQ; ++j) {
+        const int q = 4 * (sub + kLn * j);
+        const float4 b = *reinterpret_cast<const float4*>(&BC[0][i * Tn + t][q]);
+        const float4 k = *reinterpret_cast<const float4*>(&BC[1][i * Tn + t][q]);
+        float (&s)[4] = h[i][j];
+        s[0] = fmaf(ex2(di * A[j][0]), s[0], dxi * b.x);
+        s[1] = fmaf(ex2(di * A[j][1]), s[1], dxi * b.y);
+        s[2] = fmaf(ex2(di * A[j][2]), s[2], dxi * b.z);
+        s[3] = fmaf(ex2(di * A[j][3]), s[3], dxi * b.w);
+        acc[i] = fmaf(k.x, s[0], fmaf(k.y, s[1], fmaf(k.z, s[2], fmaf(k.w, s[3], acc[i]))));
+        if (t + 1 == stop[i]) __stcs(at + i * hop + j * kLn, make_float4(s[0], s[1], s[2], s[3]));
+      }
     }
     if (!yp) continue;
     // halving exchange inside a channel's lanes: lane sub ends with sequence sub
@@ -133,7 +142,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(
 
 cudaError_t launch_scan_step(const ScanArgs& a, int bf16, int S, float* state,
                              const int32_t* n_advance, bool multi, cudaStream_t s) {
-  const int lanes = S / 4;
+  const int lanes = S / 8;
   const int64_t blocks = (int64_t)a.G * (((int64_t)a.C / a.G * lanes + kStepThreads - 1) / kStepThreads);
   const int64_t grid = blocks * (((int64_t)a.N + lanes - 1) / lanes);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
