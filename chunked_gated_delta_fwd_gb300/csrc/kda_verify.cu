@@ -34,13 +34,14 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // A weight w in [0, 1] as a whole number of 2^-56, the rest cut off, in three parts of 23, 23 and
 // 10 bits: w + 1 rounded down holds floor(2^23 w) in its low bits, and what is left of w, 2^23
-// times as large, is taken the same way.  Every step is exact but for the cutting.  (In packed fp32
+// times as large, is taken the same way; what then is left, r < 2^-23, meets 2^-10, whose last bit
+// is 2^-33: floor(2^33 r).  Every step is exact but for the cutting.  (In packed fp32
 // and 32-bit sums: a conversion to 64 bits takes a clock an SM, 74 us for 128 rows of 163840 whose
 // traffic takes 22; shifts of 64 bits 44 us.)
 struct Parts {
   uint32_t hi, mid, lo;  // sums of the parts with the exponent's bits of what held them
 };
-constexpr uint32_t kOne = 0x3f800000u, k8192 = 0x46000000u;  // 1.f, and 8192.f, whose last bit is 2^-10
+constexpr uint32_t kOne = 0x3f800000u, kLast = 0x3a800000u;  // 1.f and 2^-10
 __device__ __forceinline__ void add_pair(Parts& s, float w0, float w1) {
   const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
   const float2 scale = make_float2(0x1p23f, 0x1p23f), neg = make_float2(-0x1p23f, -0x1p23f);
@@ -50,7 +51,7 @@ __device__ __forceinline__ void add_pair(Parts& s, float w0, float w1) {
   const float2 r1 = __ffma2_rn(__fadd2_rn(t1, minus), neg, __fmul2_rn(w, scale));
   const float2 t2 = __fadd2_rz(r1, one);
   const float2 r2 = __ffma2_rn(__fadd2_rn(t2, minus), minus, r1);
-  const float2 t3 = __fadd2_rz(r2, make_float2(8192.f, 8192.f));
+  const float2 t3 = __fadd2_rz(r2, make_float2(0x1p-10f, 0x1p-10f));
   s.hi += __float_as_uint(t1.x) + __float_as_uint(t1.y);
   s.mid += __float_as_uint(t2.x) + __float_as_uint(t2.y);
   s.lo += __float_as_uint(t3.x) + __float_as_uint(t3.y);
@@ -58,7 +59,7 @@ __device__ __forceinline__ void add_pair(Parts& s, float w0, float w1) {
 // The sum of n <= 511 weights added up in s.
 __device__ __forceinline__ uint64_t total_of(const Parts& s, uint32_t n) {
   return ((uint64_t)(s.hi - n * kOne) << 33) + ((uint64_t)(s.mid - n * kOne) << 10) +
-         (s.lo - n * k8192);
+         (s.lo - n * kLast);
 }
 __device__ __forceinline__ uint64_t units_of(float w) {
   Parts s{0, 0, 0};
