@@ -1038,6 +1038,9 @@ kda_status_t kda_causal_conv_fwd(const void* x, int dtype, const float* weight, 
   kda_status_t st = conv_shape(fn, dtype, C, W, flags);
   if (st == KDA_OK) st = packed_counts(fn, cu_seqlens, n_seqs, B, T, &N, &NT);
   if (st != KDA_OK) return st;
+  // (the kernel's search over the offsets and its walk over sequences without tokens count in 32 bits)
+  if ((cu_seqlens || NT == 0) && N > (1 << 30))
+    return fail(KDA_ERR_INVALID_ARG, "%s: %d sequences", fn, N);
   if (!weight || (NT > 0 && (!x || !y)))
     return fail(KDA_ERR_INVALID_ARG, "%s: null required pointer", fn);
   const void* ptrs[] = {weight, bias, state, final_state};

@@ -510,9 +510,10 @@ enum { KDA_CONV_SILU = 1u };
  *   final_state  like state, written (NULL to skip): the last W-1 inputs, those of `state` among
  *            them where a sequence is shorter; it may be `state`.  It continues as the state of
  *            the calls below.
- *   cu_seqlens, n_seqs, B, T  as kda_chunk_fwd.  Offsets that do not run from 0 to NT without
- *            decreasing are reported by kda_get_device_error; y and final_state are then
- *            unspecified, nothing outside them is written.
+ *   cu_seqlens, n_seqs, B, T  as kda_chunk_fwd, n_seqs (and B where T is 0) at most 2^30.  Offsets
+ *            that do not run from 0 to NT without decreasing are reported by
+ *            kda_get_device_error; y and final_state are then unspecified, nothing outside them
+ *            is written.
  *   flags    KDA_CONV_SILU: act is x Sigmoid(x), else the identity.
  * Sums are fp32, rounded once to `dtype`.  No workspace.
  */
