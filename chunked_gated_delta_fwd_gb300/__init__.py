@@ -722,6 +722,13 @@ def _row_stride(t: torch.Tensor, name: str, tail: tuple, dtype, device) -> int:
     return row if step is None else step
 
 
+def _count(n, name):
+    """``n``, which goes over as a 32-bit integer (ctypes would cut it off)."""
+    if n > 0x7fffffff:
+        raise ValueError(f"{name}: {n} is more than 2^31 - 1")
+    return n
+
+
 def _tokens(x, name):
     """(shape, dtype, device, dtype code) of a call's first tensor, tokens of channels."""
     if not isinstance(x, torch.Tensor):
@@ -731,6 +738,7 @@ def _tokens(x, name):
     shape, dtype = x.shape, x.dtype
     if len(shape) < 2:
         raise ValueError(f"{name} must be [..., channels], got {tuple(shape)}")
+    _count(max(shape), name)
     return shape, dtype, x.device, _dtype_code(x)
 
 
@@ -740,7 +748,7 @@ def _packed(lead, cu_seqlens, dev, name):
         _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
         if len(lead) not in (1, 2) or (len(lead) == 2 and lead[0] != 1):
             raise ValueError(f"with cu_seqlens, {name} must be packed as [1, NT, C] or [NT, C]")
-        return cu_seqlens.numel() - 1, 1, lead[-1]
+        return _count(cu_seqlens.numel() - 1, "cu_seqlens"), 1, lead[-1]
     if len(lead) != 2:
         raise ValueError(f"{name} must be [B, T, C] without cu_seqlens")
     return lead[0], lead[0], lead[1]
@@ -759,7 +767,7 @@ def _conv_inputs(x, weight, bias):
         _need(bias, "bias", torch.float32, dev)
         if bias.shape != (C,):
             raise ValueError(f"bias must be [{C}], got {tuple(bias.shape)}")
-    return sx, shape, dtype, dev, C, ws[1], code
+    return sx, shape, dtype, dev, C, _count(ws[1], "weight"), code
 
 
 def _rows_out(out, x, C):
@@ -847,7 +855,7 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias):
     As = A.shape
     if len(As) != 2 or As[0] != n:
         raise ValueError(f"A must be [{n}, states], got {tuple(As)}")
-    S = As[1]
+    S = _count(As[1], "A")
     G = B.shape[-2] if isinstance(B, torch.Tensor) and B.dim() > 2 else 1
     row, bc = (n,), (G, S)
     sx = _row_stride(x, "x", row, dtype, dev)
@@ -958,6 +966,7 @@ def verify_draft(draft_tokens, draft_probs, target_probs, accept_uniforms, sampl
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError(f"target_probs must be [N, T+1, V], got {tuple(target_probs.shape)}")
     N, T, V = target_probs.shape
+    _count(max(N, T, V), "target_probs")
     T -= 1
     dt = _dtype_code(target_probs)
     _like(draft_tokens, "draft_tokens", (N, T), torch.int32, dev, given=True)
