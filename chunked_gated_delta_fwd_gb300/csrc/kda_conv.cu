@@ -9,7 +9,8 @@
 // are worked on, and the eight behind them on theirs to L2 (79 -> 70 us in the first case below);
 // products are packed pairs.  Sums are fp32, rounded once.  8192 tokens x 12288
 // channels, W = 4 with SiLU: bf16 65 us (6.2 TB/s), fp32 123 us (6.5 TB/s); 512 single tokens of as many
-// channels 21 us (4.8 TB/s), one 4.4 us.
+// channels bf16 20 to 21 us (5 TB/s), fp32 33 us (6.1 TB/s): some 6 us a call that do not grow with it,
+// the first loads and the last stores; one token 4.4 us cold, 1.5 us behind another call.
 #include <algorithm>
 #include <type_traits>
 

@@ -599,9 +599,13 @@ int sm_count() {
 }
 
 // Whether three rings of 4 warps an SM are expected to end before one of 12.  A ring of 12 takes
-// 117 ns a tile, one of 4 takes 200 alone, 265 beside another and 330 beside two (S = 16; the ratios
-// are about the same for 8 and 32), and a CTA some 3 us to begin and end, which others cover where
-// there are any.  (512 units of 1024 tiles: 460 against 530 us; 4096 of 64: 279 against 220.)
+// 117 ns a tile, one of 4 takes 200 alone, 265 beside another and 330 beside two, and a CTA some 3 us
+// to begin and end, which others cover where there are any.  (512 units of 1024 tiles: 457 us by
+// rings of 12, 522 by rings of 4; 2048 of 64: 136 and 116; 4096 of 64: 279 and 220.)  These hold for 16
+// states and up to some 128 tiles.  At 1024 tiles one of 4 takes 216, 263 and 377: with 400 units the
+// rule is 12% off (385 us by rings of 4, 345 by rings of 12), with 2048 3%.  There, with 8, 16 and 32
+// states, a ring of 12 takes 135, 117 and 139 (fp32 150, 117 and 169), and rings of 4 take 1.8, 1.9 and
+// 1.3 times as long alone, 2.3, 2.2 and 2.1 beside another and 3.2, 3.2 and 3.0 beside two.
 bool short_rings(int64_t units, int64_t tiles, int sms, double rounds_of_12) {
   const double t = (double)tiles, one = t * 0.117 + 3;
   const int64_t rounds = units / (3 * sms), rest = units - rounds * 3 * sms;
@@ -619,9 +623,12 @@ cudaError_t launch_scan(const ScanArgs& a, int bf16, int S, int* err, cudaStream
   const int64_t tiles = (a.NT / a.N + kTok - 1) / kTok;  // of a sequence, on average
   const int sms = sm_count();
   // Few units of long sequences: a cluster each, its CTAs a segment each.  The pass that finds
-  // what a segment does to a state costs half a scan, so two segments gain little (8192 tokens x
-  // 1024 channels 122 -> 110 us; 1024 tokens lose), four halve the time (x 512 channels 121 -> 62 us,
-  // 2048 tokens 38 -> 26).
+  // what a segment does to a state takes about as long as its scan, so two segments gain next to
+  // nothing (8192 tokens x 1024 channels 122 -> 110 us on one GPU, 119 -> 120 on another; 1024 tokens
+  // lose), four halve the time (x 512 channels 119 to 121 -> 62 to 66 us,
+  // 2048 tokens 38 -> 26), eight take a third (x 128 channels 119 -> 39 us).  A cluster lies within one
+  // GPC, so fewer of them run at once than SMs / CTAs: 16 units and more by eights and 37 and more by
+  // fours take two turns (16 to 19 units of 8192 tokens 70 us, by fours 65; 37 and 38 123 us, uncut 119).
   int cut = 1;
   while (cut < 8 && units * cut * 2 <= sms && tiles >= 128 * cut) cut *= 2;
   if (cut == 2 && tiles < 512) cut = 1;

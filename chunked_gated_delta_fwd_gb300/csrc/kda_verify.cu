@@ -15,9 +15,9 @@
 //
 // Bound by HBM for large batches (one row of p, one of q where a token was rejected) and by its
 // chain of loads for small ones: drafted token -> its probabilities -> rows -> search.  128 rows of
-// 163840: fp32 31 to 35 us (4.3 to 4.8 TB/s of the rows it needs), bf16 21 us; of 163841, whose rows
-// begin anywhere, token by token: 35 and 32 us (42 and 40 with 4 loads in flight); one row of 32000:
-// 6 us, of 163840: 8.
+// 163840: fp32 31 to 35 us (4.3 to 4.8 TB/s of the rows it needs), bf16 21 to 24 us; of 163841, whose
+// rows begin anywhere, token by token: 35 to 38 and 32 to 34 us (42 and 40 with 4 loads in flight); one
+// row of 32000: 6 to 7 us, of 163840: 8 to 10.
 #include <cooperative_groups.h>
 
 #include "kda_internal.cuh"
